@@ -9,6 +9,7 @@ present the calls raise.
 Functions mirror the C entry points:
   workspace_bytes(problem)            -> moe_fp4_workspace_bytes
   workspace_offsets(problem)          -> moe_fp4_workspace_offsets
+  gate(x, gate_w, top_k, ...)         -> moe_fp4_gate (the router)
   route(problem, topk_ids, ...)       -> moe_fp4_route
   forward(x, topk_ids, topk_w, ...)   -> moe_fp4_forward (fused=True: moe_fp4_forward_fused)
   forward_static(x, topk_ids, ...)    -> moe_fp4_forward_static (no workspace)
@@ -24,7 +25,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-__all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "route", "forward",
+__all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
            "forward_problem", "forward_static",
            "requant_gran_k", "prepare_gemm_weights", "prepare_gemm_weights_g16", "quantize_act", "quantize_act_fp4",
            "dropped_assignments", "LIB_PATH"]
@@ -37,12 +38,19 @@ GATE_UP, UP_GATE = 0, 1
 
 
 OUT_BF16, OUT_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GATE_W_BF16, GATE_W_F32 = 0, 1
 W_RAW, W_GEMM = 0, 1
 
 
 class Problem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("T", "E", "top_k", "H", "I", "gran_k", "act_fmt", "w13_order", "out_fmt", "w_layout")]
+
+
+class Gate(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("top_k", "shared", "scoring", "renormalize", "w_fmt")] + \
+        [("scale", ctypes.c_float)]
 
 
 class MoeFp4Error(RuntimeError):
@@ -70,6 +78,12 @@ def lib():
         L.moe_fp4_workspace_offsets.restype = st
         L.moe_fp4_route.argtypes = [ctypes.POINTER(Problem), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_route.restype = st
+        i64 = ctypes.c_int64
+        L.moe_fp4_gate_workspace_bytes.argtypes = [ctypes.POINTER(Gate), i64, i64, i64,
+                                                   ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fp4_gate_workspace_bytes.restype = st
+        L.moe_fp4_gate.argtypes = [ctypes.POINTER(Gate), i64, i64, i64, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.moe_fp4_gate.restype = st
         L.moe_fp4_forward.argtypes = [ctypes.POINTER(Problem), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_forward.restype = st
@@ -132,6 +146,45 @@ def _dev(t, name, dtypes):
     return t
 
 
+def _arg(t, name, dtypes, shape, device):
+    """A tensor argument of gate / layer / project: _dev's checks, its shape, and its device, which must be the
+    first argument's and the current one (the library launches on the current device)."""
+    if t is None:
+        return None
+    _dev(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _current(t):
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for work on ``stream`` (allocated on it, so that the allocator does not hand it to another one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace, need, device, stream):
+    import torch
+    if workspace is None:
+        return _empty(max(need, 256), torch.uint8, device, stream)
+    _dev(workspace, "workspace", (torch.uint8,))
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    return workspace
+
+
 def _order(w13_order):
     if isinstance(w13_order, str):
         return {"gate_up": GATE_UP, "w31": GATE_UP, "up_gate": UP_GATE, "w13": UP_GATE}[w13_order]
@@ -167,6 +220,55 @@ def _workspace(problem, workspace, device):
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
     return workspace
+
+
+def make_gate(top_k, scoring="softmax", renormalize=False, scale=1.0, shared=0, w_fmt=GATE_W_BF16) -> Gate:
+    if isinstance(scoring, str):
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+        scoring = SCORE_SIGMOID if scoring == "sigmoid" else SCORE_SOFTMAX
+    return Gate(top_k, shared, scoring, 1 if renormalize else 0, w_fmt, scale)
+
+
+def _router_args(x, gate_w, bias):
+    """(T, E, H, w_fmt, device) of a router's tensors, checked."""
+    import torch
+    _dev(x, "x", (torch.bfloat16,))
+    _dev(gate_w, "gate_w", (torch.bfloat16, torch.float32))
+    if x.dim() != 2 or gate_w.dim() != 2:
+        raise ValueError("x must be [T, H] and gate_w [E, H]")
+    dev = _current(x)
+    (T, H), E = x.shape, gate_w.shape[0]
+    _arg(gate_w, "gate_w", (torch.bfloat16, torch.float32), (E, H), dev)
+    _arg(bias, "bias", (torch.float32,), (E,), dev)
+    return T, E, H, GATE_W_F32 if gate_w.dtype == torch.float32 else GATE_W_BF16, dev
+
+
+def gate(x, gate_w, top_k, bias=None, scoring="softmax", renormalize=False, scale=1.0, shared=0, topk_ids=None,
+         topk_w=None, workspace=None, stream=None):
+    """The router: (topk_ids [T, top_k + shared] int32, topk_w float32) for
+    forward().  x [T, H] bfloat16; gate_w [E, H] bfloat16 or float32; bias [E]
+    float32 or None, added to the scores for the selection only (-inf masks an
+    expert); scoring "softmax" or "sigmoid"; renormalize divides the selected
+    scores by their sum; scale multiplies the weights; shared appends experts
+    E, E + 1, ... with weight 1.  Places without an expert (everything masked,
+    or logits that are not finite) hold id -1 and weight 0."""
+    import torch
+    T, E, H, w_fmt, dev = _router_args(x, gate_w, bias)
+    g = make_gate(top_k, scoring, renormalize, scale, shared, w_fmt)
+    need = ctypes.c_size_t(0)
+    _check(lib().moe_fp4_gate_workspace_bytes(ctypes.byref(g), T, E, H, ctypes.byref(need)))
+    shape = (T, top_k + shared)
+    if topk_ids is None:
+        topk_ids = _empty(shape, torch.int32, dev, stream)
+    if topk_w is None:
+        topk_w = _empty(shape, torch.float32, dev, stream)
+    _arg(topk_ids, "topk_ids", (torch.int32,), shape, dev)
+    _arg(topk_w, "topk_w", (torch.float32,), shape, dev)
+    ws = _scratch(workspace, need.value, dev, stream)
+    _check(lib().moe_fp4_gate(ctypes.byref(g), T, E, H, _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(topk_ids),
+                              _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+    return topk_ids, topk_w
 
 
 def route(problem: Problem, topk_ids, workspace=None, stream=None):

@@ -379,6 +379,34 @@ moefp4_status forward_impl(const moefp4_problem* p, const Layout& L, const void*
   return ok();
 }
 
+// The router's argument checks and plan.
+moefp4_status gate_check(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, moefp4::GatePlan* plan) {
+  if (!g) return fail(MOEFP4_EINVAL, "gate is NULL");
+  if (T < 0 || E < 1 || H < 8 || H % 8)
+    return fail(MOEFP4_EINVAL, "need T >= 0, E >= 1 and H a positive multiple of 8, got T=%lld E=%lld H=%lld",
+                (long long)T, (long long)E, (long long)H);
+  if (g->top_k < 1 || g->top_k > E || g->shared < 0)
+    return fail(MOEFP4_EINVAL, "need 1 <= top_k <= E=%lld and shared >= 0, got top_k=%d shared=%d", (long long)E,
+                g->top_k, g->shared);
+  if (g->scoring != MOEFP4_SCORE_SOFTMAX && g->scoring != MOEFP4_SCORE_SIGMOID)
+    return fail(MOEFP4_EINVAL, "unknown scoring %d", g->scoring);
+  if (g->w_fmt != MOEFP4_GATE_W_BF16 && g->w_fmt != MOEFP4_GATE_W_F32)
+    return fail(MOEFP4_EINVAL, "unknown gate weight format %d", g->w_fmt);
+  if (E > moefp4::kMaxExperts || g->shared > moefp4::kMaxExperts - E)
+    return fail(MOEFP4_EUNSUPPORTED, "E + shared must be at most %d, got %lld + %d", moefp4::kMaxExperts, (long long)E,
+                g->shared);
+  if (g->top_k > moefp4::kGateMaxTopK)
+    return fail(MOEFP4_EUNSUPPORTED, "top_k must be at most %d, got %d", moefp4::kGateMaxTopK, g->top_k);
+  if (T > (1 << 24) || H > (1 << 24) || T * H >= (1ll << 40))
+    return fail(MOEFP4_EUNSUPPORTED, "T and H must be at most 2^24 and T*H below 2^40");
+  *plan = moefp4::gate_plan((int)T, (int)E, (int)H, g->w_fmt == MOEFP4_GATE_W_F32);
+  return MOEFP4_OK;
+}
+
+moefp4::GateSel gate_sel(const moefp4_gate* g, int E, const float* bias) {
+  return moefp4::GateSel{E, g->top_k, g->shared, g->scoring, g->renormalize != 0, g->scale, bias};
+}
+
 }  // namespace
 
 extern "C" {
@@ -417,6 +445,38 @@ moefp4_status moe_fp4_route(const moefp4_problem* p, const int32_t* topk_ids, in
                 workspace ? ws_bytes : (size_t)0);
   st = route_into(p, L, topk_ids, counts, offsets, sorted_assign, slot_of, workspace, nullptr, 0,
                   nullptr, nullptr, nullptr, nullptr, nullptr, stream);
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+moefp4_status moe_fp4_gate_workspace_bytes(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, size_t* bytes) {
+  if (!bytes) return fail(MOEFP4_EINVAL, "bytes is NULL");
+  moefp4::GatePlan P;
+  moefp4_status st = gate_check(g, T, E, H, &P);
+  if (st != MOEFP4_OK) return st;
+  *bytes = align_up(P.part_bytes) + align_up(P.planes_bytes);
+  return ok();
+}
+
+moefp4_status moe_fp4_gate(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, const void* x, const void* w,
+                           const float* bias, int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes,
+                           hipStream_t stream) {
+  moefp4::GatePlan P;
+  moefp4_status st = gate_check(g, T, E, H, &P);
+  if (st != MOEFP4_OK) return st;
+  if (T == 0) return ok();
+  if (!x || !w || !topk_ids || !topk_w)
+    return fail(MOEFP4_EINVAL, "x, w, topk_ids and topk_w must be non-NULL");
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(bias, 4) || misaligned(topk_ids, 4) || misaligned(topk_w, 4))
+    return fail(MOEFP4_EINVAL, "x and w must be 16-byte aligned, bias, topk_ids and topk_w 4-byte");
+  const size_t need = align_up(P.part_bytes) + align_up(P.planes_bytes);
+  if (!workspace || ws_bytes < need)
+    return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  st = hip_status(moefp4::launch_gate(P, gate_sel(g, (int)E, bias), w, g->w_fmt == MOEFP4_GATE_W_F32,
+                                      static_cast<const uint16_t*>(x), (int)T, (int)H,
+                                      at<uint16_t>(workspace, align_up(P.part_bytes)), at<float>(workspace, 0),
+                                      topk_ids, topk_w, stream),
+                  "gate");
   return st == MOEFP4_OK ? ok() : st;
 }
 

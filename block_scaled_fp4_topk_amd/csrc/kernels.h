@@ -6,9 +6,33 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/moefp4.h"
+
 namespace moefp4 {
 
 constexpr int kMaxExperts = 512;
+
+// The router's selection (moefp4_gate): E routed experts, bias [E] or null.
+struct GateSel {
+  int E, top_k, shared, scoring, renorm;
+  float scale;
+  const float* bias;
+};
+constexpr int kGateMaxTopK = 64;   // one lane per selected expert
+constexpr int kGateDotTokens = 8;  // tokens per workgroup of the dot form
+constexpr int kGateDotMax = 16;    // most tokens it is used for
+
+// Logits of T tokens: one dot product per expert and token (dot), or a tiled
+// product with K split in `parts` of `per` stages.  part_bytes: the logits
+// [parts][T][E] float32; planes_bytes: FP32 weights as bfloat16 planes.
+struct GatePlan {
+  bool dot;
+  int per, parts;
+  size_t planes_bytes, part_bytes;
+};
+GatePlan gate_plan(int T, int E, int H, bool w_f32);
+hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool w_f32, const uint16_t* x, int T, int H,
+                       uint16_t* planes, float* part, int32_t* ids, float* wts, hipStream_t s);
 
 // Tile of activation rows processed by one grouped-GEMM workgroup.
 struct RouteOut {

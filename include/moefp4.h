@@ -144,6 +144,41 @@ moefp4_status moe_fp4_route(const moefp4_problem* p, const int32_t* topk_ids,
                             int32_t* sorted_assign, int32_t* slot_of,
                             void* workspace, size_t ws_bytes, hipStream_t stream);
 
+/* The router: which experts each token takes, and with what weight.
+ * logits = x W^T (FP32 accumulation); score = softmax over the token's experts
+ * or the sigmoid of each logit; the top_k experts by score + bias (by score
+ * without one), equal ones by the lower index, in descending order; weight =
+ * the score (without the bias), divided by the sum of the selected scores if
+ * renormalize, times scale.  Then `shared` experts that every token takes
+ * (ids E, E + 1, ... with weight 1: a layer's shared experts, kept as the
+ * last experts of its weight tensors).  The results are the topk_ids /
+ * topk_w of a moe_fp4_forward with E + shared experts and top_k + shared
+ * experts per token.
+ * An expert whose logit is not finite, or whose score + bias is NaN or -inf
+ * (a bias of -inf masks an expert), is never selected, and a logit that is
+ * not finite takes no part in the softmax; places for which no expert is
+ * left get id -1 (which route and forward drop and count) and weight 0.
+ * With a bias the scores are formed and compared in 64 bits. */
+typedef enum moefp4_score { MOEFP4_SCORE_SOFTMAX = 0, MOEFP4_SCORE_SIGMOID = 1 } moefp4_score;
+typedef enum moefp4_gate_fmt { MOEFP4_GATE_W_BF16 = 0, MOEFP4_GATE_W_F32 = 1 } moefp4_gate_fmt;
+typedef struct moefp4_gate {
+  int32_t top_k, shared, scoring, renormalize, w_fmt;
+  float scale;
+} moefp4_gate;
+
+/* Workspace of moe_fp4_gate for T tokens, E routed experts and hidden size H. */
+moefp4_status moe_fp4_gate_workspace_bytes(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, size_t* bytes);
+
+/* x [T, H] bfloat16, w [E, H] bfloat16 or float32 (g->w_fmt), bias [E] float32
+ * or NULL, topk_ids [T, top_k + shared] int32, topk_w [T, top_k + shared]
+ * float32, all device memory, x and w 16-byte aligned, the workspace 256-byte
+ * aligned.  H a multiple of 8, 1 <= top_k <= E, shared >= 0 (EINVAL
+ * otherwise); E + shared <= 512, top_k <= 64, T <= 2^24, T*E and T*H below
+ * 2^40 and H <= 2^24 (EUNSUPPORTED otherwise).  Enqueued on `stream`. */
+moefp4_status moe_fp4_gate(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, const void* x, const void* w,
+                           const float* bias, int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes,
+                           hipStream_t stream);
+
 /* MoE forward: out[t] = sum_j topk_w[t, j] * FC2_e(SwiGLU(FC1_e(x[t]))),
  * e = topk_ids[t, j]; FC1 uses w13 [E, 2I, H/2] + w13_sf [E, 2I, H/gran]
  * (+ w13_gs [E]), FC2 uses w2 [E, H, I/2] + w2_sf [E, H, I/gran] (+ w2_gs),
