@@ -12,6 +12,7 @@ Functions mirror the C entry points:
   gate(x, gate_w, top_k, ...)         -> moe_fp4_gate (the router)
   route(problem, topk_ids, ...)       -> moe_fp4_route
   forward(x, topk_ids, topk_w, ...)   -> moe_fp4_forward (fused=True: moe_fp4_forward_fused)
+  layer(x, gate_w, top_k, w13, ...)   -> moe_fp4_layer (router and forward)
   forward_static(x, topk_ids, ...)    -> moe_fp4_forward_static (no workspace)
   requant_gran_k(src, src_sf, ...)    -> fp4_requant_gran_k
   prepare_gemm_weights(src, src_sf, ...) -> moe_fp4_prepare_gemm_weights
@@ -26,7 +27,7 @@ import ctypes
 import os
 
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
-           "forward_problem", "forward_static",
+           "forward_problem", "forward_static", "layer",
            "requant_gran_k", "prepare_gemm_weights", "prepare_gemm_weights_g16", "quantize_act", "quantize_act_fp4",
            "dropped_assignments", "LIB_PATH"]
 
@@ -84,6 +85,11 @@ def lib():
         L.moe_fp4_gate_workspace_bytes.restype = st
         L.moe_fp4_gate.argtypes = [ctypes.POINTER(Gate), i64, i64, i64, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_gate.restype = st
+        gp = ctypes.POINTER(Gate)
+        L.moe_fp4_layer_workspace_bytes.argtypes = [ctypes.POINTER(Problem), gp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fp4_layer_workspace_bytes.restype = st
+        L.moe_fp4_layer.argtypes = [ctypes.POINTER(Problem), gp] + [_P] * 13 + [ctypes.c_size_t, _P]
+        L.moe_fp4_layer.restype = st
         L.moe_fp4_forward.argtypes = [ctypes.POINTER(Problem), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_forward.restype = st
@@ -380,6 +386,58 @@ def forward_static(x, topk_ids, topk_w, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, g
     _check(lib().moe_fp4_forward_static(ctypes.byref(p), _ptr(x), _ptr(x_sf), _ptr(topk_ids), _ptr(topk_w),
                                         _ptr(w13), _ptr(w13_sf), _ptr(w13_gs), _ptr(w2), _ptr(w2_sf),
                                         _ptr(w2_gs), _ptr(out), _stream(stream)))
+    return out
+
+
+def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=None, scoring="softmax",
+          renormalize=False, scale=1.0, shared=0, w13_order="gate_up", out=None, workspace=None, stream=None,
+          out_dtype=None, quantize_x=False, w_layout="raw", topk_ids=None, topk_w=None):
+    """A whole mixture-of-experts layer on bfloat16 x [T, H]: gate() with
+    gate_w [E - shared, H], then forward() over the E experts of the weight
+    tensors, the last `shared` of which every token takes with weight 1.  Up
+    to 16 tokens run in two launches (moe_fp4_layer).  quantize_x, w_layout,
+    w13_order and out_dtype as for forward(); topk_ids / topk_w
+    [T, top_k + shared]: optional outputs for the selection.  Returns out
+    [T, H]."""
+    import torch
+    T, routed, H, w_fmt, dev = _router_args(x, gate_w, bias)
+    quant = {False: ACT_BF16, None: ACT_BF16, True: ACT_BF16_QUANT_FP8_K32, "fp8": ACT_BF16_QUANT_FP8_K32,
+             "fp4": ACT_BF16_QUANT_FP4_K32}.get(quantize_x)
+    if quant is None:
+        raise ValueError(f"quantize_x must be False, True, 'fp8' or 'fp4', got {quantize_x!r}")
+    if gran_k not in (16, 32):
+        raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
+    u8, f32 = (torch.uint8,), (torch.float32,)
+    E = routed + shared
+    _dev(w13, "w13", u8)
+    if w13.dim() != 3:
+        raise ValueError("w13 must be [E, 2I, H/2]")
+    I = w13.shape[1] // 2
+    _arg(w13, "w13", u8, (E, 2 * I, H // 2), dev)
+    _arg(w13_sf, "w13_sf", u8, (E, 2 * I, H // gran_k), dev)
+    _arg(w2, "w2", u8, (E, H, I // 2), dev)
+    _arg(w2_sf, "w2_sf", u8, (E, H, I // gran_k), dev)
+    _arg(w13_gs, "w13_gs", f32, (E,), dev)
+    _arg(w2_gs, "w2_gs", f32, (E,), dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    g = make_gate(top_k, scoring, renormalize, scale, shared, w_fmt)
+    p = make_problem(T, E, top_k + shared, H, I, gran_k, quant, w13_order,
+                     OUT_F32 if out_dtype == torch.float32 else OUT_BF16, w_layout)
+    need = ctypes.c_size_t(0)
+    _check(lib().moe_fp4_layer_workspace_bytes(ctypes.byref(p), ctypes.byref(g), ctypes.byref(need)))
+    if out is None:
+        out = _empty((T, H), out_dtype, dev, stream)
+    else:
+        _arg(out, "out", (out_dtype,), (T, H), dev)
+    _arg(topk_ids, "topk_ids", (torch.int32,), (T, top_k + shared), dev)
+    _arg(topk_w, "topk_w", f32, (T, top_k + shared), dev)
+    ws = _scratch(workspace, need.value, dev, stream)
+    _check(lib().moe_fp4_layer(ctypes.byref(p), ctypes.byref(g), _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(w13),
+                               _ptr(w13_sf), _ptr(w13_gs), _ptr(w2), _ptr(w2_sf), _ptr(w2_gs), _ptr(out),
+                               _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 

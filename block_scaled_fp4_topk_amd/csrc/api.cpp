@@ -407,6 +407,56 @@ moefp4::GateSel gate_sel(const moefp4_gate* g, int E, const float* bias) {
   return moefp4::GateSel{E, g->top_k, g->shared, g->scoring, g->renormalize != 0, g->scale, bias};
 }
 
+// A layer's checks and the places of its two forms in the workspace.
+struct LayerPlan {
+  Layout L;                 // the forward's (at 0)
+  moefp4::GatePlan gate;
+  bool few;
+  size_t part, planes, ids, wts;                        // gate + forward
+  size_t flags, logits, xs, x16, h, hexp, sync, parts;  // few tokens
+  int ld, nwg;
+  size_t total;
+};
+
+moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPlan* P) {
+  moefp4_status st = plan(p, &P->L);
+  if (st != MOEFP4_OK) return st;
+  if (!g) return fail(MOEFP4_EINVAL, "gate is NULL");
+  if (p->act_fmt != MOEFP4_ACT_BF16 && !P->L.quant_x)
+    return fail(MOEFP4_EINVAL, "the router takes bfloat16 x: act_fmt must be BF16 or one of the BF16_QUANT formats");
+  if (g->shared < 0 || g->shared >= p->E || g->top_k != p->top_k - g->shared)
+    return fail(MOEFP4_EINVAL, "need 0 <= shared < E and top_k (with the shared experts) = %d + %d, got E=%d top_k=%d",
+                g->top_k, g->shared, p->E, p->top_k);
+  st = gate_check(g, p->T, p->E - g->shared, p->H, &P->gate);
+  if (st != MOEFP4_OK) return st;
+  const size_t T = p->T, H = p->H, I = p->I, A = T * p->top_k;
+  // (both forms at 16 tokens: see the launcher's comment)
+  P->few = p->T >= 1 && p->T <= moefp4::kFewTokens && p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH &&
+           p->top_k <= moefp4::kFewMaxK;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
+  if (P->few) {
+    P->ld = p->E - g->shared <= 256 ? 256 : 512;
+    P->nwg = moefp4::cu_count();
+    P->flags = take(64);
+    P->logits = take(T * P->ld * 4);
+    P->xs = take(P->L.g16_a16 ? T * 4 : 0);
+    P->x16 = take(P->L.g16_a16 ? T * H * 2 : 0);
+    P->h = take(P->L.g16_a16 ? A * I * 2 : A * I * 4);
+    P->hexp = take(P->L.g16_a16 ? A * (I / 16) : 0);
+    P->sync = take((size_t)moefp4::few_sync_words(p->H) * 4);
+    P->parts = take((size_t)P->nwg * 2 * 512 * 4);
+  } else {
+    o = P->L.total;
+    P->ids = take(A * 4);
+    P->wts = take(A * 4);
+    P->part = take(P->gate.part_bytes);
+    P->planes = take(P->gate.planes_bytes);
+  }
+  P->total = o;
+  return MOEFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -507,6 +557,83 @@ moefp4_status moe_fp4_forward_fused(const moefp4_problem* p, const void* x, cons
                 L.nt == 8 ? "128-row GEMM" : "64-row");
   return forward_impl(p, L, x, x_sf, topk_ids, topk_w, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, out, workspace,
                       ws_bytes, true, stream);
+}
+
+moefp4_status moe_fp4_layer_workspace_bytes(const moefp4_problem* p, const moefp4_gate* g, size_t* bytes) {
+  if (!bytes) return fail(MOEFP4_EINVAL, "bytes is NULL");
+  LayerPlan P;
+  moefp4_status st = layer_plan(p, g, &P);
+  if (st != MOEFP4_OK) return st;
+  *bytes = P.total;
+  return ok();
+}
+
+moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const void* x, const void* gate_w,
+                            const float* bias, const uint8_t* w13, const uint8_t* w13_sf, const float* w13_gs,
+                            const uint8_t* w2, const uint8_t* w2_sf, const float* w2_gs, void* out,
+                            int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  LayerPlan P;
+  moefp4_status st = layer_plan(p, g, &P);
+  if (st != MOEFP4_OK) return st;
+  if (p->T == 0) return ok();
+  if (!x || !gate_w || !w13 || !w13_sf || !w2 || !w2_sf || !out)
+    return fail(MOEFP4_EINVAL, "x, gate_w, w13, w13_sf, w2, w2_sf and out must be non-NULL");
+  if (misaligned(x, 16) || misaligned(gate_w, 16) || misaligned(w13, 16) || misaligned(w2, 16) || misaligned(out, 16) ||
+      misaligned(w13_sf, 16) || misaligned(w2_sf, 16))
+    return fail(MOEFP4_EINVAL, "x, gate_w, w13, w13_sf, w2, w2_sf and out must be 16-byte aligned");
+  if (misaligned(bias, 4) || misaligned(w13_gs, 4) || misaligned(w2_gs, 4) || misaligned(topk_ids, 4) ||
+      misaligned(topk_w, 4))
+    return fail(MOEFP4_EINVAL, "bias, w13_gs, w2_gs, topk_ids and topk_w must be 4-byte aligned");
+  if (!workspace || ws_bytes < P.total)
+    return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", P.total,
+                workspace ? ws_bytes : (size_t)0);
+  if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  const moefp4::GateSel sel = gate_sel(g, p->E - g->shared, bias);
+  const bool w_f32 = g->w_fmt == MOEFP4_GATE_W_F32;
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  if (!P.few) {
+    int32_t* ids = topk_ids ? topk_ids : at<int32_t>(workspace, P.ids);
+    float* wts = topk_w ? topk_w : at<float>(workspace, P.wts);
+    st = hip_status(moefp4::launch_gate(P.gate, sel, gate_w, w_f32, xb, p->T, p->H, at<uint16_t>(workspace, P.planes),
+                                        at<float>(workspace, P.part), ids, wts, stream),
+                    "gate");
+    if (st != MOEFP4_OK) return st;
+    return forward_impl(p, P.L, x, nullptr, ids, wts, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, out, workspace, ws_bytes,
+                        false, stream);
+  }
+  moefp4::FewArgs a;
+  memset(&a, 0, sizeof a);
+  a.g = sel;
+  a.T = p->T;
+  a.H = p->H;
+  a.I = p->I;
+  a.w13_order = p->w13_order;
+  a.g16 = P.L.g16_a16;
+  a.w_f32 = w_f32;
+  a.out_f32 = p->out_fmt == MOEFP4_OUT_F32;
+  a.x = xb;
+  a.gate_w = gate_w;
+  a.w13 = w13;
+  a.w13_sf = w13_sf;
+  a.w13_gs = w13_gs;
+  a.w2 = w2;
+  a.w2_sf = w2_sf;
+  a.w2_gs = w2_gs;
+  a.out = out;
+  a.ids = topk_ids;
+  a.wts = topk_w;
+  a.flags = at<int32_t>(workspace, P.flags);
+  a.logits = at<float>(workspace, P.logits);
+  a.ld = P.ld;
+  a.x16 = at<uint16_t>(workspace, P.x16);
+  a.xs = at<float>(workspace, P.xs);
+  a.h = at<uint16_t>(workspace, P.h);
+  a.hexp = at<int8_t>(workspace, P.hexp);
+  a.sync = at<int32_t>(workspace, P.sync);
+  a.part = at<float>(workspace, P.parts);
+  a.nwg = P.nwg;
+  st = hip_status(moefp4::launch_few(a, stream), "layer");
+  return st == MOEFP4_OK ? ok() : st;
 }
 
 moefp4_status moe_fp4_forward_static(const moefp4_problem* p, const void* x, const uint8_t* x_sf,

@@ -15,12 +15,12 @@ namespace moefp4 {
 
 namespace {
 
-template <bool WF32>
+template <bool WF32, int TB>
 __global__ __launch_bounds__(256) void gate_dot_kernel(const void* __restrict__ w, const uint16_t* __restrict__ x,
-                                                       int T, int E, int H, float* __restrict__ logits) {
-  __shared__ float s_red[4 * kGateDotTokens];
-  const int t0 = blockIdx.y * kGateDotTokens;
-  gate_dot_expert<WF32, kGateDotTokens>(w, x, blockIdx.x, t0, min(kGateDotTokens, T - t0), E, H, logits, s_red);
+                                                       int T, int ld, int H, float* __restrict__ logits) {
+  __shared__ float s_red[4 * TB];
+  const int t0 = blockIdx.y * TB;
+  gate_dot_expert<WF32, TB>(w, x, blockIdx.x, t0, min(TB, T - t0), ld, H, logits, s_red);
 }
 
 // FP32 [E, H] -> three bfloat16 planes [3][E][H] by truncation.
@@ -80,7 +80,8 @@ __device__ __forceinline__ void gate_stage(const uint16_t* __restrict__ src, int
 // logits.  4 waves of 64 experts x 64 tokens; WP planes of W.
 template <int WP>
 __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ x,
-                                                        int T, int E, int H, int per, float* __restrict__ part) {
+                                                        int T, int E, int ld, int H, int per,
+                                                        float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint8_t s[2][(WP + 1) * kTile * 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
     }
   }
   // lane: experts 4 q .. + 3 of each 16, token r16
-  float* out = part + (size_t)blockIdx.z * T * E;
+  float* out = part + (size_t)blockIdx.z * T * ld;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int t = t0 + wt + 16 * j + r16;
@@ -136,28 +137,29 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = e0 + we + 16 * i + 4 * q;
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (e + v < E) out[(size_t)t * E + e + v] = acc[i][j][v];
+      if (e < ld) *reinterpret_cast<v4f*>(out + (size_t)t * ld + e) = acc[i][j];
     }
   }
 }
 
-// One wavefront per token.
+// One wavefront per token.  The logits' rows are padded to 64 * NI experts
+// (what lies past E is not looked at).
 template <int NI, bool BIAS>
 __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restrict__ part, int nparts, int T,
                                                           GateSel g, int32_t* __restrict__ ids,
                                                           float* __restrict__ wts) {
   const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
+  using vec = typename std::conditional<NI == 1, float, float __attribute__((ext_vector_type(NI)))>::type;
+  vec sum = 0.0f;
+  const float* row = part + (size_t)t * (64 * NI) + lane * NI;
+#pragma unroll 8
+  for (int s = 0; s < nparts; ++s) sum += *reinterpret_cast<const vec*>(row + (size_t)s * T * (64 * NI));
   float l[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) l[i] = 0.0f;
-  for (int s = 0; s < nparts; ++s) {
-    const float* row = part + ((size_t)s * T + t) * g.E;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (lane * NI + i < g.E) l[i] += row[lane * NI + i];
+  for (int i = 0; i < NI; ++i) {
+    if constexpr (NI == 1) l[i] = sum;
+    else l[i] = sum[i];
   }
   const int kt = g.top_k + g.shared;
   gate_select<NI, BIAS>(l, g, lane, [&](int j, int id, float w) __attribute__((always_inline)) {
@@ -185,6 +187,7 @@ void gate_split_k(int T, int E, int H, int* per, int* parts) {
   const int nst = (H + kGK - 1) / kGK;
   const int tiles = ((T + kTile - 1) / kTile) * ((E + kTile - 1) / kTile);
   int n = (256 + tiles - 1) / tiles;
+  n = n > 16 ? 16 : n;
   n = n > nst / 2 ? nst / 2 : n;
   n = n < 1 ? 1 : n;
   *per = (nst + n - 1) / n;
@@ -200,8 +203,17 @@ GatePlan gate_plan(int T, int E, int H, bool w_f32) {
   p.parts = 1;
   if (!p.dot) gate_split_k(T, E, H, &p.per, &p.parts);
   p.planes_bytes = !p.dot && w_f32 ? (size_t)3 * E * H * 2 : 0;
-  p.part_bytes = (size_t)p.parts * T * E * 4;
+  p.ld = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512;
+  p.part_bytes = (size_t)p.parts * T * p.ld * 4;
   return p;
+}
+
+template <int TB>
+static void launch_dot(const void* w, bool w_f32, const uint16_t* x, int T, int E, int ld, int H, float* part,
+                       hipStream_t s) {
+  const dim3 grid(E, (T + TB - 1) / TB);
+  if (w_f32) hipLaunchKernelGGL((gate_dot_kernel<true, TB>), grid, dim3(256), 0, s, w, x, T, ld, H, part);
+  else hipLaunchKernelGGL((gate_dot_kernel<false, TB>), grid, dim3(256), 0, s, w, x, T, ld, H, part);
 }
 
 hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool w_f32, const uint16_t* x, int T, int H,
@@ -209,9 +221,9 @@ hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool 
   if (T <= 0) return hipSuccess;
   const int E = g.E;
   if (p.dot) {
-    const dim3 grid(E, (T + kGateDotTokens - 1) / kGateDotTokens);
-    if (w_f32) hipLaunchKernelGGL(gate_dot_kernel<true>, grid, dim3(256), 0, s, w, x, T, E, H, part);
-    else hipLaunchKernelGGL(gate_dot_kernel<false>, grid, dim3(256), 0, s, w, x, T, E, H, part);
+    if (T == 1) launch_dot<1>(w, w_f32, x, T, E, p.ld, H, part, s);
+    else if (T <= 4) launch_dot<4>(w, w_f32, x, T, E, p.ld, H, part, s);
+    else launch_dot<8>(w, w_f32, x, T, E, p.ld, H, part, s);
   } else {
     const dim3 grid((T + kTile - 1) / kTile, (E + kTile - 1) / kTile, p.parts);
     if (w_f32) {
@@ -220,15 +232,16 @@ hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool 
                          static_cast<const float*>(w), n, planes);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;
-      hipLaunchKernelGGL(gate_gemm_kernel<3>, grid, dim3(256), 0, s, planes, x, T, E, H, p.per, part);
+      hipLaunchKernelGGL(gate_gemm_kernel<3>, grid, dim3(256), 0, s, planes, x, T, E, p.ld, H, p.per, part);
     } else {
-      hipLaunchKernelGGL(gate_gemm_kernel<1>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(w), x, T, E, H,
-                         p.per, part);
+      hipLaunchKernelGGL(gate_gemm_kernel<1>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(w), x, T, E, p.ld,
+                         H, p.per, part);
     }
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (E <= 64) launch_select<1>(part, p.parts, T, g, ids, wts, s);
+  else if (E <= 128) launch_select<2>(part, p.parts, T, g, ids, wts, s);
   else if (E <= 256) launch_select<4>(part, p.parts, T, g, ids, wts, s);
   else launch_select<8>(part, p.parts, T, g, ids, wts, s);
   return hipGetLastError();

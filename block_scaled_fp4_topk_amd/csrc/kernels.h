@@ -19,15 +19,18 @@ struct GateSel {
   const float* bias;
 };
 constexpr int kGateMaxTopK = 64;   // one lane per selected expert
-constexpr int kGateDotTokens = 8;  // tokens per workgroup of the dot form
-constexpr int kGateDotMax = 16;    // most tokens it is used for
+// Most tokens the dot form is used for.  Both forms, with the selection, for
+// 256 experts: H = 6144 10.8 us against 12.1 us for 16 tokens, 13.3 against
+// 12.6 for 32, 17.3 against 13.2 for 64; H = 2048 9.3 against 9.4 for 16, 10.5
+// against 9.6 for 32.
+constexpr int kGateDotMax = 16;
 
 // Logits of T tokens: one dot product per expert and token (dot), or a tiled
 // product with K split in `parts` of `per` stages.  part_bytes: the logits
-// [parts][T][E] float32; planes_bytes: FP32 weights as bfloat16 planes.
+// [parts][T][ld] float32; planes_bytes: FP32 weights as bfloat16 planes.
 struct GatePlan {
   bool dot;
-  int per, parts;
+  int per, parts, ld;
   size_t planes_bytes, part_bytes;
 };
 GatePlan gate_plan(int T, int E, int H, bool w_f32);
@@ -89,6 +92,41 @@ hipError_t launch_quantize_act(const uint16_t* x, long long T, int H, uint8_t* x
 // maximum lands in [2**14, 2**15); scale[t] = 2**p_t.
 hipError_t launch_rows_to_f16(const uint16_t* x, int T, int H, uint16_t* x16, float* scale,
                               hipStream_t s);
+
+// The whole layer for a few tokens in two launches (layer.hip).  T <= 16,
+// H % 256 == 0, H <= 6144, I % 256 == 0, I * H < 2^31, at most 64 experts per
+// token (shared ones among them), E = routed + shared <= 512.
+constexpr int kFewTokens = 16;
+constexpr int kFewMaxH = 6144;
+constexpr int kFewMaxK = 64;
+struct FewArgs {
+  GateSel g;              // E: routed experts
+  int T, H, I, w13_order;
+  bool g16, w_f32, out_f32;
+  const uint16_t* x;      // [T, H] bf16
+  const void* gate_w;
+  const uint8_t *w13, *w13_sf, *w2, *w2_sf;
+  const float *w13_gs, *w2_gs;
+  void* out;
+  int32_t* ids;           // optional outputs [T, top_k + shared]
+  float* wts;
+  // workspace
+  int32_t* flags;         // [2] places without an expert, waits past their limit
+  float* logits;          // [T][ld]
+  int ld;
+  uint16_t* x16;          // group16: x as fp16 * 2**-p [T, H] ...
+  float* xs;              // ... and 2**p [T]
+  uint16_t* h;            // [T * k][I] fp16 in blocks of 16 with a shared exponent (group16), or bf16 high and low
+                          // parts [2][T * k][I] (group32); K order of a 256-element chunk as the lanes read it
+  int8_t* hexp;           // group16: [T * k][I / 16] exponents
+  int32_t* sync;          // [few_sync_words]
+  float* part;            // [workgroups][2][64 lanes][8] partial outputs
+  int nwg;
+};
+constexpr int few_sync_words(int H) { return 2 + H / 32; }
+hipError_t launch_few(const FewArgs& a, hipStream_t s);
+// CUs of the current device (the workgroups of the persistent kernels)
+int cu_count();
 
 struct FcArgs {
   const uint8_t* w;          // [E, N, K/2]

@@ -250,6 +250,27 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
                                      const uint8_t* w2, const uint8_t* w2_sf, const float* w2_gs,
                                      void* out, hipStream_t stream);
 
+/* A whole mixture-of-experts layer on bfloat16 x: moe_fp4_gate, then
+ * moe_fp4_forward with the ids and weights it gives (p->E counts the routed
+ * experts and the g->shared last ones, p->top_k = g->top_k + g->shared).
+ * Up to 16 tokens of BF16 activations (and H <= 6144, top_k <= 64) run in two
+ * launches: router logits, then one persistent kernel for selection, FC1, FC2
+ * and the weighted sum.  That form keeps h to at least 11 significant bits
+ * between FC1 and FC2 (moe_fp4_forward rounds it to bfloat16); all its waits
+ * are bounded, and if one ever exceeded its 50 ms, the workspace's second word
+ * is nonzero and the result is not valid.  Other sizes and formats run
+ * moe_fp4_gate and moe_fp4_forward one after the other.
+ * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
+ * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
+ * rows); topk_ids / topk_w [T, top_k] receive the selection, NULL if it is
+ * not wanted; the rest as for moe_fp4_forward.  The workspace's first word
+ * then holds the number of places without an expert. */
+moefp4_status moe_fp4_layer_workspace_bytes(const moefp4_problem* p, const moefp4_gate* g, size_t* bytes);
+moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const void* x, const void* gate_w,
+                            const float* bias, const uint8_t* w13, const uint8_t* w13_sf, const float* w13_gs,
+                            const uint8_t* w2, const uint8_t* w2_sf, const float* w2_gs, void* out,
+                            int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, hipStream_t stream);
+
 /* Reorder group32 weights (RAW layout, UE8M0 scales) into the GEMM layout
  * of the prefill kernels.  which = 0: w13 (N = 2I rows in w13_order, K =
  * H); which = 1: w2 (N = H, K = I).  The GEMM's weight rows are taken in
