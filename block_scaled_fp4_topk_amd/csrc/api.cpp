@@ -433,11 +433,14 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
   // (both forms at 16 tokens: see the launcher's comment)
   P->few = p->T >= 1 && p->T <= moefp4::kFewTokens && p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH &&
            p->top_k <= moefp4::kFewMaxK;
+  P->nwg = moefp4::cu_count();
+  // (launch 2 counts FC2's steps times workgroups in 31 bits)
+  if (P->few && (H / 32) * ((size_t)p->E * (I / 256) / 8 + 1) * P->nwg >= (1ull << 31)) P->few = false;
+  if (P->few && A * I * 4 >= (1ull << 31)) P->few = false;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
   if (P->few) {
     P->ld = p->E - g->shared <= 256 ? 256 : 512;
-    P->nwg = moefp4::cu_count();
     P->flags = take(64);
     P->logits = take(T * P->ld * 4);
     P->xs = take(P->L.g16_a16 ? T * 4 : 0);

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
 
 // One wavefront per token.  The logits' rows are padded to 64 * NI experts
 // (what lies past E is not looked at).
-template <int NI, bool BIAS>
+template <int NI>
 __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restrict__ part, int nparts, int T,
                                                           GateSel g, int32_t* __restrict__ ids,
                                                           float* __restrict__ wts) {
@@ -162,7 +162,12 @@ __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restric
     else l[i] = sum[i];
   }
   const int kt = g.top_k + g.shared;
-  gate_select<NI, BIAS>(l, g, lane, [&](int j, int id, float w) __attribute__((always_inline)) {
+  auto again = [&](int e) __attribute__((always_inline)) {
+    float v = 0.0f;
+    for (int s = 0; s < nparts; ++s) v += part[((size_t)s * T + t) * (64 * NI) + e];
+    return v;
+  };
+  gate_select<NI>(l, g, lane, again, [&](int j, int id, float w) __attribute__((always_inline)) {
     ids[(size_t)t * kt + j] = id;
     wts[(size_t)t * kt + j] = w;
   });
@@ -175,10 +180,7 @@ __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restric
 template <int NI>
 void launch_select(const float* part, int nparts, int T, const GateSel& g, int32_t* ids, float* wts, hipStream_t s) {
   const dim3 grid((T + 3) / 4);
-  if (g.bias)
-    hipLaunchKernelGGL((gate_select_kernel<NI, true>), grid, dim3(256), 0, s, part, nparts, T, g, ids, wts);
-  else
-    hipLaunchKernelGGL((gate_select_kernel<NI, false>), grid, dim3(256), 0, s, part, nparts, T, g, ids, wts);
+  hipLaunchKernelGGL(gate_select_kernel<NI>, grid, dim3(256), 0, s, part, nparts, T, g, ids, wts);
 }
 
 // K stages per workgroup and the number of parts: workgroups for every CU

@@ -79,43 +79,54 @@ __device__ __forceinline__ void take_top(S (&sel)[NI], int n, int lane, F&& take
 }
 
 // The 64-bit selection of gate_select's biased form: the expert and score of
-// place j to lane j.
-template <int NI>
-__device__ __forceinline__ void gate_select64(const float (&l)[NI], const GateSel& g, int lane, int* expert,
-                                                        float* score) {
+// place j to lane j.  It runs for few tokens and is written to be small (the
+// code of a launch comes from memory too): every round reads the logits again,
+// logit_of(e), and forms the scores anew.
+template <int NI, class L>
+__device__ __forceinline__ void gate_select64(const GateSel& g, int lane, L&& logit_of, int* expert, float* score) {
   const double kNone = -__builtin_inf();
-  double p[NI], sel[NI];
-  double m = kNone, sum = 0;
-  bool fin[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    fin[i] = lane * NI + i < g.E && __builtin_isfinite(l[i]);
-    if (fin[i]) m = max_of(m, (double)l[i]);
-  }
   const bool softmax = g.scoring == MOEFP4_SCORE_SOFTMAX;
-  if (softmax) m = wave_max(m);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    p[i] = !fin[i] ? 0.0 : softmax ? exp((double)l[i] - m) : 1.0 / (1.0 + exp(-(double)l[i]));
-    sum += p[i];
+  const int e0 = lane * NI, e1 = min(e0 + NI, g.E);
+  double m = 0, inv = 1, sum = 0;
+  if (softmax) {
+    m = kNone;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const float v = logit_of(e);
+      if (__builtin_isfinite(v)) m = max_of(m, (double)v);
+    }
+    m = wave_max(m);
   }
-  const double inv = softmax ? 1.0 / wave_sum(sum) : 1.0;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    p[i] *= inv;
-    const double s = p[i] + (double)(fin[i] ? g.bias[lane * NI + i] : 0.0f);
-    sel[i] = fin[i] && s > kNone ? s : kNone;  // (false for NaN)
-  }
+  uint32_t taken = 0;
   int my = -1;
   float mine = 0.0f;
-  take_top<NI>(sel, g.top_k, lane, [&](int j, int who, int wi, double) __attribute__((always_inline)) {
-    float ps = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (i == wi) ps = (float)p[i];
-    ps = __shfl(ps, who, 64);
-    if (lane == j) mine = ps, my = who * NI + wi;
-  });
+  // round -1 sums the softmax, round j takes place j
+#pragma unroll 1
+  for (int j = softmax ? -1 : 0; j < g.top_k; ++j) {
+    double best = kNone, bp = 0;
+    int be = 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const float v = logit_of(e);
+      if (!__builtin_isfinite(v)) continue;
+      const double x = exp(softmax ? (double)v - m : -(double)v);
+      const double p = softmax ? x * inv : 1.0 / (1.0 + x);
+      sum += p;
+      const double s = p + (double)g.bias[e];
+      if (!((taken >> (e - e0)) & 1) && s > best) best = s, bp = p, be = e;
+    }
+    if (j < 0) {
+      inv = 1.0 / wave_sum(sum);
+      continue;
+    }
+    const double top = wave_max(best);
+    if (!(top > kNone)) break;
+    const int who = __builtin_ctzll(ballot(best == top));
+    const float ps = __shfl((float)bp, who, 64);
+    const int we = __shfl(be, who, 64);
+    if (lane == who) taken |= 1u << (we - e0);
+    if (lane == j) mine = ps, my = we;
+  }
   *expert = my;
   *score = mine;
 }
@@ -123,7 +134,7 @@ __device__ __forceinline__ void gate_select64(const float (&l)[NI], const GateSe
 // Selects the experts of one token.  Lane l holds the logits of experts
 // l * NI + i, so that among equal scores the lowest lane, and in it the
 // lowest i, is the lowest expert index.  score = softmax over the finite
-// logits, or sigmoid; selection by score + bias (BIAS) or by score alone,
+// logits, or sigmoid; selection by score + bias, or without a bias by score alone,
 // for which the logits themselves are compared (both scores grow with the
 // logit).  Experts whose logit is not finite, or whose score + bias is NaN or
 // -inf, are never selected; when none is left the remaining places get id -1
@@ -138,68 +149,61 @@ __device__ __forceinline__ void gate_select64(const float (&l)[NI], const GateSe
 // selected again in 64 bits.  (All in 64 bits measured 19.5 us against 11.9 us
 // for 8192 tokens of 256 experts.)
 //
+// l: the lane's logits; logit_of(e): expert e's, read again.
 // emit(j, id, weight) is called by lane j with place j's expert and its
 // weight: the score, divided by the selected scores' sum if renorm, times
 // scale.
-template <int NI, bool BIAS, class F>
-__device__ __forceinline__ void gate_select(const float (&l)[NI], const GateSel& g, int lane, F&& emit) {
+template <int NI, class L, class F>
+__device__ __forceinline__ void gate_select(const float (&l)[NI], const GateSel& g, int lane, L&& logit_of, F&& emit) {
   const float kNone = -__builtin_inff();
-  float p[NI], sel[NI];
+  const bool softmax = g.scoring == MOEFP4_SCORE_SOFTMAX, biased = g.bias != nullptr;
+  float p[NI], sel[NI], bias[NI];
   bool fin[NI];
   float m = kNone, inv = 1.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    fin[i] = lane * NI + i < g.E && __builtin_isfinite(l[i]);
+    const int e = lane * NI + i;
+    fin[i] = e < g.E && __builtin_isfinite(l[i]);
+    bias[i] = biased && e < g.E ? g.bias[e] : 0.0f;
     if (fin[i]) m = max_of(m, l[i]);
   }
-  const bool softmax = g.scoring == MOEFP4_SCORE_SOFTMAX;
-  if (softmax) {
-    m = wave_max(m);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      p[i] = fin[i] ? expf(l[i] - m) : 0.0f;
-      sum += p[i];
-    }
-    inv = 1.0f / wave_sum(sum);
-  }
+  if (softmax) m = wave_max(m);
+  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if constexpr (BIAS) {
-      p[i] = softmax ? p[i] * inv : 1.0f / (1.0f + expf(-l[i]));
-      const float s = p[i] + (fin[i] ? g.bias[lane * NI + i] : 0.0f);
-      sel[i] = fin[i] && s > kNone ? s : kNone;  // (false for NaN)
-    } else {
-      sel[i] = fin[i] ? l[i] : kNone;
-    }
+    // e^(l - m) of the softmax, or e^-l of the sigmoid
+    const float x = expf(softmax ? l[i] - m : -l[i]);
+    p[i] = !fin[i] ? 0.0f : softmax ? x : 1.0f / (1.0f + x);
+    sum += p[i];
+  }
+  if (softmax) inv = 1.0f / wave_sum(sum);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    p[i] *= inv;
+    const float s = biased ? p[i] + bias[i] : l[i];
+    sel[i] = fin[i] && s > kNone ? s : kNone;  // (false for NaN)
   }
   float mine = 0.0f;  // the score of the place this lane holds
   int my = -1;        // and its expert
   float prev = 0.0f;
   bool narrow = false;
   // (biased: one place more than needed, for the gap behind the last one)
-  take_top<NI>(sel, BIAS ? g.top_k + 1 : g.top_k, lane, [&](int j, int who, int wi, float top)
-                                                           __attribute__((always_inline)) {
-    if constexpr (BIAS) {
-      if (j > 0 && !(prev - top > 0x1p-20f * max_of(1.0f, __builtin_fabsf(prev)))) narrow = true;
-      prev = top;
-    }
+  take_top<NI>(sel, biased ? g.top_k + 1 : g.top_k, lane, [&](int j, int who, int wi, float top)
+                                                             __attribute__((always_inline)) {
+    if (biased && j > 0 && !(prev - top > 0x1p-20f * max_of(1.0f, __builtin_fabsf(prev)))) narrow = true;
+    prev = top;
     float ps = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (i == wi) ps = BIAS || softmax ? p[i] : l[i];
-    ps = __shfl(ps, who, 64);
+      if (i == wi) ps = p[i];
+    ps = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ps), who));
     if (lane == j && j < g.top_k) mine = ps, my = who * NI + wi;
   });
-  if constexpr (BIAS) {
-    if (narrow) gate_select64<NI>(l, g, lane, &my, &mine);
-  } else {
-    if (my >= 0) mine = softmax ? mine * inv : 1.0f / (1.0f + expf(-mine));
-  }
+  if (narrow) gate_select64<NI>(g, lane, logit_of, &my, &mine);
   float f = g.scale;
   if (g.renorm) {
-    const float sum = wave_sum(lane < g.top_k ? mine : 0.0f);
-    f = sum > 0.0f ? f / sum : 0.0f;
+    const float total = wave_sum(lane < g.top_k ? mine : 0.0f);
+    f = total > 0.0f ? f / total : 0.0f;
   }
   if (lane < g.top_k) emit(lane, my, mine * f);
 }

@@ -117,13 +117,16 @@ struct FewArgs {
   uint16_t* x16;          // group16: x as fp16 * 2**-p [T, H] ...
   float* xs;              // ... and 2**p [T]
   uint16_t* h;            // [T * k][I] fp16 in blocks of 16 with a shared exponent (group16), or bf16 high and low
-                          // parts [2][T * k][I] (group32); K order of a 256-element chunk as the lanes read it
+                          // parts [2][T * k][I] (group32)
   int8_t* hexp;           // group16: [T * k][I / 16] exponents
   int32_t* sync;          // [few_sync_words]
   float* part;            // [workgroups][2][64 lanes][8] partial outputs
   int nwg;
 };
-constexpr int few_sync_words(int H) { return 2 + H / 32; }
+// launch 2's counters: a queue and a count of finished items per XCD, a line
+// each, then one word per 32 outputs
+constexpr int kFewQueues = 8, kFewLine = 32;
+constexpr int few_sync_words(int H) { return 2 * kFewQueues * kFewLine + H / 32; }
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
 // CUs of the current device (the workgroups of the persistent kernels)
 int cu_count();

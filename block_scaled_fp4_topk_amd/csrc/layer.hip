@@ -43,7 +43,12 @@ namespace moefp4 {
 namespace {
 
 constexpr int kWaves = 8;
+constexpr int kQueues = kFewQueues, kLine = kFewLine;
 constexpr int kThreads = 64 * kWaves;
+
+// Stride in LDS of a token's h (256 values, 16 bytes of padding against bank
+// conflicts).
+constexpr int kHRow = 512 + 16;
 
 // Longest wait for FC1, in ticks of the 100 MHz real-time counter (50 ms).
 constexpr uint64_t kFewMaxWait = 5000000;
@@ -100,7 +105,7 @@ __global__ __launch_bounds__(256) void few_gate_kernel(FewArgs a) {
     const int t0 = (b % nt) * TB;
     gate_dot_expert<WF32, TB>(a.gate_w, a.x, b / nt, t0, min(TB, a.T - t0), a.ld, a.H, a.logits, s_red);
   } else if (b == nd) {
-    for (int i = threadIdx.x; i < 2 + a.H / 32; i += 256) a.sync[i] = 0;
+    for (int i = threadIdx.x; i < 2 * kQueues * kLine + a.H / 32; i += 256) a.sync[i] = 0;
     if (threadIdx.x < 2) a.flags[threadIdx.x] = 0;
   } else {
     const int t = b - nd - 1;
@@ -119,47 +124,117 @@ __device__ __forceinline__ void st_agent(void* p, uint64_t v) {
 // float -> bf16 bits, round to nearest even, NaN kept.
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
+// The XCD (accelerator complex die) this wave runs on.
+__device__ __forceinline__ int xcc_id() {
+  unsigned v;
+  asm volatile("s_getreg_b32 %0, hwreg(HW_REG_XCC_ID)" : "=s"(v));
+  return (int)(v & 0xFu);
+}
+
+// n items of a queue, by one lane.  (The offset the compiler cannot see keeps
+// it from merging the wave's lanes into one atomic, which waits for the result
+// on the spot, and with it for every load before it.)
+__device__ __forceinline__ int claim_from(int32_t* queue, int n) {
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
+  return __hip_atomic_fetch_add(queue + zero, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // LDS-only barrier: the waves' loads from memory stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 __device__ __forceinline__ void drain_memory() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// A wave-uniform pointer in scalar registers, for loads with a 32-bit
-// per-lane offset.
-__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
+// A wave-uniform pointer to memory in scalar registers, for loads with a
+// 32-bit per-lane offset.  (The address space is kept in the type: a generic
+// pointer's loads also count as LDS accesses, and the waits for LDS would then
+// wait for every weight in flight: measured 91 us instead of XX us for one
+// token of the 256-expert layer.)
+typedef const __attribute__((address_space(1))) uint8_t* GPtr;
+__device__ __forceinline__ GPtr uniform_ptr(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-  return reinterpret_cast<const uint8_t*>((uint64_t)lo | ((uint64_t)hi << 32));
+  return (GPtr)((uint64_t)lo | ((uint64_t)hi << 32));
+}
+template <class V>
+__device__ __forceinline__ V gload(GPtr p, uint32_t off) {
+  return *(const __attribute__((address_space(1))) V*)(p + off);
+}
+__device__ __forceinline__ u32x4 gload_nt(GPtr p, uint32_t off) {
+  return __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4*)(p + off));
 }
 
-// Two 16-row weight tiles x 256 K in registers: lane (r16, q) holds K [64 q,
-// 64 q + 64) of row r16 of each (32 bytes of codes; 4 group16 or 2 group32
-// scale bytes).
+// Two 16-row weight tiles x 256 K on their way: instruction j holds rows
+// 8 (j & 1) + lane / 8 of tile j / 2, 16 bytes at 16 (lane & 7): eight whole
+// 128-byte lines per instruction, marked non-temporal (measured on this
+// stream, 104 experts: 7.0 TB/s; loads in the MFMA operand's own layout ask
+// for half lines and reach 6.2 TB/s, 5.2 if non-temporal).  s: the scales of
+// the lane's operand rows (r16 of each tile, K [64 q, 64 q + 64): 4 group16 or
+// 2 group32 bytes).
 struct WPair {
-  uint4 c[4];
+  u32x4 c[4];
   uint32_t s[2];
 };
 
+// Where a pair's rows lie: code offsets of the lane's rows in instructions 0
+// and 2 (8 rows further on in 1 and 3) and scale offsets of its operand rows.
+// Chunk c is c * 128 code and c * 16 (group16) or c * 8 scale bytes on.
+struct WSrc {
+  GPtr codes, sf;
+  uint32_t o0, o1, step8, f0, f1;
+};
+
 template <int MODE>
-__device__ __forceinline__ void load_pair(WPair& w, const uint8_t* codes, uint32_t o0, uint32_t o1, const uint8_t* sf,
-                                          uint32_t f0, uint32_t f1) {
-  w.c[0] = ld_nt(codes + o0);
-  w.c[1] = ld_nt(codes + o0 + 16);
-  w.c[2] = ld_nt(codes + o1);
-  w.c[3] = ld_nt(codes + o1 + 16);
+__device__ __forceinline__ void load_pair(WPair& w, const WSrc& s, uint32_t c) {
+  w.c[0] = gload_nt(s.codes, s.o0 + c * 128);
+  w.c[1] = gload_nt(s.codes, s.o0 + s.step8 + c * 128);
+  w.c[2] = gload_nt(s.codes, s.o1 + c * 128);
+  w.c[3] = gload_nt(s.codes, s.o1 + s.step8 + c * 128);
   if (MODE == 0) {
-    w.s[0] = *reinterpret_cast<const uint32_t*>(sf + f0);
-    w.s[1] = *reinterpret_cast<const uint32_t*>(sf + f1);
+    w.s[0] = gload<uint32_t>(s.sf, s.f0 + c * 16);
+    w.s[1] = gload<uint32_t>(s.sf, s.f1 + c * 16);
   } else {
-    w.s[0] = *reinterpret_cast<const uint16_t*>(sf + f0);
-    w.s[1] = *reinterpret_cast<const uint16_t*>(sf + f1);
+    w.s[0] = gload<uint16_t>(s.sf, s.f0 + c * 8);
+    w.s[1] = gload<uint16_t>(s.sf, s.f1 + c * 8);
   }
 }
 
-__device__ __forceinline__ uint32_t dword(const uint4& v, int r) {
-  return r == 0 ? v.x : r == 1 ? v.y : r == 2 ? v.z : v.w;
+// The codes turned into operand order through the wave's own 4 KB of LDS (no
+// barrier: a wave's LDS accesses stay in order): row r's 16-byte segment s
+// sits at s ^ ((r >> 1) & 7), which spreads the 16 rows of a read over all
+// banks.  at: the lane's write offsets of instructions 0 and 1 and read offsets
+// of its two segments.
+struct Turn {
+  uint32_t w0, w1, r0, r1;
+};
+__device__ __forceinline__ Turn turn_offsets(int lane) {
+  const int r16 = lane & 15, q = lane >> 4, wr = lane >> 3, seg = lane & 7;
+  Turn t;
+  t.w0 = wr * 128 + 16 * (seg ^ (wr >> 1));
+  t.w1 = (wr + 8) * 128 + 16 * (seg ^ ((wr + 8) >> 1));
+  t.r0 = r16 * 128 + 16 * ((2 * q) ^ (r16 >> 1));
+  t.r1 = r16 * 128 + 16 * ((2 * q + 1) ^ (r16 >> 1));
+  return t;
+}
+__device__ __forceinline__ void turn_pair(WPair& w, uint8_t* lds, const Turn& t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<u32x4*>(lds + 2048 * i + t.w0) = w.c[2 * i];
+    *reinterpret_cast<u32x4*>(lds + 2048 * i + t.w1) = w.c[2 * i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w.c[2 * i] = *reinterpret_cast<const u32x4*>(lds + 2048 * i + t.r0);
+    w.c[2 * i + 1] = *reinterpret_cast<const u32x4*>(lds + 2048 * i + t.r1);
+  }
+}
+
+// The pair is used from here on: its decoding does not move up in front of
+// other pairs' products, where it would wait for its loads too early.
+__device__ __forceinline__ void use_from_here(WPair& w) {
+  asm volatile("" : "+v"(w.c[0]), "+v"(w.c[1]), "+v"(w.c[2]), "+v"(w.c[3]), "+v"(w.s[0]), "+v"(w.s[1]));
 }
 
 // acc[i] += tile i x B over the chunk; B(j): the operand of K [64 q + 8 j, + 8),
@@ -167,52 +242,70 @@ __device__ __forceinline__ uint32_t dword(const uint4& v, int r) {
 template <int MODE, int NB, class BF>
 __device__ __forceinline__ void mfma_pair(const WPair& w, v4f (&acc)[2], BF&& B) {
   if constexpr (MODE == 0) {
+    v2h sc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const v2h lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.s[i], 1.0f, false);
-      const v2h hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.s[i], 1.0f, true);
+      sc[i][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.s[i], 1.0f, false);
+      sc[i][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.s[i], 1.0f, true);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const _Float16 s = j < 2 ? lo[0] : j < 4 ? lo[1] : j < 6 ? hi[0] : hi[1];
-        const v8h A = dq8_f16(dword(w.c[2 * i + (j >> 2)], j & 3), v2h{s, s});
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A, __builtin_bit_cast(v8h, B(j, 0)), acc[i], 0, 0, 0);
+    for (int j = 0; j < 8; ++j) {
+      const v8h b = __builtin_bit_cast(v8h, B(j, 0));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const _Float16 s = sc[i][j >> 2][(j >> 1) & 1];
+        const v8h A = dq8_f16(w.c[2 * i + (j >> 2)][j & 3], v2h{s, s});
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A, b, acc[i], 0, 0, 0);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float lo = ue8m0_to_f32(w.s[i] & 0xFFu), hi = ue8m0_to_f32(w.s[i] >> 8);
+    for (int j = 0; j < 8; ++j) {
+      v8bf b[NB];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const v8bf A = dq8_bf16(dword(w.c[2 * i + (j >> 2)], j & 3), j < 4 ? lo : hi);
+      for (int n = 0; n < NB; ++n) b[n] = __builtin_bit_cast(v8bf, B(j, n));
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, __builtin_bit_cast(v8bf, B(j, n)), acc[i], 0, 0, 0);
+      for (int i = 0; i < 2; ++i) {
+        const v8bf A = dq8_bf16(w.c[2 * i + (j >> 2)][j & 3], ue8m0_to_f32((w.s[i] >> (8 * (j >> 2))) & 0xFFu));
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, b[n], acc[i], 0, 0, 0);
       }
     }
   }
 }
 
 // Launch 2.  MODE 0: group16 (fp16 products), 1: group32 (bf16); NC: chunks of
-// H per wave.
-template <int MODE, int NC>
+// H per wave; NI: router logits per lane.
+template <int MODE, int NC, int NI>
 __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ float4 s_red[2][kWaves][2][64];
+  __shared__ __attribute__((aligned(16))) uint8_t s_turn[kWaves][4096];
+  __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][(MODE == 0 ? 4 : 8) * kHRow];
   __shared__ int s_ids[kFewTokens * kFewMaxK];
   __shared__ float s_tw[kFewTokens * kFewMaxK];
   __shared__ short s_rank[kMaxExperts], s_act[kMaxExperts];
   __shared__ uint8_t s_col[kMaxExperts * kFewTokens];  // [active][token]: place of the expert in the token's list
+  __shared__ uint8_t s_idx[kMaxExperts * kFewTokens];  // [active][token]: the token's number among the expert's
+  __shared__ __attribute__((aligned(16))) uint16_t s_slot[kMaxExperts * kFewTokens];  // [active][number]: its h row
+  __shared__ uint8_t s_ne[kMaxExperts];                // [active]: tokens
+  __shared__ float s_gs13[kMaxExperts], s_gs2[kMaxExperts], s_xs[kFewTokens];
   __shared__ int s_cnt[kWaves], s_claim[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4;
   const int T = a.T, H = a.H, I = a.I, kt = a.g.top_k + a.g.shared;
-  int32_t* const queue = a.sync;
-  int32_t* const done = a.sync + 1;
+  // A queue of items and a counter of finished ones per XCD, a line each:
+  // item i belongs to queue i % 8.  (256 workgroups on one counter: 50 ns per
+  // claim, 13 us until the last one has its first item.)
+  const int xcd = xcc_id() & (kQueues - 1);
+  int32_t* const queues = a.sync;
+  int32_t* const dones = a.sync + kQueues * kLine;
 
   // the first claim does not need the selection
-  if (tid == 0) s_claim[0] = __hip_atomic_fetch_add(queue, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  int q_of = xcd;  // the queue this workgroup claims from
+  int claimed = 0;
+  if (tid == 0) claimed = claim_from(queues + q_of * kLine, 2);
 
   // ---- selection, by every workgroup for itself
   for (int i = tid; i < kMaxExperts; i += kThreads) s_rank[i] = 0;
@@ -223,21 +316,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       s_ids[t * kt + j] = id;
       s_tw[t * kt + j] = w;
     };
-    if (a.ld <= 256) {
-      float l[4];
-      // (rows are padded to ld: lanes past it hold nothing)
-      const float4 v = 4 * lane < a.ld ? *reinterpret_cast<const float4*>(row + 4 * lane) : float4{0.f, 0.f, 0.f, 0.f};
-      l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
-      if (a.g.bias) gate_select<4, true>(l, a.g, lane, emit);
-      else gate_select<4, false>(l, a.g, lane, emit);
-    } else {
-      float l[8];
-      const float4 u = *reinterpret_cast<const float4*>(row + 8 * lane);
-      const float4 v = *reinterpret_cast<const float4*>(row + 8 * lane + 4);
-      l[0] = u.x, l[1] = u.y, l[2] = u.z, l[3] = u.w, l[4] = v.x, l[5] = v.y, l[6] = v.z, l[7] = v.w;
-      if (a.g.bias) gate_select<8, true>(l, a.g, lane, emit);
-      else gate_select<8, false>(l, a.g, lane, emit);
+    // (rows are padded to 64 * NI)
+    float l[NI];
+#pragma unroll
+    for (int i = 0; i < NI; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(row + lane * NI + i);
+      l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
     }
+    gate_select<NI>(l, a.g, lane, [&](int e) __attribute__((always_inline)) { return row[e]; }, emit);
     for (int j = lane; j < a.g.shared; j += 64) {
       s_ids[t * kt + a.g.top_k + j] = a.g.E + j;
       s_tw[t * kt + a.g.top_k + j] = 1.0f;
@@ -245,22 +331,23 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   }
   // this wave's activations (behind the selection: its registers are free now)
   const int nch = H >> 8;
-  uint4 xb[NC][8];
+  u32x4 xb[NC][8];
   {
     const uint16_t* src = (MODE == 0 ? a.x16 : a.x) + (size_t)(r16 < T ? r16 : 0) * H + 64 * q;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int ck = wave * NC + i;
+      const int ck = wave + kWaves * i;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xb[i][j] = uint4{0u, 0u, 0u, 0u};
+      for (int j = 0; j < 8; ++j) xb[i][j] = u32x4{0u, 0u, 0u, 0u};
       if (ck < nch && r16 < T) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xb[i][j] = *reinterpret_cast<const uint4*>(src + ck * 256 + 8 * j);
+        for (int j = 0; j < 8; ++j) xb[i][j] = *reinterpret_cast<const u32x4*>(src + ck * 256 + 8 * j);
       }
     }
   }
+  if (tid == 0) s_claim[0] = claimed;
   __syncthreads();
-  int item = __builtin_amdgcn_readfirstlane(s_claim[0]), next = item + 1;
+  int item = __builtin_amdgcn_readfirstlane(s_claim[0]) * kQueues + q_of, next = item + kQueues;
   for (int i = tid; i < T * kt; i += kThreads)
     if (s_ids[i] >= 0) s_rank[s_ids[i]] = 1;
   __syncthreads();
@@ -279,7 +366,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     const int rank = before + __popcll(on & ((1ull << lane) - 1ull));
     s_act[rank] = (short)tid;
     s_rank[tid] = (short)rank;
+    s_gs13[rank] = a.w13_gs ? a.w13_gs[tid] : 1.0f;
+    s_gs2[rank] = a.w2_gs ? a.w2_gs[tid] : 1.0f;
   }
+  if (tid < kFewTokens) s_xs[tid] = MODE == 0 && tid < T ? a.xs[tid] : 1.0f;
   __syncthreads();
   int none = 0;
   for (int i = tid; i < T * kt; i += kThreads) {
@@ -292,6 +382,24 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
   }
   if (none) atomicAdd(a.flags, none);
+  if (nact == 0) {  // no token has an expert (every workgroup finds the same)
+    for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < (size_t)T * H; i += (size_t)gridDim.x * kThreads) {
+      if (a.out_f32) static_cast<float*>(a.out)[i] = 0.0f;
+      else static_cast<uint16_t*>(a.out)[i] = 0;
+    }
+    return;
+  }
+  __syncthreads();
+  if (tid < nact) {
+    int n = 0;
+    for (int t = 0; t < T; ++t) {
+      s_idx[tid * kFewTokens + t] = (uint8_t)n;
+      const int col = s_col[tid * kFewTokens + t];
+      if (col != 255) s_slot[tid * kFewTokens + n++] = (uint16_t)(t * kt + col);
+    }
+    s_ne[tid] = (uint8_t)n;
+    for (; n < kFewTokens; ++n) s_slot[tid * kFewTokens + n] = s_slot[tid * kFewTokens];  // (any row that exists)
+  }
   __syncthreads();
 
   // ---- FC1 + SwiGLU: h
@@ -301,36 +409,60 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const size_t A = (size_t)T * kt;
   WPair w1[NC];
   auto expert = [&](int act) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((int)s_act[act]); };
-  auto load1 = [&](int item, int i, WPair& w) __attribute__((always_inline)) {
-    const int ck = wave * NC + i;
-    if (item < n1 && ck < nch) {
-      const int act = item / npt, pt = item - act * npt, e = expert(act);
-      const uint8_t* codes = uniform_ptr(a.w13 + (size_t)e * 2 * I * rowb);
-      const uint8_t* sf = uniform_ptr(a.w13_sf + (size_t)e * 2 * I * rows);
-      const uint32_t g0 = (uint32_t)(pt * 16 + r16) + (a.w13_order ? (uint32_t)I : 0u);
-      const uint32_t u0 = (uint32_t)(pt * 16 + r16) + (a.w13_order ? 0u : (uint32_t)I);
-      const uint32_t co = (uint32_t)(ck * 128 + 32 * q), so = MODE == 0 ? ck * 16 + 4 * q : ck * 8 + 2 * q;
-      load_pair<MODE>(w, codes, g0 * rowb + co, u0 * rowb + co, sf, g0 * rows + so, u0 * rows + so);
-    }
+  auto src1 = [&](int it) __attribute__((always_inline)) -> WSrc {
+    const int i0 = it < n1 ? it : 0;
+    const int act = i0 / npt, pt = i0 - act * npt, e = expert(act);
+    // (past the last item the lanes' offsets collapse to one line: loads that
+    // are issued all the same and whose data is not used)
+    const uint32_t on = it < n1 ? 1u : 0u;
+    const uint32_t g0 = (uint32_t)(pt * 16) + (a.w13_order ? (uint32_t)I : 0u);
+    const uint32_t u0 = (uint32_t)(pt * 16) + (a.w13_order ? 0u : (uint32_t)I);
+    const uint32_t co = 16 * (lane & 7), so = MODE == 0 ? 4 * q : 2 * q;
+    return WSrc{uniform_ptr(a.w13 + (size_t)e * 2 * I * rowb), uniform_ptr(a.w13_sf + (size_t)e * 2 * I * rows),
+                on * ((g0 + (lane >> 3)) * rowb + co), on * ((u0 + (lane >> 3)) * rowb + co), on * 8 * rowb,
+                on * ((g0 + r16) * rows + so), on * ((u0 + r16) * rows + so)};
   };
+  const Turn turn = turn_offsets(lane);
+  uint8_t* const my_turn = s_turn[wave];
   int buf = 0, mine = 0;
+  // chunk i of this wave, one that exists where H has fewer (its activations
+  // are zero).  No load of the loop is conditional: the compiler counts the
+  // loads in flight over every path, and waits for more than it has to where
+  // one of them has fewer.
+  uint32_t ck1[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) load1(item, i, w1[i]);
+  for (int i = 0; i < NC; ++i) ck1[i] = (uint32_t)(wave + kWaves * i < nch ? wave + kWaves * i : nch - 1);
   while (item < n1) {
-    int claim = 0;
-    if (wave == 0) claim = __hip_atomic_fetch_add(queue, lane == 0 ? 1 : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+    const WSrc src = src1(item);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (wave * NC + i < nch)
-        mfma_pair<MODE, 1>(w1[i], acc, [&](int j, int) __attribute__((always_inline)) { return xb[i][j]; });
-      load1(next, i, w1[i]);
+      load_pair<MODE>(w1[i], src, ck1[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (the activations, requested earlier, have arrived: without this they
+    // would count as in flight throughout the loop)
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(xb[i][j]));
+  do {
+    int claim = 0;
+    if (tid == 0) claim = claim_from(queues + q_of * kLine, 1);
+    v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+    const WSrc src = src1(next);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      use_from_here(w1[i]);
+      turn_pair(w1[i], my_turn, turn);
+      mfma_pair<MODE, 1>(w1[i], acc, [&](int j, int) __attribute__((always_inline)) { return xb[i][j]; });
+      load_pair<MODE>(w1[i], src, ck1[i]);
+      __builtin_amdgcn_sched_barrier(0);
     }
     s_red[buf][wave][0][lane] = float4{acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
     s_red[buf][wave][1][lane] = float4{acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
-    if (wave == 0) s_claim[buf] = __builtin_amdgcn_readfirstlane(claim);
+    if (tid == 0) s_claim[buf] = claim;
     lds_barrier();
-    const int after = __builtin_amdgcn_readfirstlane(s_claim[buf]);
+    const int after = __builtin_amdgcn_readfirstlane(s_claim[buf]) * kQueues + q_of;
     if (wave == (mine & (kWaves - 1))) {
       // the waves take turns: sum, SwiGLU, store.  Lane: rows 4 q .. + 3, token r16.
       float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
@@ -340,8 +472,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         g[0] += gv.x, g[1] += gv.y, g[2] += gv.z, g[3] += gv.w;
         u[0] += uv.x, u[1] += uv.y, u[2] += uv.z, u[3] += uv.w;
       }
-      const int act = item / npt, pt = item - act * npt, e = expert(act);
-      const float cs = (a.w13_gs ? a.w13_gs[e] : 1.0f) * (MODE == 0 && r16 < T ? a.xs[r16] : 1.0f);
+      const int act = item / npt, pt = item - act * npt;
+      const float cs = s_gs13[act] * s_xs[r16];
       const int col = s_col[act * kFewTokens + r16];
       float h[4];
       float amax = 0.0f;
@@ -350,11 +482,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         h[i] = swiglu(g[i] * cs, u[i] * cs);
         amax = fmaxf(amax, fabsf(h[i]));
       }
-      // K [16 pt + 4 q, + 4) in the order FC2's lanes read a chunk: [j][q'][8]
-      // for K = 64 q' + 8 j + (0 .. 7)
-      const int kk = (pt & 15) * 16 + 4 * q;
-      const size_t slot = (size_t)r16 * kt + col;
-      const size_t at = slot * I + (size_t)(pt >> 4) * 256 + ((kk >> 3) & 7) * 32 + (kk >> 6) * 8 + (kk & 4);
+      const size_t slot = (size_t)r16 * kt + col, at = slot * I + pt * 16 + 4 * q;
       if constexpr (MODE == 0) {
         amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
         amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
@@ -385,101 +513,135 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
     ++mine;
     buf ^= 1;
+    // (a queue's claims only grow: with this item past the end, so is the next)
     item = next;
     next = after;
+  } while (item < n1);
+    // this queue is empty: on to one that is not, if there is one (the XCD's
+    // workgroups may not all be running)
+    if (wave == 0) {
+      const int taken = __hip_atomic_load(queues + (lane & (kQueues - 1)) * kLine, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+      const uint64_t left = ballot(lane < kQueues && taken * kQueues + lane < n1);
+      if (lane == 0) s_claim[buf] = left ? (int)__builtin_ctzll(left) : -1;
+    }
+    lds_barrier();
+    const int other = __builtin_amdgcn_readfirstlane(s_claim[buf]);
+    buf ^= 1;
+    if (other < 0) break;
+    q_of = other;
+    if (tid == 0) s_claim[buf] = claim_from(queues + q_of * kLine, 2);
+    lds_barrier();
+    item = __builtin_amdgcn_readfirstlane(s_claim[buf]) * kQueues + q_of;
+    buf ^= 1;
+    next = item + kQueues;
   }
 
   // ---- FC2: this workgroup's run of steps
   const int nch2 = I >> 8, units = nact * nch2;
-  const int ns = units > kWaves ? (units + kWaves - 1) / kWaves : 1;
+  const int ns = (units + kWaves - 1) / kWaves;
   const int nrb = H >> 5;
-  const long long total = (long long)nrb * ns;
-  const int G = a.nwg < total ? a.nwg : (int)total;
-  const int wg = blockIdx.x;
+  const uint32_t total = (uint32_t)(nrb * ns);  // total * nwg < 2^31 (checked by the launch)
+  const uint32_t G = min((uint32_t)a.nwg, total);
+  const uint32_t wg = blockIdx.x;
   drain_memory();  // this wave's stores of h are complete
   const bool works = wg < G;
-  const long long begin = works ? wg * total / G : 0, end = works ? (wg + 1) * total / G : 0;
+  const int begin = works ? (int)(wg * total / G) : 0, end = works ? (int)((wg + 1) * total / G) : 0;
   const uint32_t rowb2 = (uint32_t)(I >> 1), rows2 = (uint32_t)(MODE == 0 ? I >> 4 : I >> 5);
-  constexpr int NB = MODE == 0 ? 1 : 2;
-  constexpr int NS = MODE == 0 ? 3 : 2;  // steps in flight (what the registers hold)
+  constexpr int NB = MODE == 0 ? 1 : 2;  // parts of h
+  constexpr int kHalf = 4;               // tokens of an expert taken at a time
+  constexpr int NS = 3;                  // steps in flight
   WPair w2[NS];
-  uint2 hb[NS][8 * NB][2];
+  uint64_t hb[NS][NB][kHalf];
   uint32_t hx[NS];
-  // the (row block, step) walked by the loads, and by the products
-  struct Pos { int rb, st; };
-  auto advance = [&](Pos& p) __attribute__((always_inline)) {
-    if (++p.st == ns) p.st = 0, ++p.rb;
+  // The run is walked in groups of up to NS steps of one row block.
+  struct Group { int rb, st, n; };
+  auto group = [&](int s) __attribute__((always_inline)) -> Group {
+    const int rb = s / ns, st = s - rb * ns;
+    return Group{rb, st, min(NS, min(ns - st, end - s))};
   };
-  Pos lw = {(int)(begin / ns), (int)(begin % ns)}, lh = lw, pc = lw;
-  auto load_w2 = [&](const Pos& p, WPair& w) __attribute__((always_inline)) {
-    const int f = p.st * kWaves + wave;
-    if (f < units) {
-      const int act = f / nch2, c = f - act * nch2, e = expert(act);
-      const uint8_t* codes = uniform_ptr(a.w2 + (size_t)e * H * rowb2);
-      const uint8_t* sf = uniform_ptr(a.w2_sf + (size_t)e * H * rows2);
-      const uint32_t r0 = (uint32_t)(p.rb * 32 + r16), r1 = r0 + 16;
-      const uint32_t co = (uint32_t)(c * 128 + 32 * q), so = MODE == 0 ? c * 16 + 4 * q : c * 8 + 2 * q;
-      load_pair<MODE>(w, codes, r0 * rowb2 + co, r1 * rowb2 + co, sf, r0 * rows2 + so, r1 * rows2 + so);
+  // the unit of step st that this wave takes (where the last step of a block
+  // has fewer than 8, a unit that exists, whose product is not added)
+  auto unit = [&](int st, int* act, int* c) __attribute__((always_inline)) {
+    int f = st * kWaves + wave;
+    f = f < units ? f : units - 1;
+    *act = f / nch2;
+    *c = f - *act * nch2;
+  };
+  // Step k of a group.  Loads of steps that the group does not have are issued
+  // too, all lanes from one line (see FC1).
+  auto load_w2 = [&](const Group& g, int k, WPair& w) __attribute__((always_inline)) {
+    const uint32_t on = k < g.n ? 1u : 0u;
+    int act, c;
+    unit(on ? g.st + k : g.st, &act, &c);
+    const int e = expert(act);
+    const uint32_t r0 = (uint32_t)(g.rb * 32), co = 16 * (lane & 7), so = MODE == 0 ? 4 * q : 2 * q;
+    load_pair<MODE>(w, WSrc{uniform_ptr(a.w2 + (size_t)e * H * rowb2), uniform_ptr(a.w2_sf + (size_t)e * H * rows2),
+                            on * ((r0 + (lane >> 3)) * rowb2 + co), on * ((r0 + 16 + (lane >> 3)) * rowb2 + co),
+                            on * 8 * rowb2, on * ((r0 + r16) * rows2 + so), on * ((r0 + 16 + r16) * rows2 + so)}, c);
+  };
+  // h of the expert's tokens n0 .. n0 + kHalf - 1, a token's 512 bytes per
+  // load (and per part); loads for tokens it does not have collapse likewise.
+  // (Offsets in 32 bits: h is below 2 GB.)
+  auto h_rows = [&](int act, int c, int n0, bool on, uint64_t (&b)[NB][kHalf]) __attribute__((always_inline)) {
+    const uint2 four = *reinterpret_cast<const uint2*>(s_slot + act * kFewTokens + n0);
+    const int ne = on ? __builtin_amdgcn_readfirstlane((int)s_ne[act]) : 0;
+    const uint32_t pair[2] = {(uint32_t)__builtin_amdgcn_readfirstlane((int)four.x),
+                              (uint32_t)__builtin_amdgcn_readfirstlane((int)four.y)};
+#pragma unroll
+    for (int n = 0; n < kHalf; ++n) {
+      const uint32_t slot = (pair[n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
+      const uint32_t o = 2 * (slot * (uint32_t)I + c * 256) + (n0 + n < ne ? 8 * lane : 0);
+#pragma unroll
+      for (int p = 0; p < NB; ++p) b[p][n] = ld_agent(reinterpret_cast<const uint8_t*>(a.h + p * A * I) + o);
     }
   };
-  auto load_h = [&](const Pos& p, uint2 (&b)[8 * NB][2], uint32_t& x) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 8 * NB; ++j) b[j][0] = b[j][1] = uint2{0u, 0u};
-    x = 0x80808080u;
-    const int f = p.st * kWaves + wave;
-    if (f < units) {
-      const int act = f / nch2, c = f - act * nch2;
+  auto load_h = [&](const Group& g, int k, uint64_t (&b)[NB][kHalf], uint32_t& x) __attribute__((always_inline)) {
+    const bool on = k < g.n;
+    int act, c;
+    unit(on ? g.st + k : g.st, &act, &c);
+    h_rows(act, c, 0, on, b);
+    if (MODE == 0) {
       const int col = s_col[act * kFewTokens + r16];
-      if (col != 255) {
-        const size_t slot = (size_t)r16 * kt + col;
-        const uint16_t* src = a.h + slot * I + c * 256 + 8 * q;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            b[8 * n + j][0] = __builtin_bit_cast(uint2, ld_agent(src + n * A * I + 32 * j));
-            b[8 * n + j][1] = __builtin_bit_cast(uint2, ld_agent(src + n * A * I + 32 * j + 4));
-          }
-        if (MODE == 0)
-          x = __hip_atomic_load(reinterpret_cast<const uint32_t*>(a.hexp + slot * (I >> 4) + c * 16 + 4 * q),
-                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[act * kFewTokens];
+      const uint32_t o = slot * (uint32_t)(I >> 4) + c * 16 + 4 * q;
+      x = __hip_atomic_load(reinterpret_cast<const uint32_t*>(a.hexp + o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   };
-  long long ahead = begin;
+  Group cur = group(begin);
 #pragma unroll
-  for (int s = 0; s < NS; ++s)
-    if (begin + s < end) {
-      load_w2(lw, w2[s]);
-      advance(lw);
-      ++ahead;
-    }
+  for (int k = 0; k < NS; ++k) {
+    load_w2(cur, k, w2[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   lds_barrier();  // (every wave's stores are complete)
-  if (wave == 0 && (works || mine)) {
-    if (mine) __hip_atomic_fetch_add(done, lane == 0 ? mine : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (wave == 0) {
+    if (mine && lane == 0)
+      __hip_atomic_fetch_add(dones + xcd * kLine, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
     while (works) {
-      const int d =
-          __builtin_amdgcn_readfirstlane(__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-      if (d >= n1) break;
+      int d = __hip_atomic_load(dones + (lane & (kQueues - 1)) * kLine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      d += __shfl_xor(d, 1, 64);
+      d += __shfl_xor(d, 2, 64);
+      d += __shfl_xor(d, 4, 64);
+      if (__builtin_amdgcn_readfirstlane(d) >= n1) break;
       if (__builtin_amdgcn_s_memrealtime() - t0 > kFewMaxWait) {
-        __hip_atomic_fetch_add(a.flags + 1, lane == 0 ? 1 : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) __hip_atomic_fetch_add(a.flags + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         break;
       }
-      __builtin_amdgcn_s_sleep(1);
+      __builtin_amdgcn_s_sleep(4);
     }
   }
   lds_barrier();
 #pragma unroll
-  for (int s = 0; s < NS; ++s)
-    if (begin + s < end) {
-      load_h(lh, hb[s], hx[s]);
-      advance(lh);
-    }
+  for (int k = 0; k < NS; ++k) {
+    load_h(cur, k, hb[k], hx[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
   float oacc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   int first = 1;  // still in the run's first row block
-  int turn = 0;
+  int flushes = 0;
   // the row block's sum over the waves, and on to the output: directly where
   // the run holds the whole block, else through the parts
   auto flush = [&](int rb) __attribute__((always_inline)) {
@@ -488,7 +650,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) oacc[i] = 0.0f;
     lds_barrier();
-    if (wave == (turn & (kWaves - 1))) {
+    if (wave == (flushes & (kWaves - 1))) {
       float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
@@ -496,7 +658,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         o[0] += u.x, o[1] += u.y, o[2] += u.z, o[3] += u.w;
         o[4] += v.x, o[5] += v.y, o[6] += v.z, o[7] += v.w;
       }
-      const long long s0 = (long long)rb * ns, s1 = s0 + ns;
+      const int s0 = rb * ns, s1 = s0 + ns;
       bool write = true;
       if (begin > s0 || end < s1) {
         float* mypart = a.part + ((size_t)wg * 2 + (first ? 0 : 1)) * 512 + lane * 8;
@@ -504,15 +666,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         for (int i = 0; i < 4; ++i) st_agent(mypart + 2 * i, (uint64_t)f2u(o[2 * i]) | ((uint64_t)f2u(o[2 * i + 1]) << 32));
         drain_memory();
         // owners of the block's first and last step (the last w with w total / G <= step)
-        const int o0 = (int)(((s0 + 1) * G - 1) / total), o1 = (int)((s1 * G - 1) / total);
-        const int arrived = __builtin_amdgcn_readfirstlane(
-            __hip_atomic_fetch_add(a.sync + 2 + rb, lane == 0 ? 1 : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        write = arrived == o1 - o0;
+        const uint32_t o0 = ((s0 + 1) * G - 1) / total, o1 = (s1 * G - 1) / total;
+        const int came = __builtin_amdgcn_readfirstlane(
+            __hip_atomic_fetch_add(a.sync + 2 * kQueues * kLine + rb, lane == 0 ? 1 : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        write = came == (int)(o1 - o0);
         if (write) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-          for (int w = o0; w <= o1; ++w) {
-            const bool head = (w * total / G) / ns == rb;  // the block is run w's first
+          for (uint32_t w = o0; w <= o1; ++w) {
+            const bool head = (int)(w * total / G) >= s0;  // the block is run w's first
             const float* p = a.part + ((size_t)w * 2 + (head ? 0 : 1)) * 512 + lane * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -537,41 +699,77 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         }
       }
     }
-    ++turn;
+    ++flushes;
     buf ^= 1;
     first = 0;
   };
-  for (long long s = begin; s < end; s += NS) {
+  uint8_t* const my_h = s_h[wave];
+  // (waits for loads of h here, so that code behind a branch does not)
+  auto arrived = [](uint64_t (&b)[NB][kHalf]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < NB; ++p)
+#pragma unroll
+      for (int n = 0; n < kHalf; ++n) asm volatile("" : "+v"(b[p][n]));
+  };
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    arrived(hb[k]);
+    if (MODE == 0) asm volatile("" : "+v"(hx[k]));
+  }
+  for (int s = begin; s < end;) {
+    const int after = s + cur.n;
+    // (past the end: the last group's place, with no steps)
+    Group nxt = group(after < end ? after : s);
+    nxt.n = after < end ? nxt.n : 0;
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
-      if (s + k < end) {
-        const int f = pc.st * kWaves + wave;
-        if (f < units) {
-          const int act = f / nch2, e = expert(act);
-          const int col = s_col[act * kFewTokens + r16];
-          float cs = a.w2_gs ? a.w2_gs[e] : 1.0f;
-          v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
-          if constexpr (MODE == 0) {
-            // the chunk's largest exponent P; each 16-block's values times 2**(p - P)
-            const int p0 = (int)(int8_t)(hx[k] & 0xFFu), p1 = (int)(int8_t)((hx[k] >> 8) & 0xFFu);
-            const int p2 = (int)(int8_t)((hx[k] >> 16) & 0xFFu), p3 = (int)(int8_t)(hx[k] >> 24);
-            int P = max(max(p0, p1), max(p2, p3));
-            P = max(P, __shfl_xor(P, 16, 64));
-            P = max(P, __shfl_xor(P, 32, 64));
-            cs = __builtin_ldexpf(cs, P);
-            const _Float16 fb[4] = {(_Float16)__builtin_ldexpf(1.0f, p0 - P), (_Float16)__builtin_ldexpf(1.0f, p1 - P),
-                                    (_Float16)__builtin_ldexpf(1.0f, p2 - P), (_Float16)__builtin_ldexpf(1.0f, p3 - P)};
-            mfma_pair<MODE, 1>(w2[k], acc, [&](int j, int) __attribute__((always_inline)) {
-              const uint4 v = {hb[k][j][0].x, hb[k][j][0].y, hb[k][j][1].x, hb[k][j][1].y};
-              return __builtin_bit_cast(v8h, v) * fb[j >> 1];
-            });
-          } else {
-            mfma_pair<MODE, 2>(w2[k], acc, [&](int j, int n) __attribute__((always_inline)) {
-              return uint4{hb[k][8 * n + j][0].x, hb[k][8 * n + j][0].y, hb[k][8 * n + j][1].x, hb[k][8 * n + j][1].y};
-            });
+      use_from_here(w2[k]);
+      if (k < cur.n) {
+        int act, c;
+        unit(cur.st + k, &act, &c);
+        const int ne = __builtin_amdgcn_readfirstlane((int)s_ne[act]);
+        const int col = s_col[act * kFewTokens + r16], idx = s_idx[act * kFewTokens + r16];
+        float cs = s_gs2[act] * s_tw[r16 * kt + (col != 255 ? col : 0)];
+        turn_pair(w2[k], my_turn, turn);
+        _Float16 f4[4];
+        if constexpr (MODE == 0) {
+          // the chunk's largest exponent P; each 16-block's values times 2**(p - P)
+          int p[4], P = -128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = (int)(int8_t)(hx[k] >> (8 * i));
+            P = max(P, p[i]);
           }
-          if (col != 255) {
-            cs *= s_tw[r16 * kt + col];
+          P = max(P, __shfl_xor(P, 16, 64));
+          P = max(P, __shfl_xor(P, 32, 64));
+          cs = __builtin_ldexpf(cs, P);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f4[i] = (_Float16)__builtin_ldexpf(1.0f, p[i] - P);
+        }
+        const bool valid = col != 255 && (cur.st + k) * kWaves + wave < units;
+        // kHalf tokens at a time (more of one expert: once again, their h
+        // fetched on the spot)
+#pragma unroll 1
+        for (int n0 = 0; n0 < ne; n0 += kHalf) {
+          if (n0 > 0) {
+            h_rows(act, c, n0, true, hb[k]);
+            arrived(hb[k]);
+          }
+#pragma unroll
+          for (int p = 0; p < NB; ++p)
+#pragma unroll
+            for (int n = 0; n < kHalf; ++n)
+              *reinterpret_cast<uint64_t*>(my_h + (p * kHalf + n) * kHRow + 8 * lane) = hb[k][p][n];
+          // (columns of other tokens read some row and are not used)
+          const int r = idx - n0;
+          const uint8_t* row = my_h + (r >= 0 && r < kHalf ? r : 0) * kHRow + 128 * q;
+          v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+          mfma_pair<MODE, NB>(w2[k], acc, [&](int j, int p) __attribute__((always_inline)) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + p * kHalf * kHRow + 16 * j);
+            if constexpr (MODE == 0) return __builtin_bit_cast(v8h, v) * f4[j >> 1];
+            else return v;
+          });
+          if (valid && r >= 0 && r < kHalf) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               oacc[i] = __builtin_fmaf(acc[0][i], cs, oacc[i]);
@@ -579,27 +777,24 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
             }
           }
         }
-        if (ahead < end) {
-          load_w2(lw, w2[k]);
-          load_h(lw, hb[k], hx[k]);
-          advance(lw);
-          ++ahead;
-        }
-        const int rb = pc.rb;
-        advance(pc);
-        if (pc.st == 0 || s + k + 1 == end) flush(rb);
       }
+      load_w2(nxt, k, w2[k]);
+      load_h(nxt, k, hb[k], hx[k]);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (cur.st + cur.n == ns || after >= end) flush(cur.rb);
+    s = after;
+    cur = nxt;
   }
 }
 
-template <int MODE>
+template <int MODE, int NI>
 void launch_layer(const FewArgs& a, hipStream_t s) {
   const int nc = (a.H / 256 + kWaves - 1) / kWaves;
   const dim3 grid(a.nwg), block(kThreads);
-  if (nc <= 1) hipLaunchKernelGGL((few_layer_kernel<MODE, 1>), grid, block, 0, s, a);
-  else if (nc == 2) hipLaunchKernelGGL((few_layer_kernel<MODE, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((few_layer_kernel<MODE, 3>), grid, block, 0, s, a);
+  if (nc <= 1) hipLaunchKernelGGL((few_layer_kernel<MODE, 1, NI>), grid, block, 0, s, a);
+  else if (nc == 2) hipLaunchKernelGGL((few_layer_kernel<MODE, 2, NI>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((few_layer_kernel<MODE, 3, NI>), grid, block, 0, s, a);
 }
 
 template <bool WF32>
@@ -627,8 +822,10 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   else launch_gate_part<false>(a, s);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  if (a.g16) launch_layer<0>(a, s);
-  else launch_layer<1>(a, s);
+  if (a.g16 && a.ld == 256) launch_layer<0, 4>(a, s);
+  else if (a.g16) launch_layer<0, 8>(a, s);
+  else if (a.ld == 256) launch_layer<1, 4>(a, s);
+  else launch_layer<1, 8>(a, s);
   return hipGetLastError();
 }
 
