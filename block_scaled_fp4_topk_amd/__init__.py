@@ -14,6 +14,7 @@ Functions mirror the C entry points:
   forward(x, topk_ids, topk_w, ...)   -> moe_fp4_forward (fused=True: moe_fp4_forward_fused)
   layer(x, gate_w, top_k, w13, ...)   -> moe_fp4_layer (router and forward)
   forward_static(x, topk_ids, ...)    -> moe_fp4_forward_static (no workspace)
+  project(x, w, w_sf, w_gs, ...)      -> moe_fp4_project (FP4 projection with low-rank adapters)
   requant_gran_k(src, src_sf, ...)    -> fp4_requant_gran_k
   prepare_gemm_weights(src, src_sf, ...) -> moe_fp4_prepare_gemm_weights
   prepare_gemm_weights_g16(src, src_sf, src_gs, ...) -> moe_fp4_prepare_gemm_weights_g16
@@ -27,7 +28,7 @@ import ctypes
 import os
 
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
-           "forward_problem", "forward_static", "layer",
+           "forward_problem", "forward_static", "layer", "project",
            "requant_gran_k", "prepare_gemm_weights", "prepare_gemm_weights_g16", "quantize_act", "quantize_act_fp4",
            "dropped_assignments", "LIB_PATH"]
 
@@ -52,6 +53,11 @@ class Problem(ctypes.Structure):
 class Gate(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("top_k", "shared", "scoring", "renormalize", "w_fmt")] + \
         [("scale", ctypes.c_float)]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "N", "K")] + \
+        [(n, ctypes.c_int32) for n in ("gran_k", "out_fmt", "adapters", "rank")]
 
 
 class MoeFp4Error(RuntimeError):
@@ -90,6 +96,11 @@ def lib():
         L.moe_fp4_layer_workspace_bytes.restype = st
         L.moe_fp4_layer.argtypes = [ctypes.POINTER(Problem), gp] + [_P] * 13 + [ctypes.c_size_t, _P]
         L.moe_fp4_layer.restype = st
+        lp = ctypes.POINTER(Linear)
+        L.moe_fp4_project_workspace_bytes.argtypes = [lp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fp4_project_workspace_bytes.restype = st
+        L.moe_fp4_project.argtypes = [lp] + [_P] * 10 + [ctypes.c_size_t, _P]
+        L.moe_fp4_project.restype = st
         L.moe_fp4_forward.argtypes = [ctypes.POINTER(Problem), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_forward.restype = st
@@ -438,6 +449,57 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
     _check(lib().moe_fp4_layer(ctypes.byref(p), ctypes.byref(g), _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(w13),
                                _ptr(w13_sf), _ptr(w13_gs), _ptr(w2), _ptr(w2_sf), _ptr(w2_gs), _ptr(out),
                                _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+    return out
+
+
+def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lora_scale=None, out=None,
+            workspace=None, stream=None, out_dtype=None):
+    """A projection over FP4 weights with low-rank adapters beside it:
+    out[t] = W x[t] + lora_scale[l] * B_l (A_l x[t]), l = lora_id[t] (outside
+    [0, L), e.g. -1: no adapter).  x [T, K] bfloat16; w [N, K/2] uint8, w_sf
+    [N, K/gran_k] uint8, w_gs [1] float32 or None; lora_a [L, R, K] and lora_b
+    [L, N, R] bfloat16, lora_id [T] int32, lora_scale [L] float32, or all four
+    None.  Returns out [T, N] bfloat16 (default) or float32."""
+    import torch
+    u8, f32, bf = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
+    _dev(x, "x", bf)
+    _dev(w, "w", u8)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [T, K] and w [N, K/2]")
+    if gran_k not in (16, 32):
+        raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
+    dev = _current(x)
+    (T, K), N = x.shape, w.shape[0]
+    _arg(w, "w", u8, (N, K // 2), dev)
+    _arg(w_sf, "w_sf", u8, (N, K // gran_k), dev)
+    _arg(w_gs, "w_gs", f32, (1,), dev)
+    lora = (lora_a, lora_b, lora_id, lora_scale)
+    if any(t is None for t in lora) and any(t is not None for t in lora):
+        raise ValueError("lora_a, lora_b, lora_id and lora_scale go together")
+    adapters = rank = 0
+    if lora_a is not None:
+        _dev(lora_a, "lora_a", bf)
+        if lora_a.dim() != 3 or lora_a.shape[0] < 1:
+            raise ValueError("lora_a must be [L, R, K] with L >= 1")
+        adapters, rank = lora_a.shape[:2]
+        _arg(lora_a, "lora_a", bf, (adapters, rank, K), dev)
+        _arg(lora_b, "lora_b", bf, (adapters, N, rank), dev)
+        _arg(lora_id, "lora_id", (torch.int32,), (T,), dev)
+        _arg(lora_scale, "lora_scale", f32, (adapters,), dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    p = Linear(T, N, K, gran_k, OUT_F32 if out_dtype == torch.float32 else OUT_BF16, adapters, rank)
+    need = ctypes.c_size_t(0)
+    _check(lib().moe_fp4_project_workspace_bytes(ctypes.byref(p), ctypes.byref(need)))
+    if out is None:
+        out = _empty((T, N), out_dtype, dev, stream)
+    else:
+        _arg(out, "out", (out_dtype,), (T, N), dev)
+    ws = _scratch(workspace, need.value, dev, stream)
+    _check(lib().moe_fp4_project(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(w_sf), _ptr(w_gs), _ptr(lora_a), _ptr(lora_b),
+                                 _ptr(lora_id), _ptr(lora_scale), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 

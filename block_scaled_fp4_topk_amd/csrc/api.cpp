@@ -460,6 +460,43 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
   return MOEFP4_OK;
 }
 
+struct ProjectPlan {
+  size_t x16, xs, u, total;
+};
+
+moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
+  if (!p) return fail(MOEFP4_EINVAL, "linear is NULL");
+  if (p->T < 0 || p->N <= 0 || p->K <= 0) return fail(MOEFP4_EINVAL, "need T >= 0, N > 0 and K > 0");
+  if (p->gran_k != 16 && p->gran_k != 32) return fail(MOEFP4_EINVAL, "gran_k must be 16 or 32, got %d", p->gran_k);
+  if (p->out_fmt != MOEFP4_OUT_BF16 && p->out_fmt != MOEFP4_OUT_F32)
+    return fail(MOEFP4_EINVAL, "unknown out_fmt %d", p->out_fmt);
+  if (p->K % 32) return fail(MOEFP4_EINVAL, "K must be a multiple of 32, got %lld", (long long)p->K);
+  if (p->adapters < 0) return fail(MOEFP4_EINVAL, "adapters must be >= 0, got %d", p->adapters);
+  if (p->adapters > 0 && (p->rank <= 0 || p->rank % 8))
+    return fail(MOEFP4_EINVAL, "rank must be a positive multiple of 8, got %d", p->rank);
+  if (p->adapters > 0 && p->rank > 128) return fail(MOEFP4_EUNSUPPORTED, "rank must be at most 128, got %d", p->rank);
+  if (p->K % 256 || p->N % 16)
+    return fail(MOEFP4_EUNSUPPORTED, "K must be a multiple of 256 and N of 16, got K=%lld N=%lld", (long long)p->K,
+                (long long)p->N);
+  const int64_t lim = 1ll << 32;
+  if (p->T >= (1 << 24) || p->N >= lim || p->K >= lim || p->N * p->K >= lim ||
+      (p->T + 127) / 128 * ((p->N + 127) / 128) >= (1ll << 24) ||
+      (p->adapters > 0 && (int64_t)p->adapters * p->rank >= lim / p->N))
+    return fail(MOEFP4_EUNSUPPORTED,
+                "T must be below 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38, got T=%lld N=%lld K=%lld",
+                (long long)p->T, (long long)p->N, (long long)p->K);
+  // (few tokens: rows for whole groups of 16, as many as the launch multiplies)
+  const size_t T = (size_t)p->T, Tg = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
+  const bool few = p->T <= moefp4::kProjectFew;
+  P->x16 = take(few ? Tg * p->K * 2 : p->gran_k == 16 ? T * p->K * 2 : 0);
+  P->xs = take(p->gran_k == 16 ? T * 4 : 0);
+  P->u = take(p->adapters > 0 ? T * p->rank * 4 : 0);
+  P->total = o;
+  return MOEFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -636,6 +673,59 @@ moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const
   a.part = at<float>(workspace, P.parts);
   a.nwg = P.nwg;
   st = hip_status(moefp4::launch_few(a, stream), "layer");
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* bytes) {
+  if (!bytes) return fail(MOEFP4_EINVAL, "bytes is NULL");
+  ProjectPlan P;
+  moefp4_status st = project_check(p, &P);
+  if (st != MOEFP4_OK) return st;
+  *bytes = P.total;
+  return ok();
+}
+
+moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8_t* w, const uint8_t* w_sf,
+                              const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
+                              const float* scale, void* out, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  ProjectPlan P;
+  moefp4_status st = project_check(p, &P);
+  if (st != MOEFP4_OK) return st;
+  if (p->T == 0) return ok();
+  if (!x || !w || !w_sf || !out) return fail(MOEFP4_EINVAL, "x, w, w_sf and out must be non-NULL");
+  if (p->adapters > 0 && (!lora_a || !lora_b || !id || !scale))
+    return fail(MOEFP4_EINVAL, "lora_a, lora_b, id and scale must be non-NULL with adapters");
+  if (p->adapters == 0 && (lora_a || lora_b || id || scale))
+    return fail(MOEFP4_EINVAL, "lora_a, lora_b, id and scale must be NULL without adapters");
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(w_sf, 16) || misaligned(out, 16) || misaligned(lora_a, 16) ||
+      misaligned(lora_b, 16) || misaligned(w_gs, 4) || misaligned(id, 4) || misaligned(scale, 4))
+    return fail(MOEFP4_EINVAL, "x, w, w_sf, lora_a, lora_b and out must be 16-byte aligned, w_gs, id and scale 4-byte");
+  if (!workspace || ws_bytes < P.total)
+    return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", P.total,
+                workspace ? ws_bytes : (size_t)0);
+  if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  moefp4::ProjectArgs a;
+  memset(&a, 0, sizeof a);
+  a.T = (int)p->T;
+  a.N = (int)p->N;
+  a.K = (int)p->K;
+  a.L = p->adapters;
+  a.R = p->rank;
+  a.g16 = p->gran_k == 16;
+  a.out_f32 = p->out_fmt == MOEFP4_OUT_F32;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = w;
+  a.w_sf = w_sf;
+  a.w_gs = w_gs;
+  a.a = static_cast<const uint16_t*>(lora_a);
+  a.b = static_cast<const uint16_t*>(lora_b);
+  a.id = id;
+  a.scale = scale;
+  a.out = out;
+  a.x16 = at<uint16_t>(workspace, P.x16);
+  a.xs = at<float>(workspace, P.xs);
+  a.u = at<float>(workspace, P.u);
+  st = hip_status(moefp4::launch_project(a, stream), "project");
   return st == MOEFP4_OK ? ok() : st;
 }
 

@@ -103,8 +103,10 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   if (s0 < s1) stage(s0, s[0]);
   for (int c = s0; c < s1; ++c) {
-    // this stage's loads are in, and every wave is past the stage before,
+    // every wave waits for its own direct loads of this stage before the
+    // barrier that hands them to the others, and is past the stage before,
     // whose buffer the next one's loads take
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     const uint8_t* b = s[(c - s0) & 1];
     if (c + 1 < s1) stage(c + 1, s[(c + 1 - s0) & 1]);

@@ -131,6 +131,27 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s);
 // CUs of the current device (the workgroups of the persistent kernels)
 int cu_count();
 
+// The projection with adapters (project.hip).  K % 256 == 0, N % 16 == 0, R a
+// multiple of 8 up to 128, N * K < 2^32, T < 2^24.
+constexpr int kProjectFew = 64;   // most tokens of the form for few tokens
+constexpr int kProjectDot = 256;  // most tokens whose u is computed by dot products
+struct ProjectArgs {
+  int T, N, K, L, R;   // L = 0: no adapters
+  bool g16, out_f32;
+  const uint16_t* x;   // [T, K] bf16
+  const uint8_t *w, *w_sf;
+  const float* w_gs;   // [1] or null
+  const uint16_t *a, *b;  // [L, R, K], [L, N, R] bf16
+  const int32_t* id;      // [T]
+  const float* scale;     // [L]
+  void* out;
+  // workspace
+  uint16_t* x16;  // x as the products read it (fp16 * 2**-p for group16)
+  float* xs;      // group16: 2**p [T]
+  float* u;       // [T, R]
+};
+hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
+
 struct FcArgs {
   const uint8_t* w;          // [E, N, K/2]
   const uint8_t* wsf;        // [E, N, K/gran]

@@ -271,6 +271,35 @@ moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const
                             const uint8_t* w2, const uint8_t* w2_sf, const float* w2_gs, void* out,
                             int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, hipStream_t stream);
 
+/* A projection over FP4 weights with low-rank adapters of many requests
+ * beside it: out[t] = W x[t] + scale[l] * B_l (A_l x[t]), l = id[t]; a token
+ * whose id lies outside [0, adapters) (-1) has no adapter.  W [N, K] in the
+ * RAW layout above with group16 or group32 scales (one matrix: a layer's
+ * shared expert, or any projection quantised alike); FP32 accumulation, the
+ * low-rank activations A_l x kept to 16 bits or more; out [T, N] bfloat16 or
+ * float32 (out_fmt, moefp4_out_fmt).
+ * adapters = 0: none (lora_a, lora_b, id and scale NULL, rank ignored).
+ * Adapters of a lower rank are padded with zero rows of A and columns of B. */
+typedef struct moefp4_linear {
+  int64_t T, N, K;
+  int32_t gran_k, out_fmt, adapters, rank;
+} moefp4_linear;
+
+/* Workspace of moe_fp4_project. */
+moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* bytes);
+
+/* x [T, K] bfloat16, w [N, K/2], w_sf [N, K/gran], w_gs [1] float32 or NULL,
+ * lora_a [adapters, rank, K] and lora_b [adapters, N, rank] bfloat16, id [T]
+ * int32, scale [adapters] float32, all device memory; x, w, w_sf, lora_a,
+ * lora_b and out 16-byte aligned, the workspace 256-byte aligned.  K a
+ * multiple of 256 and N of 16, rank a multiple of 8 up to 128 (K and rank
+ * multiples of 32 and 8 EINVAL otherwise, the rest EUNSUPPORTED); T < 2^24 and
+ * N*K, T*N/16 and adapters*N*rank below 2^32 (EUNSUPPORTED otherwise).
+ * Enqueued on `stream`. */
+moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8_t* w, const uint8_t* w_sf,
+                              const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
+                              const float* scale, void* out, void* workspace, size_t ws_bytes, hipStream_t stream);
+
 /* Reorder group32 weights (RAW layout, UE8M0 scales) into the GEMM layout
  * of the prefill kernels.  which = 0: w13 (N = 2I rows in w13_order, K =
  * H); which = 1: w2 (N = H, K = I).  The GEMM's weight rows are taken in

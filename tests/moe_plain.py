@@ -57,3 +57,21 @@ def layer(x, ids, wts, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran, order, hrel)
         # the weights' own error (tests/test_gpu_gate.py) and the sums over experts
         bound[t] += np.abs(wj) * (dy + 1024 * U32 * np.abs(y))
     return out, bound
+
+
+def project(x, w, w_sf, w_gs, gran, a=None, b=None, ids=None, scale=None):
+    """(y, bound) [T, N]: W x + s B (A x), and how far a kernel may be from it that sums in FP32 in any order, keeps
+    x to 2^-39 of its row's maximum and A x to 17 bits."""
+    W = weight(w, w_sf, None if w_gs is None else w_gs[0], gran)
+    K = x.shape[1]
+    y, ya = x @ W.T, np.abs(x) @ np.abs(W).T
+    bound = (K + 16) * U32 * ya + 2.0 ** -38 * np.max(np.abs(x), axis=1, keepdims=True) * np.abs(W).sum(1)[None, :]
+    if a is not None:
+        L, R = a.shape[:2]
+        for l in range(L):
+            t = np.nonzero(ids == l)[0]
+            u, ua = scale[l] * (x[t] @ a[l].T), np.abs(scale[l]) * (np.abs(x[t]) @ np.abs(a[l]).T)
+            du = (K + 16) * U32 * ua + 2.0 ** -17 * np.abs(u)
+            y[t] += u @ b[l].T
+            bound[t] += du @ np.abs(b[l]).T + (R + 16) * U32 * (np.abs(u) @ np.abs(b[l]).T)
+    return y, bound + 8 * U32 * np.abs(y)
