@@ -25,6 +25,7 @@ Functions mirror the C entry points:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
@@ -43,6 +44,9 @@ OUT_BF16, OUT_F32 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GATE_W_BF16, GATE_W_F32 = 0, 1
 W_RAW, W_GEMM = 0, 1
+_LAYOUTS = {"raw": W_RAW, "gemm": W_GEMM}
+_LAYER_ACT = {False: ACT_BF16, None: ACT_BF16, True: ACT_BF16_QUANT_FP8_K32, "fp8": ACT_BF16_QUANT_FP8_K32,
+              "fp4": ACT_BF16_QUANT_FP4_K32}
 
 
 class Problem(ctypes.Structure):
@@ -163,21 +167,33 @@ def _dev(t, name, dtypes):
     return t
 
 
+# gate / layer / project are called for single tokens, where the host's work
+# per call shows: one test per tensor argument, workspace sizes remembered per
+# problem, raw addresses handed to ctypes.
+
+
 def _arg(t, name, dtypes, shape, device):
-    """A tensor argument of gate / layer / project: _dev's checks, its shape, and its device, which must be the
-    first argument's and the current one (the library launches on the current device)."""
+    """A tensor argument of gate / layer / project: its type, shape, layout and device, which must be the first
+    argument's and the current one (the library launches on the current device).  Returns its address."""
     if t is None:
         return None
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev(t, name, dtypes)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _current(t):
+def _first(t, name, dtypes, dims):
+    """The argument the others are measured by: its type, number of dimensions, layout and (the current) device."""
     import torch
+    _dev(t, name, dtypes)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return t.device
@@ -200,6 +216,34 @@ def _scratch(workspace, need, device, stream):
     if workspace.device != device:
         raise ValueError(f"workspace is on {workspace.device}, expected {device}")
     return workspace
+
+
+def _raw_stream(stream, device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _need(fn, *args):
+    n = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _gate_need(top_k, shared, scoring, w_fmt, T, E, H):
+    return _need(lib().moe_fp4_gate_workspace_bytes, ctypes.byref(make_gate(top_k, scoring, False, 1.0, shared, w_fmt)),
+                 T, E, H)
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_need(device, top_k, shared, scoring, w_fmt, *problem):
+    g = make_gate(top_k, scoring, False, 1.0, shared, w_fmt)
+    return _need(lib().moe_fp4_layer_workspace_bytes, ctypes.byref(Problem(*problem)), ctypes.byref(g))
+
+
+@functools.lru_cache(maxsize=1024)
+def _project_need(*linear):
+    return _need(lib().moe_fp4_project_workspace_bytes, ctypes.byref(Linear(*linear)))
 
 
 def _order(w13_order):
@@ -248,17 +292,14 @@ def make_gate(top_k, scoring="softmax", renormalize=False, scale=1.0, shared=0, 
 
 
 def _router_args(x, gate_w, bias):
-    """(T, E, H, w_fmt, device) of a router's tensors, checked."""
+    """(T, E, H, w_fmt, device, addresses) of a router's tensors, checked."""
     import torch
-    _dev(x, "x", (torch.bfloat16,))
-    _dev(gate_w, "gate_w", (torch.bfloat16, torch.float32))
-    if x.dim() != 2 or gate_w.dim() != 2:
-        raise ValueError("x must be [T, H] and gate_w [E, H]")
-    dev = _current(x)
-    (T, H), E = x.shape, gate_w.shape[0]
-    _arg(gate_w, "gate_w", (torch.bfloat16, torch.float32), (E, H), dev)
-    _arg(bias, "bias", (torch.float32,), (E,), dev)
-    return T, E, H, GATE_W_F32 if gate_w.dtype == torch.float32 else GATE_W_BF16, dev
+    dev = _first(x, "x", (torch.bfloat16,), 2)
+    wt = (torch.bfloat16, torch.float32)
+    _dev(gate_w, "gate_w", wt)
+    (T, H), E = x.shape, len(gate_w)
+    at = x.data_ptr(), _arg(gate_w, "gate_w", wt, (E, H), dev), _arg(bias, "bias", (torch.float32,), (E,), dev)
+    return T, E, H, GATE_W_F32 if gate_w.dtype is torch.float32 else GATE_W_BF16, dev, at
 
 
 def gate(x, gate_w, top_k, bias=None, scoring="softmax", renormalize=False, scale=1.0, shared=0, topk_ids=None,
@@ -271,20 +312,18 @@ def gate(x, gate_w, top_k, bias=None, scoring="softmax", renormalize=False, scal
     E, E + 1, ... with weight 1.  Places without an expert (everything masked,
     or logits that are not finite) hold id -1 and weight 0."""
     import torch
-    T, E, H, w_fmt, dev = _router_args(x, gate_w, bias)
+    T, E, H, w_fmt, dev, at = _router_args(x, gate_w, bias)
     g = make_gate(top_k, scoring, renormalize, scale, shared, w_fmt)
-    need = ctypes.c_size_t(0)
-    _check(lib().moe_fp4_gate_workspace_bytes(ctypes.byref(g), T, E, H, ctypes.byref(need)))
+    need = _gate_need(top_k, shared, scoring, w_fmt, T, E, H)
     shape = (T, top_k + shared)
     if topk_ids is None:
         topk_ids = _empty(shape, torch.int32, dev, stream)
     if topk_w is None:
         topk_w = _empty(shape, torch.float32, dev, stream)
-    _arg(topk_ids, "topk_ids", (torch.int32,), shape, dev)
-    _arg(topk_w, "topk_w", (torch.float32,), shape, dev)
-    ws = _scratch(workspace, need.value, dev, stream)
-    _check(lib().moe_fp4_gate(ctypes.byref(g), T, E, H, _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(topk_ids),
-                              _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+    ws = _scratch(workspace, need, dev, stream)
+    _check(_lib.moe_fp4_gate(ctypes.byref(g), T, E, H, *at, _arg(topk_ids, "topk_ids", (torch.int32,), shape, dev),
+                             _arg(topk_w, "topk_w", (torch.float32,), shape, dev), ws.data_ptr(), ws.numel(),
+                             _raw_stream(stream, dev)))
     return topk_ids, topk_w
 
 
@@ -411,44 +450,35 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
     [T, top_k + shared]: optional outputs for the selection.  Returns out
     [T, H]."""
     import torch
-    T, routed, H, w_fmt, dev = _router_args(x, gate_w, bias)
-    quant = {False: ACT_BF16, None: ACT_BF16, True: ACT_BF16_QUANT_FP8_K32, "fp8": ACT_BF16_QUANT_FP8_K32,
-             "fp4": ACT_BF16_QUANT_FP4_K32}.get(quantize_x)
-    if quant is None:
+    T, routed, H, w_fmt, dev, at = _router_args(x, gate_w, bias)
+    act = _LAYER_ACT.get(quantize_x)
+    if act is None:
         raise ValueError(f"quantize_x must be False, True, 'fp8' or 'fp4', got {quantize_x!r}")
     if gran_k not in (16, 32):
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
     u8, f32 = (torch.uint8,), (torch.float32,)
-    E = routed + shared
+    E, kt = routed + shared, top_k + shared
     _dev(w13, "w13", u8)
-    if w13.dim() != 3:
-        raise ValueError("w13 must be [E, 2I, H/2]")
-    I = w13.shape[1] // 2
-    _arg(w13, "w13", u8, (E, 2 * I, H // 2), dev)
-    _arg(w13_sf, "w13_sf", u8, (E, 2 * I, H // gran_k), dev)
-    _arg(w2, "w2", u8, (E, H, I // 2), dev)
-    _arg(w2_sf, "w2_sf", u8, (E, H, I // gran_k), dev)
-    _arg(w13_gs, "w13_gs", f32, (E,), dev)
-    _arg(w2_gs, "w2_gs", f32, (E,), dev)
+    I = w13.shape[1] // 2 if w13.dim() == 3 else 0
+    weights = (_arg(w13, "w13", u8, (E, 2 * I, H // 2), dev), _arg(w13_sf, "w13_sf", u8, (E, 2 * I, H // gran_k), dev),
+               _arg(w13_gs, "w13_gs", f32, (E,), dev), _arg(w2, "w2", u8, (E, H, I // 2), dev),
+               _arg(w2_sf, "w2_sf", u8, (E, H, I // gran_k), dev), _arg(w2_gs, "w2_gs", f32, (E,), dev))
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     g = make_gate(top_k, scoring, renormalize, scale, shared, w_fmt)
-    p = make_problem(T, E, top_k + shared, H, I, gran_k, quant, w13_order,
-                     OUT_F32 if out_dtype == torch.float32 else OUT_BF16, w_layout)
-    need = ctypes.c_size_t(0)
-    _check(lib().moe_fp4_layer_workspace_bytes(ctypes.byref(p), ctypes.byref(g), ctypes.byref(need)))
+    problem = (T, E, kt, H, I, gran_k, act, _order(w13_order), OUT_F32 if out_dtype is torch.float32 else OUT_BF16,
+               _LAYOUTS.get(w_layout, w_layout))
+    need = _layer_need(dev, top_k, shared, scoring, w_fmt, *problem)
     if out is None:
         out = _empty((T, H), out_dtype, dev, stream)
-    else:
-        _arg(out, "out", (out_dtype,), (T, H), dev)
-    _arg(topk_ids, "topk_ids", (torch.int32,), (T, top_k + shared), dev)
-    _arg(topk_w, "topk_w", f32, (T, top_k + shared), dev)
-    ws = _scratch(workspace, need.value, dev, stream)
-    _check(lib().moe_fp4_layer(ctypes.byref(p), ctypes.byref(g), _ptr(x), _ptr(gate_w), _ptr(bias), _ptr(w13),
-                               _ptr(w13_sf), _ptr(w13_gs), _ptr(w2), _ptr(w2_sf), _ptr(w2_gs), _ptr(out),
-                               _ptr(topk_ids), _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+    ws = _scratch(workspace, need, dev, stream)
+    _check(_lib.moe_fp4_layer(ctypes.byref(Problem(*problem)), ctypes.byref(g), *at, *weights,
+                              _arg(out, "out", (out_dtype,), (T, H), dev),
+                              _arg(topk_ids, "topk_ids", (torch.int32,), (T, kt), dev),
+                              _arg(topk_w, "topk_w", f32, (T, kt), dev), ws.data_ptr(), ws.numel(),
+                              _raw_stream(stream, dev)))
     return out
 
 
@@ -462,44 +492,38 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     None.  Returns out [T, N] bfloat16 (default) or float32."""
     import torch
     u8, f32, bf = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
-    _dev(x, "x", bf)
+    dev = _first(x, "x", bf, 2)
     _dev(w, "w", u8)
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("x must be [T, K] and w [N, K/2]")
     if gran_k not in (16, 32):
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
-    dev = _current(x)
-    (T, K), N = x.shape, w.shape[0]
-    _arg(w, "w", u8, (N, K // 2), dev)
-    _arg(w_sf, "w_sf", u8, (N, K // gran_k), dev)
-    _arg(w_gs, "w_gs", f32, (1,), dev)
-    lora = (lora_a, lora_b, lora_id, lora_scale)
-    if any(t is None for t in lora) and any(t is not None for t in lora):
-        raise ValueError("lora_a, lora_b, lora_id and lora_scale go together")
+    (T, K), N = x.shape, len(w)
+    at = (x.data_ptr(), _arg(w, "w", u8, (N, K // 2), dev), _arg(w_sf, "w_sf", u8, (N, K // gran_k), dev),
+          _arg(w_gs, "w_gs", f32, (1,), dev))
     adapters = rank = 0
+    lora = (None, None, None, None)
     if lora_a is not None:
+        if lora_b is None or lora_id is None or lora_scale is None:
+            raise ValueError("lora_a, lora_b, lora_id and lora_scale go together")
         _dev(lora_a, "lora_a", bf)
-        if lora_a.dim() != 3 or lora_a.shape[0] < 1:
+        if lora_a.dim() != 3 or len(lora_a) < 1:
             raise ValueError("lora_a must be [L, R, K] with L >= 1")
         adapters, rank = lora_a.shape[:2]
-        _arg(lora_a, "lora_a", bf, (adapters, rank, K), dev)
-        _arg(lora_b, "lora_b", bf, (adapters, N, rank), dev)
-        _arg(lora_id, "lora_id", (torch.int32,), (T,), dev)
-        _arg(lora_scale, "lora_scale", f32, (adapters,), dev)
+        lora = (_arg(lora_a, "lora_a", bf, (adapters, rank, K), dev), _arg(lora_b, "lora_b", bf, (adapters, N, rank), dev),
+                _arg(lora_id, "lora_id", (torch.int32,), (T,), dev),
+                _arg(lora_scale, "lora_scale", f32, (adapters,), dev))
+    elif lora_b is not None or lora_id is not None or lora_scale is not None:
+        raise ValueError("lora_a, lora_b, lora_id and lora_scale go together")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-    p = Linear(T, N, K, gran_k, OUT_F32 if out_dtype == torch.float32 else OUT_BF16, adapters, rank)
-    need = ctypes.c_size_t(0)
-    _check(lib().moe_fp4_project_workspace_bytes(ctypes.byref(p), ctypes.byref(need)))
+    linear = (T, N, K, gran_k, OUT_F32 if out_dtype is torch.float32 else OUT_BF16, adapters, rank)
+    need = _project_need(*linear)
     if out is None:
         out = _empty((T, N), out_dtype, dev, stream)
-    else:
-        _arg(out, "out", (out_dtype,), (T, N), dev)
-    ws = _scratch(workspace, need.value, dev, stream)
-    _check(lib().moe_fp4_project(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(w_sf), _ptr(w_gs), _ptr(lora_a), _ptr(lora_b),
-                                 _ptr(lora_id), _ptr(lora_scale), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    ws = _scratch(workspace, need, dev, stream)
+    _check(_lib.moe_fp4_project(ctypes.byref(Linear(*linear)), *at, *lora, _arg(out, "out", (out_dtype,), (T, N), dev),
+                                ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return out
 
 
