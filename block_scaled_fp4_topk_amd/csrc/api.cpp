@@ -461,7 +461,10 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
 }
 
 struct ProjectPlan {
-  size_t x16, xs, u, total;
+  size_t x16, xs, u, part, total;
+  bool group;  // u by matrix instructions
+  size_t counts, offsets, sorted, slot_of, tiles, ntiles, flags, hist;
+  int chunk, chunks, ku;
 };
 
 moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
@@ -474,6 +477,8 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
   if (p->adapters < 0) return fail(MOEFP4_EINVAL, "adapters must be >= 0, got %d", p->adapters);
   if (p->adapters > 0 && (p->rank <= 0 || p->rank % 8))
     return fail(MOEFP4_EINVAL, "rank must be a positive multiple of 8, got %d", p->rank);
+  if (p->adapters > moefp4::kMaxExperts)
+    return fail(MOEFP4_EUNSUPPORTED, "adapters must be at most %d, got %d", moefp4::kMaxExperts, p->adapters);
   if (p->adapters > 0 && p->rank > 128) return fail(MOEFP4_EUNSUPPORTED, "rank must be at most 128, got %d", p->rank);
   if (p->K % 256 || p->N % 16)
     return fail(MOEFP4_EUNSUPPORTED, "K must be a multiple of 256 and N of 16, got K=%lld N=%lld", (long long)p->K,
@@ -486,13 +491,34 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
                 "T must be below 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38, got T=%lld N=%lld K=%lld",
                 (long long)p->T, (long long)p->N, (long long)p->K);
   // (few tokens: rows for whole groups of 16, as many as the launch multiplies)
-  const size_t T = (size_t)p->T, Tg = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  const size_t T = (size_t)p->T, Tg = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
   const bool few = p->T <= moefp4::kProjectFew;
   P->x16 = take(few ? Tg * p->K * 2 : p->gran_k == 16 ? T * p->K * 2 : 0);
   P->xs = take(p->gran_k == 16 ? T * 4 : 0);
-  P->u = take(p->adapters > 0 ? T * p->rank * 4 : 0);
+  P->ku = p->adapters > 0 ? moefp4::project_u_parts(p->T, p->K, p->rank) : 1;
+  P->u = take(p->adapters > 0 ? P->ku * T * p->rank * 4 : 0);
+  const int parts = few || T == 0 ? 1 : moefp4::project_gemm_plan(p->T, p->N, p->K).parts;
+  P->part = take(parts > 1 ? (size_t)parts * T * p->N * 4 : 0);
+  P->group = p->adapters > 0 && !moefp4::project_dot(p->T, p->K, p->rank);
+  P->chunk = P->chunks = 0;
+  if (P->group) {
+    const size_t L = p->adapters;
+    // (one workgroup takes 21 us to group 8192 tokens)
+    if (p->T > 2048) {
+      P->chunk = p->T > moefp4::kRouteSingleMax ? moefp4::route_chunk(p->T) : 1024;
+      P->chunks = (int)((p->T + P->chunk - 1) / P->chunk);
+    }
+    P->counts = take(L * 4);
+    P->offsets = take((L + 1) * 4);
+    P->sorted = take(T * 4);
+    P->slot_of = take(T * 4);
+    P->tiles = take((T / 32 + L) * 8);
+    P->ntiles = take(4);
+    P->flags = take(64);
+    P->hist = take((size_t)P->chunks * (L + 1) * 4);
+  }
   P->total = o;
   return MOEFP4_OK;
 }
@@ -725,6 +751,20 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
   a.x16 = at<uint16_t>(workspace, P.x16);
   a.xs = at<float>(workspace, P.xs);
   a.u = at<float>(workspace, P.u);
+  a.ku = P.ku;
+  a.part = at<float>(workspace, P.part);
+  if (P.group) {
+    a.route.counts = at<int32_t>(workspace, P.counts);
+    a.route.offsets = at<int32_t>(workspace, P.offsets);
+    a.route.sorted_assign = at<int32_t>(workspace, P.sorted);
+    a.route.slot_of = at<int32_t>(workspace, P.slot_of);
+    a.route.tiles = at<int32_t>(workspace, P.tiles);
+    a.route.ntiles = at<int32_t>(workspace, P.ntiles);
+    a.route.flags = at<int32_t>(workspace, P.flags);
+    a.route.nchunks = P.chunks;
+    a.route.chunk = P.chunk;
+    a.route.hist = P.chunks ? at<int32_t>(workspace, P.hist) : nullptr;
+  }
   st = hip_status(moefp4::launch_project(a, stream), "project");
   return st == MOEFP4_OK ? ok() : st;
 }

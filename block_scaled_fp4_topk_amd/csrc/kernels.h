@@ -133,8 +133,13 @@ int cu_count();
 
 // The projection with adapters (project.hip).  K % 256 == 0, N % 16 == 0, R a
 // multiple of 8 up to 128, N * K < 2^32, T < 2^24.
-constexpr int kProjectFew = 64;   // most tokens of the form for few tokens
-constexpr int kProjectDot = 256;  // most tokens whose u is computed by dot products
+// Most tokens of the form for few tokens; beyond, the tiled product.  Both at
+// N = 4096, K = 6144, group16 without adapters: 64 tokens 14.8 us against 23.4
+// us, 128 tokens 23.7 against 27.6; N = 1968, K = 2048: 128 tokens 11.7 against
+// 15.2.  (256 tokens in the few form: 117 us against 35.)
+constexpr int kProjectFew = 128;
+// u by dot products (every token reads its adapter's A for itself)?
+inline bool project_dot(long long T, long long K, long long R) { return T <= 64 || T * K * R <= (120ll << 20); }
 struct ProjectArgs {
   int T, N, K, L, R;   // L = 0: no adapters
   bool g16, out_f32;
@@ -148,8 +153,19 @@ struct ProjectArgs {
   // workspace
   uint16_t* x16;  // x as the products read it (fp16 * 2**-p for group16)
   float* xs;      // group16: 2**p [T]
-  float* u;       // [T, R]
+  float* u;       // [ku][T, R]
+  int ku;
+  float* part;    // [parts][T, N] of the tiled product
+  RouteOut route; // u by matrix instructions: tokens grouped by adapter, tiles of 32
 };
+// The tiled product: tokens per workgroup, parts of K and their 64-element
+// stages.
+struct ProjectGemm {
+  int tt, per, parts;
+};
+// parts of K in which u is computed
+int project_u_parts(long long T, long long K, long long R);
+ProjectGemm project_gemm_plan(long long T, long long N, long long K);
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
 
 struct FcArgs {

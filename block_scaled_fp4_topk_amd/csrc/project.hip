@@ -6,8 +6,9 @@
 //     activations u = s_l A_l x (one workgroup per token and 4 ranks).
 //     group16 weights multiply in fp16, x as fp16 * 2**-p (exact down to 2**-24
 //     of the row's maximum); group32 weights in bfloat16, x as it is.
-//     (More tokens: project_shrink computes u with matrix instructions.)
-//  2. up to 64 tokens, project_few: the FP4 stream bounds it (an N x K matrix
+//     (More tokens: grouped by adapter as the router groups by expert, and
+//     project_shrink computes u with matrix instructions.)
+//  2. up to 128 tokens, project_few: the FP4 stream bounds it (an N x K matrix
 //     is read once for N K / 2 bytes).  A workgroup owns 16 output rows, its 8
 //     waves an eighth of K each; the weights come as whole 128-byte lines into
 //     registers, all requested before the first is used.
@@ -28,6 +29,18 @@ namespace moefp4 {
 namespace {
 
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// Eight bfloat16 values times eight floats.
+__device__ __forceinline__ float dot8(const uint4& v, const v4f& a, const v4f& b) {
+  float s = u2f(v.x << 16) * a[0];
+  s = __builtin_fmaf(u2f(v.x & 0xFFFF0000u), a[1], s);
+  s = __builtin_fmaf(u2f(v.y << 16), a[2], s);
+  s = __builtin_fmaf(u2f(v.y & 0xFFFF0000u), a[3], s);
+  s = __builtin_fmaf(u2f(v.z << 16), b[0], s);
+  s = __builtin_fmaf(u2f(v.z & 0xFFFF0000u), b[1], s);
+  s = __builtin_fmaf(u2f(v.w << 16), b[2], s);
+  return __builtin_fmaf(u2f(v.w & 0xFFFF0000u), b[3], s);
+}
 
 // ---------------------------------------------------------------------------
 // 1. preparation
@@ -140,57 +153,91 @@ __global__ __launch_bounds__(256) void project_prep_kernel(ProjectArgs a, int pr
   }
 }
 
-// u of many tokens with matrix instructions: 16 tokens per workgroup, K split
-// over its 4 waves, every adapter that occurs among the 16 in turn (runs of one
-// request's tokens: one or two), 16 ranks at a time.
-__global__ __launch_bounds__(256) void project_shrink_kernel(ProjectArgs a) {
-  __shared__ v4f s_part[4][8][64];
+// u of many tokens with matrix instructions: the tokens grouped by adapter (the
+// router's stable grouping), a tile of up to 32 tokens of one adapter per
+// workgroup, K split over its 8 waves and, where there are few tiles, over
+// a.ku workgroups (a CU draws about 30 bytes
+// per ns here, so it takes all of them: 512 tokens, K = 6144, rank 64 39 us by
+// 24 workgroups, 11 us by 192); NT: tiles of 16 ranks.
+template <int NT>
+__global__ __launch_bounds__(512, NT >= 8 ? 2 : 4) void project_shrink_kernel(ProjectArgs a) {
+  __shared__ v4f s_part[4][NT][2][64];
+  if ((int)blockIdx.x >= a.route.ntiles[0]) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K, R = a.R;
-  const int t = blockIdx.x * 16 + r16;
-  const int tc = t < a.T ? t : a.T - 1;
-  const int id = t < a.T ? a.id[t] : -1;
-  uint64_t left = __ballot((unsigned)id < (unsigned)a.L && q == 0);
-  const uint16_t* xr = a.x + (size_t)tc * K + 8 * q;
-  const int k0 = wave * (K >> 2), k1 = k0 + (K >> 2);  // (K is a multiple of 256)
-  const int nt = (R + 15) >> 4;
-  while (left) {
-    const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    left &= ~__ballot(id == l);
-    v4f acc[8];
+  const int l = a.route.tiles[2 * blockIdx.x], m0 = a.route.tiles[2 * blockIdx.x + 1];
+  const int ne = a.route.counts[l], oe = a.route.offsets[l];
+  int tok[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* A = a.a + (size_t)l * R * K + 8 * q;
-    for (int k = k0; k < k1; k += 64) {
-      v8bf B[2];
+  for (int g = 0; g < 2; ++g) {
+    const int m = m0 + 16 * g + r16;
+    tok[g] = a.route.sorted_assign[oe + (m < ne ? m : m0)];  // (rows past the last: not stored)
+  }
+  const uint16_t* A = a.a + (size_t)l * R * K + 8 * q;
+  const uint16_t* xr[2] = {a.x + (size_t)tok[0] * K + 8 * q, a.x + (size_t)tok[1] * K + 8 * q};
+  const int per = K / (8 * a.ku), k0 = (blockIdx.y * 8 + wave) * per;  // (whole steps of 32: ku divides K / 256)
+  const int n = per >> 5;
+  v4f acc[NT][2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) B[s] = *reinterpret_cast<const v8bf*>(xr + k + 32 * s);
+  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* ar[NT];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i < nt) {
-          const int r = min(16 * i + r16, R - 1);  // (ranks past R are not stored)
+  for (int i = 0; i < NT; ++i) ar[i] = A + (size_t)min(16 * i + r16, R - 1) * K;  // (ranks past R: not stored)
+  constexpr int PD = NT >= 8 ? 2 : NT >= 4 ? 3 : 4;  // steps in flight
+  v8bf bx[PD][2], ba[PD][NT];
+  auto load = [&](int s, int slot) __attribute__((always_inline)) {
+    const int k = k0 + 32 * min(s, n - 1);
+    bx[slot][0] = *reinterpret_cast<const v8bf*>(xr[0] + k);
+    bx[slot][1] = *reinterpret_cast<const v8bf*>(xr[1] + k);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const v8bf w = *reinterpret_cast<const v8bf*>(A + (size_t)r * K + k + 32 * s);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, B[s], acc[i], 0, 0, 0);
-          }
+    for (int i = 0; i < NT; ++i) ba[slot][i] = *reinterpret_cast<const v8bf*>(ar[i] + k);
+  };
+#pragma unroll
+  for (int s = 0; s < PD; ++s) load(s, s);
+  for (int s = 0; s < n; s += PD) {
+#pragma unroll
+    for (int p = 0; p < PD; ++p) {
+      if (s + p < n) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ba[p][i], bx[p][0], acc[i][0], 0, 0, 0);
+          acc[i][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ba[p][i], bx[p][1], acc[i][1], 0, 0, 0);
         }
       }
+      load(s + p + PD, p);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < nt) s_part[wave][i][lane] = acc[i];
-    __syncthreads();
-    // lane: ranks 16 i + 4 q .. + 3, token r16; the waves share the rank tiles
-    for (int i = wave; i < nt; i += 4) {
-      const v4f s = (s_part[0][i][lane] + s_part[1][i][lane]) + (s_part[2][i][lane] + s_part[3][i][lane]);
-      const int r = 16 * i + 4 * q;
-      if (id == l && r < R)
-        *reinterpret_cast<v4f*>(a.u + (size_t)t * R + r) = s * a.scale[l];
-    }
-    __syncthreads();
   }
+  // the waves' parts: 4 .. 7 hand theirs to 0 .. 3, whose sums meet in LDS
+  if (wave >= 4) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s_part[wave - 4][i][0][lane] = acc[i][0], s_part[wave - 4][i][1][lane] = acc[i][1];
+  }
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) s_part[wave][i][g][lane] = acc[i][g] + s_part[wave][i][g][lane];
+  }
+  __syncthreads();
+  // lane: ranks 16 i + 4 q .. + 3, token r16 of group g
+  const float sl = a.scale[l];
+  for (int j = wave; j < 2 * NT; j += 8) {
+    const int i = j >> 1, g = j & 1;
+    const v4f v = (s_part[0][i][g][lane] + s_part[1][i][g][lane]) + (s_part[2][i][g][lane] + s_part[3][i][g][lane]);
+    const int r = 16 * i + 4 * q;
+    if (m0 + 16 * g + r16 < ne && r < R) *reinterpret_cast<v4f*>(a.u + ((size_t)blockIdx.y * a.T + tok[g]) * R + r) = v * sl;
+  }
+}
+
+// u = the sum of its parts, in order (parts 1 .. ku - 1 added to the first).
+__global__ __launch_bounds__(256) void project_u_sum_kernel(ProjectArgs a) {
+  const long long n = (long long)a.T * a.R, i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  v4f s = *reinterpret_cast<const v4f*>(a.u + i);
+  for (int z = 1; z < a.ku; ++z) s += *reinterpret_cast<const v4f*>(a.u + z * n + i);
+  *reinterpret_cast<v4f*>(a.u + i) = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -206,7 +253,8 @@ struct WTile {
 // NG: 16-token groups; NC: chunks of K in flight per wave.
 template <int MODE, int NG, int NC>
 __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
-  __shared__ float4 s_red[8][NG][64];
+  constexpr int GP = NG < 4 ? NG : 4;  // groups summed over the waves at a time
+  __shared__ float4 s_red[8][GP][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[8][2048];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -230,13 +278,12 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
 #pragma unroll
   for (int i = 0; i < NC; ++i) load(wave + 8 * i, w[i]);
 
-  // the adapters' part of output (row rn, token rt + 32 p), while the weights come
+  // the adapters' part of output (row rn, token rt + 32 p): for few groups
+  // while the weights come, else behind the products
   const int rn = tid & 15, rt = tid >> 4;
   constexpr int NP = (NG + 1) / 2;
-  float lora[NP];
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    lora[p] = 0.0f;
+  auto adapted = [&](int p) __attribute__((always_inline)) {
+    float s = 0.0f;
     const int t = rt + 32 * p;
     if (a.L > 0 && t < a.T) {
       const int l = a.id[t];
@@ -244,22 +291,16 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
         const uint16_t* B = a.b + ((size_t)l * a.N + n0 + rn) * a.R;
         const float* u = a.u + (size_t)t * a.R;
         for (int r = 0; r < a.R; r += 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(B + r);
-          const float4 ua = *reinterpret_cast<const float4*>(u + r), ub = *reinterpret_cast<const float4*>(u + r + 4);
-          float s = lora[p];
-          s = __builtin_fmaf(u2f(v.x << 16), ua.x, s);
-          s = __builtin_fmaf(u2f(v.x & 0xFFFF0000u), ua.y, s);
-          s = __builtin_fmaf(u2f(v.y << 16), ua.z, s);
-          s = __builtin_fmaf(u2f(v.y & 0xFFFF0000u), ua.w, s);
-          s = __builtin_fmaf(u2f(v.z << 16), ub.x, s);
-          s = __builtin_fmaf(u2f(v.z & 0xFFFF0000u), ub.y, s);
-          s = __builtin_fmaf(u2f(v.w << 16), ub.z, s);
-          s = __builtin_fmaf(u2f(v.w & 0xFFFF0000u), ub.w, s);
-          lora[p] = s;
+          s += dot8(*reinterpret_cast<const uint4*>(B + r), *reinterpret_cast<const v4f*>(u + r),
+                    *reinterpret_cast<const v4f*>(u + r + 4));
         }
       }
     }
-  }
+    return s;
+  };
+  float lora[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) lora[p] = NG <= 4 ? adapted(p) : 0.0f;
 
   v4f acc[NG];
 #pragma unroll
@@ -269,6 +310,13 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
   const uint32_t tw0 = wr * 128 + 16 * (seg ^ (wr >> 1)), tw1 = (wr + 8) * 128 + 16 * (seg ^ ((wr + 8) >> 1));
   const uint32_t tr0 = r16 * 128 + 16 * ((2 * q) ^ (r16 >> 1)), tr1 = r16 * 128 + 16 * ((2 * q + 1) ^ (r16 >> 1));
   const u32x4* xf = reinterpret_cast<const u32x4*>(a.x16) + lane;
+  u32x4 x_ahead[2][8];
+  auto load_x = [&](int g, int c, u32x4 (&b)[8]) __attribute__((always_inline)) {
+    const u32x4* xc = xf + ((size_t)g * nch + min(c, nch - 1)) * 512;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = xc[64 * j];
+  };
+  load_x(0, wave, x_ahead[0]);
   for (int c0 = 0; c0 < nch; c0 += 8 * NC) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -296,111 +344,240 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const u32x4* xc = xf + ((size_t)g * nch + c) * 512;
+          u32x4 (&xb)[8] = x_ahead[(i * NG + g) & 1];
+          // the next group's (or chunk's) x, while this one multiplies
+          if (g + 1 < NG) load_x(g + 1, c, x_ahead[(i * NG + g + 1) & 1]);
+          else load_x(0, i + 1 < NC ? c + 8 : c0 + 8 * NC + wave, x_ahead[(i * NG + g + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const u32x4 b = xc[64 * j];
             if constexpr (MODE == 0)
-              acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, A[j]), __builtin_bit_cast(v8h, b),
-                                                              acc[g], 0, 0, 0);
+              acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, A[j]),
+                                                              __builtin_bit_cast(v8h, xb[j]), acc[g], 0, 0, 0);
             else
               acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, A[j]),
-                                                               __builtin_bit_cast(v8bf, b), acc[g], 0, 0, 0);
+                                                               __builtin_bit_cast(v8bf, xb[j]), acc[g], 0, 0, 0);
           }
         }
       }
       if (c0 + 8 * NC < nch) load(c + 8 * NC, w[i]);
     }
-  }
+    if constexpr ((NC * NG) & 1) {  // the two buffers change places
 #pragma unroll
-  for (int g = 0; g < NG; ++g) s_red[wave][g][lane] = float4{acc[g][0], acc[g][1], acc[g][2], acc[g][3]};
-  __syncthreads();
+      for (int j = 0; j < 8; ++j) x_ahead[0][j] = x_ahead[1][j];
+    }
+  }
   const float gs = a.w_gs ? a.w_gs[0] : 1.0f;
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int t = rt + 32 * p;
-    if (t >= a.T) continue;
-    float s = 0.0f;
+  for (int g0 = 0; g0 < NG; g0 += GP) {
+    if (g0 > 0) __syncthreads();  // (the groups before are summed)
 #pragma unroll
-    for (int v = 0; v < 8; ++v)
-      s += reinterpret_cast<const float*>(&s_red[v][t >> 4][(t & 15) + 16 * (rn >> 2)])[rn & 3];
-    s = __builtin_fmaf(s, gs * (MODE == 0 ? a.xs[t] : 1.0f), lora[p]);
-    const size_t at = (size_t)t * a.N + n0 + rn;
-    if (a.out_f32) static_cast<float*>(a.out)[at] = s;
-    else static_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16_bits(s);
+    for (int g = 0; g < GP; ++g) s_red[wave][g][lane] = float4{acc[g0 + g][0], acc[g0 + g][1], acc[g0 + g][2], acc[g0 + g][3]};
+    __syncthreads();
+#pragma unroll
+    for (int p = g0 / 2; p < (g0 + GP + 1) / 2; ++p) {
+      const int t = rt + 32 * p;
+      if (t >= a.T) continue;
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        s += reinterpret_cast<const float*>(&s_red[v][(t >> 4) - g0][(t & 15) + 16 * (rn >> 2)])[rn & 3];
+      s = __builtin_fmaf(s, gs * (MODE == 0 ? a.xs[t] : 1.0f), NG <= 4 ? lora[p] : adapted(p));
+      const size_t at = (size_t)t * a.N + n0 + rn;
+      if (a.out_f32) static_cast<float*>(a.out)[at] = s;
+      else static_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16_bits(s);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // 2b. many tokens
 
-constexpr int kTile = 128;  // weight rows and tokens per workgroup
+constexpr int kTile = 128;  // weight rows per workgroup
 constexpr int kGK = 64;     // K elements per stage
 
 // LDS rows of 128 bytes; 16-byte segment s of row r sits at s ^ ((r >> 1) & 7),
 // so that the 16 rows a lane group reads touch all 64 banks.
 __device__ __forceinline__ int pswz(int r) { return (r >> 1) & 7; }
 
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int row_tiles) {
-  // x and the decoded weights of a stage, two stages
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[kTile * 128], s_x1[kTile * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t s_w[2][kTile * 128];
+// One wave's 16 NJ tokens from t0 on x 16 NI rows from n0 on (lane: token r16 of
+// each 16, rows 4 q .. + 3 of each 16): the adapters that occur among the
+// tokens added, one after the other, and the result stored.  u enters as two
+// bfloat16 parts; a token takes its own adapter's product and nothing of the
+// others'.
+template <int NI, int NJ>
+__device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[NI][NJ], int t0, int n0) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4, N = a.N;
+  if (a.L > 0) {
+    int id[NJ];
+    uint64_t left[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int t = t0 + 16 * j + r16;
+      id[j] = t < a.T ? a.id[t] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) left[j] = __ballot((unsigned)id[j] < (unsigned)a.L && q == 0);
+    for (;;) {
+      int l = -1;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (l < 0 && left[j]) l = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
+      if (l < 0) break;
+      bool some[NJ];
+      v4f add[NI][NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint64_t mine = __ballot(id[j] == l);
+        some[j] = mine != 0;
+        left[j] &= ~mine;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) add[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+      for (int r0 = 0; r0 < a.R; r0 += 32) {
+        const int r = r0 + 8 * q;
+        v8bf B[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int n = min(n0 + 16 * i + r16, N - 1);
+          B[i] = v8bf{};
+          if (r < a.R) B[i] = *reinterpret_cast<const v8bf*>(a.b + ((size_t)l * N + n) * a.R + r);
+        }
+        v4f u[NJ][2];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          u[j][0] = u[j][1] = v4f{0.f, 0.f, 0.f, 0.f};
+          if (id[j] == l && r < a.R) {
+            const float* p = a.u + (size_t)(t0 + 16 * j + r16) * a.R + r;
+            u[j][0] = *reinterpret_cast<const v4f*>(p);
+            u[j][1] = *reinterpret_cast<const v4f*>(p + 4);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if (!some[j]) continue;
+          v8bf hi, lo;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const float f = u[j][v >> 2][v & 3];
+            hi[v] = (__bf16)f;
+            const float rest = f - (float)hi[v];
+            lo[v] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            add[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[i], lo, add[i][j], 0, 0, 0);
+            add[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[i], hi, add[i][j], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (id[j] == l) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) o[i][j] += add[i][j];
+        }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int t = t0 + 16 * j + r16;
+    if (t >= a.T) continue;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int n = n0 + 16 * i + 4 * q;
+      if (n >= N) continue;  // (N is a multiple of 16)
+      const size_t at = (size_t)t * N + n;
+      const v4f v = o[i][j];
+      if (a.out_f32)
+        *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+            uint2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+    }
+  }
+}
+
+// 16 bytes per lane from memory to consecutive places in LDS.
+__device__ __forceinline__ void direct_load(const uint16_t* src, uint8_t* lds) {
+  __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
+}
+
+// TT: tokens per workgroup, 128 (waves of 64 rows x 64 tokens) or 64 (32 x 64).
+// blockIdx.y: the part of K (stages [y * per, + per)); with more than one part
+// the products go to a.part as float32, which project_sum adds up.
+//
+// Two ways to the next stage.  TT = 64, where few workgroups hide each other's
+// waits: x, codes and scales through registers, two stages ahead, with a
+// barrier that leaves the loads in flight (N = 4096, K = 6144, 256 tokens: 29
+// us against 62 us with direct loads).  TT = 128, where the traffic through LDS
+// and the number of requests count: x by direct loads to LDS one stage ahead,
+// the weights of two stages per load (8192 tokens: 411 us against 446 us).
+template <int MODE, int TT>
+__global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int row_tiles, int per) {
+  constexpr int NI = TT == 128 ? 4 : 2;  // 16-row tiles of a wave
+  constexpr int XD = TT / 32;            // 16-byte pieces of x per thread and stage
+  constexpr bool DIRECT = TT == 128;
+  // (x's two buffers are objects of their own: reads of one do not wait for
+  // direct loads into the other)
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[TT * 128], s_x1[TT * 128], s_w[2][kTile * 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K, N = a.N, T = a.T;
-  const int n0 = (blockIdx.x % row_tiles) * kTile, t0 = (blockIdx.x / row_tiles) * kTile;
-  const int wn = (wave & 1) * 64, wt = (wave >> 1) * 64;
+  const int n0 = (blockIdx.x % row_tiles) * kTile, t0 = (blockIdx.x / row_tiles) * TT;
+  const int wn = TT == 128 ? (wave & 1) * 64 : wave * 32, wt = TT == 128 ? (wave >> 1) * 64 : 0;
   const uint16_t* xsrc = MODE == 0 ? a.x16 : a.x;
+  const int s_begin = blockIdx.y * per, s_end = min(K / kGK, s_begin + per);
 
-  // x rows by direct loads to LDS, eight whole 128-byte rows per instruction
-  // (rows past T repeat the last one: their results are not stored)
-  auto stage_x = [&](int s, uint8_t* lds) __attribute__((always_inline)) {
+  // x: eight whole 128-byte rows per instruction (rows past T repeat the last
+  // one: their results are not stored)
+  const uint16_t* xr[XD];
+  uint32_t xat[XD];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 32 * wave + 8 * i + (lane >> 3);
-      const int t = min(t0 + r, T - 1);
-      const uint16_t* src = xsrc + (size_t)t * K + s * kGK + 8 * ((lane & 7) ^ pswz(r));
-      __builtin_amdgcn_global_load_lds(src, lds + (32 * wave + 8 * i) * 128, 16, 0, 0);
-    }
-  };
-  // weights: thread = (row, half); of every two stages (64 bytes of a row) its
-  // 16 bytes of each stage's 32, and the scales of their K
+  for (int i = 0; i < XD; ++i) {
+    const int r = TT / 4 * wave + 8 * i + (lane >> 3);
+    // (direct loads land in lane order: the swizzle is in what they fetch)
+    xr[i] = xsrc + (size_t)min(t0 + r, T - 1) * K + 8 * (DIRECT ? (lane & 7) ^ pswz(r) : lane & 7);
+    xat[i] = r * 128 + 16 * ((lane & 7) ^ pswz(r));
+  }
+  // weights: thread = (row, half of the stage's 32 bytes), with the scales of its 32 K
   const int wrow = tid >> 1, half = tid & 1;
   const int nrow = min(n0 + wrow, N - 1);
   const uint8_t* wsrc = a.w + (size_t)nrow * (K >> 1) + 16 * half;
-  const uint8_t* ssrc = a.w_sf + (size_t)nrow * (MODE == 0 ? K >> 4 : K >> 5);
-  struct Raw { u32x4 c[2]; uint64_t s; };
-  auto load_w = [&](int s2, Raw& r) __attribute__((always_inline)) {  // stages 2 s2, 2 s2 + 1
-    r.c[0] = *reinterpret_cast<const u32x4*>(wsrc + s2 * 64);
-    r.c[1] = *reinterpret_cast<const u32x4*>(wsrc + s2 * 64 + 32);
-    if (MODE == 0) r.s = *reinterpret_cast<const uint64_t*>(ssrc + s2 * 8);
-    else r.s = *reinterpret_cast<const uint32_t*>(ssrc + s2 * 4);
+  const uint8_t* ssrc = a.w_sf + (size_t)nrow * (MODE == 0 ? K >> 4 : K >> 5) + (MODE == 0 ? 2 * half : half);
+  struct Raw { u32x4 x[DIRECT ? 1 : XD], c; uint32_t s; };
+  auto load = [&](int s, Raw& r) __attribute__((always_inline)) {
+    s = min(s, s_end - 1);  // (past the last stage: loaded again, not used)
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int i = 0; i < XD; ++i) r.x[i] = *reinterpret_cast<const u32x4*>(xr[i] + s * kGK);
+    }
+    r.c = *reinterpret_cast<const u32x4*>(wsrc + s * 32);
+    if (MODE == 0) r.s = *reinterpret_cast<const uint16_t*>(ssrc + s * 4);
+    else r.s = ssrc[s * 2];
   };
-  auto decode = [&](const Raw& r, int par, uint8_t* lds) __attribute__((always_inline)) {
-    const u32x4 c = r.c[par];
-    uint8_t* row = lds + wrow * 128;
+  const uint32_t wat = wrow * 128, wsz = pswz(wrow);
+  auto store = [&](const Raw& r, int buf) __attribute__((always_inline)) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>((buf ? s_x1 : s_x0) + xat[i]) = r.x[i];
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       u32x4 v;
-      if constexpr (MODE == 0) {
-        // K 32 half + 8 j of the stage: scale byte 4 par + 2 half + j / 2
-        const uint32_t b = (uint32_t)(r.s >> (8 * (4 * par + 2 * half + (j >> 1)))) & 0xFFu;
-        v = __builtin_bit_cast(u32x4, dq8_f16(c[j], e4m3_to_h2(b)));
-      } else {
-        const uint32_t b = (uint32_t)(r.s >> (8 * (2 * par + half))) & 0xFFu;
-        v = __builtin_bit_cast(u32x4, dq8_bf16(c[j], ue8m0_to_f32(b)));
-      }
-      *reinterpret_cast<u32x4*>(row + 16 * ((4 * half + j) ^ pswz(wrow))) = v;
+      if constexpr (MODE == 0) v = __builtin_bit_cast(u32x4, dq8_f16(r.c[j], e4m3_to_h2((r.s >> (8 * (j >> 1))) & 0xFFu)));
+      else v = __builtin_bit_cast(u32x4, dq8_bf16(r.c[j], ue8m0_to_f32(r.s)));
+      *reinterpret_cast<u32x4*>(s_w[buf] + wat + 16 * ((4 * half + j) ^ wsz)) = v;
     }
   };
 
-  v4f acc[4][4];
+  v4f acc[NI][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const uint8_t* sx, const uint8_t* sw) __attribute__((always_inline)) {
+  auto multiply = [&](int buf) __attribute__((always_inline)) {
+    const uint8_t *sx = buf ? s_x1 : s_x0, *sw = s_w[buf];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       u32x4 B[4];
@@ -410,7 +587,7 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
         B[j] = *reinterpret_cast<const u32x4*>(sx + r * 128 + 16 * ((4 * ks + q) ^ pswz(r)));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int r = wn + 16 * i + r16;
         const u32x4 A = *reinterpret_cast<const u32x4*>(sw + r * 128 + 16 * ((4 * ks + q) ^ pswz(r)));
 #pragma unroll
@@ -426,94 +603,109 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
     }
   };
 
-  const int n2 = K / (2 * kGK);  // pairs of stages (K is a multiple of 256)
-  Raw cur, nxt;
-  stage_x(0, s_x0);
-  load_w(0, cur);
-  decode(cur, 0, s_w[0]);
-  // every wave waits for its own direct loads before the barrier that hands
-  // them to the others (the barrier itself does not: the compiler waits where
-  // this wave reads LDS, behind it)
-  auto handover = [&]() __attribute__((always_inline)) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  };
-  for (int p = 0; p < n2; ++p) {
-    handover();  // stage 2 p is in LDS; every wave is past stage 2 p - 1
-    stage_x(2 * p + 1, s_x1);
-    load_w(min(p + 1, n2 - 1), nxt);
-    decode(cur, 1, s_w[1]);
-    multiply(s_x0, s_w[0]);
-    handover();  // stage 2 p + 1 is in LDS; every wave is past stage 2 p
-    if (p + 1 < n2) {
-      stage_x(2 * p + 2, s_x0);
-      decode(nxt, 0, s_w[0]);
+  auto stage_x = [&](int s, int buf) __attribute__((always_inline)) {
+    if (DIRECT && s < s_end) {
+#pragma unroll
+      for (int i = 0; i < XD; ++i)
+        direct_load(xr[i] + s * kGK, (buf ? s_x1 : s_x0) + (TT / 4 * wave + 8 * i) * 128);
     }
-    multiply(s_x1, s_w[1]);
-    cur = nxt;
+  };
+  // The barrier that hands a stage over: with direct loads every wave first
+  // waits for its own.
+  auto handover = []() __attribute__((always_inline)) {
+    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+  if constexpr (DIRECT) {
+    // Codes and scales of two stages at a time (64 bytes of a row are the least
+    // that memory delivers): the thread's 16 bytes of each stage's 32.  K and
+    // the parts are whole pairs of stages.
+    struct Pair { u32x4 c[2]; uint64_t s; };
+    auto load2 = [&](int s, Pair& r) __attribute__((always_inline)) {
+      s = min(s, s_end - 2);
+      r.c[0] = *reinterpret_cast<const u32x4*>(wsrc + s * 32);
+      r.c[1] = *reinterpret_cast<const u32x4*>(wsrc + s * 32 + 32);
+      const uint8_t* sp = a.w_sf + (size_t)nrow * (MODE == 0 ? K >> 4 : K >> 5) + s * (MODE == 0 ? 4 : 2);
+      if (MODE == 0) r.s = *reinterpret_cast<const uint64_t*>(sp);
+      else r.s = *reinterpret_cast<const uint32_t*>(sp);
+    };
+    auto store2 = [&](const Pair& r, int par, int buf) __attribute__((always_inline)) {
+      Raw w;
+      w.c = r.c[par];
+      w.s = (uint32_t)(r.s >> (MODE == 0 ? 32 * par + 16 * half : 16 * par + 8 * half)) & (MODE == 0 ? 0xFFFFu : 0xFFu);
+      store(w, buf);
+    };
+    Pair cur, nxt;
+    stage_x(s_begin, 0);
+    load2(s_begin, cur);
+    store2(cur, 0, 0);
+    for (int s = s_begin; s < s_end; s += 2) {
+      handover();  // stage s is in buffer 0, and every wave is past stage s - 1
+      stage_x(s + 1, 1);
+      load2(s + 2, nxt);
+      store2(cur, 1, 1);
+      multiply(0);
+      handover();  // stage s + 1 is in buffer 1, and every wave is past stage s
+      if (s + 2 < s_end) {
+        stage_x(s + 2, 0);
+        store2(nxt, 0, 0);
+      }
+      multiply(1);
+      cur = nxt;
+    }
+  } else {
+  Raw raw0, raw1;
+  load(s_begin, raw0);
+  load(s_begin + 1, raw1);
+  store(raw0, 0);
+  for (int s = s_begin; s < s_end; s += 2) {
+    handover();  // stage s is in buffer 0, and every wave is past stage s - 1
+    load(s + 2, raw0);
+    __builtin_amdgcn_sched_barrier(0);  // (the loads first: what follows waits for older ones)
+    multiply(0);
+    store(raw1, 1);
+    if (s + 1 >= s_end) break;
+    handover();  // stage s + 1 is in buffer 1, and every wave is past stage s
+    load(s + 3, raw1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1);
+    store(raw0, 0);
+  }
   }
 
-  // scales, then the adapters that occur among each 16 tokens, then the output
   const float gs = a.w_gs ? a.w_gs[0] : 1.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int t = t0 + wt + 16 * j + r16;
     const float cs = gs * (MODE == 0 && t < T ? a.xs[t] : 1.0f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i][j] *= cs;
-    if (a.L > 0) {
-      const int id = t < T ? a.id[t] : -1;
-      uint64_t left = __ballot((unsigned)id < (unsigned)a.L && q == 0);
-      while (left) {
-        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const bool mine = id == l;
-        left &= ~__ballot(mine);
-        v4f add[4];
+    for (int i = 0; i < NI; ++i) acc[i][j] *= cs;
+    if (gridDim.y > 1 && t < T) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) add[i] = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-          const int r = r0 + 8 * q;
-          v8bf hi = {}, lo = {};
-          if (mine && r < a.R) {
-            const float* u = a.u + (size_t)t * a.R + r;
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              hi[v] = (__bf16)u[v];
-              const float rest = u[v] - (float)hi[v];
-              lo[v] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.0f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = min(n0 + wn + 16 * i + r16, N - 1);
-            v8bf B = {};
-            if (r < a.R) B = *reinterpret_cast<const v8bf*>(a.b + ((size_t)l * N + n) * a.R + r);
-            add[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B, lo, add[i], 0, 0, 0);
-            add[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B, hi, add[i], 0, 0, 0);
-          }
-        }
-        if (mine) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][j] += add[i];
-        }
-      }
-    }
-    if (t < T) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int n = n0 + wn + 16 * i + 4 * q;
-        if (n < N) {  // (N is a multiple of 16)
-          const size_t at = (size_t)t * N + n;
-          const v4f o = acc[i][j];
-          if (a.out_f32)
-            *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = o;
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                uint2{bf16_bits(o[0]) | (bf16_bits(o[1]) << 16), bf16_bits(o[2]) | (bf16_bits(o[3]) << 16)};
-        }
+        if (n < N) *reinterpret_cast<v4f*>(a.part + ((size_t)blockIdx.y * T + t) * N + n) = acc[i][j];
       }
     }
   }
+  if (gridDim.y == 1) adapt_and_store<NI, 4>(a, acc, t0 + wt, n0 + wn);
+}
+
+// out = the sum of the parts, in order, and the adapters' part: 16 tokens x 256
+// rows per workgroup, 64 rows per wave, as the product's waves hold them.
+__global__ __launch_bounds__(256) void project_sum_kernel(ProjectArgs a, int parts) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int t = blockIdx.x * 16 + r16, n0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
+  if (n0 >= a.N) return;
+  v4f o[4][1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i][0] = v4f{0.f, 0.f, 0.f, 0.f};
+  const float* p = a.part + (size_t)min(t, a.T - 1) * a.N;
+#pragma unroll 2
+  for (int z = 0; z < parts; ++z, p += (size_t)a.T * a.N)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i][0] += *reinterpret_cast<const v4f*>(p + min(n0 + 16 * i + 4 * q, a.N - 4));
+  adapt_and_store<4, 1>(a, o, blockIdx.x * 16, n0);
 }
 
 template <int MODE, int NG>
@@ -526,7 +718,7 @@ void launch_few_tokens(const ProjectArgs& a, hipStream_t s) {
 template <int MODE>
 hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
   const bool few = a.T <= kProjectFew;
-  const bool dot = a.L > 0 && a.T <= kProjectDot;
+  const bool dot = a.L > 0 && project_dot(a.T, a.K, a.R);
   const int prep = few || MODE == 0 ? a.T : 0;
   const int blocks = prep + (dot ? a.T * (a.R / kShrinkRanks) : 0);
   if (blocks > 0) {
@@ -536,22 +728,65 @@ hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   if (a.L > 0 && !dot) {
-    hipLaunchKernelGGL(project_shrink_kernel, dim3((a.T + 15) / 16), dim3(256), 0, s, a);
-    const hipError_t err = hipGetLastError();
+    hipError_t err = launch_route(a.id, a.T, a.L, 32, a.route, s);
     if (err != hipSuccess) return err;
+    const dim3 grid((a.T + 31) / 32 + a.L, a.ku);
+    if (a.R <= 16) hipLaunchKernelGGL(project_shrink_kernel<1>, grid, dim3(512), 0, s, a);
+    else if (a.R <= 32) hipLaunchKernelGGL(project_shrink_kernel<2>, grid, dim3(512), 0, s, a);
+    else if (a.R <= 64) hipLaunchKernelGGL(project_shrink_kernel<4>, grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL(project_shrink_kernel<8>, grid, dim3(512), 0, s, a);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (a.ku > 1) {
+      const long long n = (long long)a.T * a.R / 4;
+      hipLaunchKernelGGL(project_u_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+      err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
   }
   if (few) {
     if (a.T <= 16) launch_few_tokens<MODE, 1>(a, s);
     else if (a.T <= 32) launch_few_tokens<MODE, 2>(a, s);
-    else launch_few_tokens<MODE, 4>(a, s);
+    else if (a.T <= 64) launch_few_tokens<MODE, 4>(a, s);
+    else launch_few_tokens<MODE, 8>(a, s);
   } else {
-    const int rt = (a.N + kTile - 1) / kTile, tt = (a.T + kTile - 1) / kTile;
-    hipLaunchKernelGGL(project_gemm_kernel<MODE>, dim3(rt * tt), dim3(256), 0, s, a, rt);
+    const ProjectGemm g = project_gemm_plan(a.T, a.N, a.K);
+    const int rt = (a.N + kTile - 1) / kTile;
+    const dim3 grid(rt * ((a.T + g.tt - 1) / g.tt), g.parts);
+    if (g.tt == 128) hipLaunchKernelGGL((project_gemm_kernel<MODE, 128>), grid, dim3(256), 0, s, a, rt, g.per);
+    else hipLaunchKernelGGL((project_gemm_kernel<MODE, 64>), grid, dim3(256), 0, s, a, rt, g.per);
+    if (g.parts > 1) {
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+      hipLaunchKernelGGL(project_sum_kernel, dim3((a.T + 15) / 16, (a.N + 255) / 256), dim3(256), 0, s, a, g.parts);
+    }
   }
   return hipGetLastError();
 }
 
 }  // namespace
+
+// 128 tokens per workgroup where that fills the chip twice over (two
+// workgroups per CU), else 64, and K in parts of at least 8 stages.
+ProjectGemm project_gemm_plan(long long T, long long N, long long K) {
+  ProjectGemm g;
+  const long long rt = (N + kTile - 1) / kTile;
+  g.tt = rt * ((T + 127) / 128) >= 512 ? 128 : 64;
+  const long long tiles = rt * ((T + g.tt - 1) / g.tt), nst = K / kGK;
+  long long parts = 512 / tiles;
+  parts = parts > nst / 8 ? nst / 8 : parts;
+  parts = parts < 1 ? 1 : parts;
+  g.per = (int)((nst + parts - 1) / parts);
+  g.parts = (int)((nst + g.per - 1) / g.per);
+  return g;
+}
+
+int project_u_parts(long long T, long long K, long long R) {
+  if (project_dot(T, K, R)) return 1;
+  int n = 8;
+  while (n > 1 && ((T + 31) / 32 * n > 256 || (K / 256) % n)) n >>= 1;
+  return n;
+}
 
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   return a.g16 ? launch_mode<0>(a, s) : launch_mode<1>(a, s);

@@ -292,9 +292,10 @@ moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* by
  * lora_a [adapters, rank, K] and lora_b [adapters, N, rank] bfloat16, id [T]
  * int32, scale [adapters] float32, all device memory; x, w, w_sf, lora_a,
  * lora_b and out 16-byte aligned, the workspace 256-byte aligned.  K a
- * multiple of 256 and N of 16, rank a multiple of 8 up to 128 (K and rank
- * multiples of 32 and 8 EINVAL otherwise, the rest EUNSUPPORTED); T < 2^24 and
- * N*K, T*N/16 and adapters*N*rank below 2^32 (EUNSUPPORTED otherwise).
+ * multiple of 32 and rank a positive multiple of 8 (EINVAL otherwise); K a
+ * multiple of 256 and N of 16, rank up to 128, up to 512 adapters, T below
+ * 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38 (EUNSUPPORTED
+ * otherwise).
  * Enqueued on `stream`. */
 moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8_t* w, const uint8_t* w_sf,
                               const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
