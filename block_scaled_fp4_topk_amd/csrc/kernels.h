@@ -94,11 +94,11 @@ hipError_t launch_rows_to_f16(const uint16_t* x, int T, int H, uint16_t* x16, fl
                               hipStream_t s);
 
 // The whole layer for a few tokens in two launches (layer.hip).  T <= 16,
-// H % 256 == 0, H <= 6144, I % 256 == 0, I * H < 2^31, at most 64 experts per
+// H % 256 == 0, H <= 6144, I % 256 == 0, I * H < 2^31, at most 16 experts per
 // token (shared ones among them), E = routed + shared <= 512.
 constexpr int kFewTokens = 16;
 constexpr int kFewMaxH = 6144;
-constexpr int kFewMaxK = 64;
+constexpr int kFewMaxK = 16;
 struct FewArgs {
   GateSel g;              // E: routed experts
   int T, H, I, w13_order;

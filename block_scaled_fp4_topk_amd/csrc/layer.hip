@@ -44,6 +44,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kQueues = kFewQueues, kLine = kFewLine;
+constexpr int kActive = kFewTokens * kFewMaxK;  // most experts that have a token
 constexpr int kThreads = 64 * kWaves;
 
 // Stride in LDS of a token's h (256 values, 16 bytes of padding against bank
@@ -178,26 +179,32 @@ struct WPair {
   uint32_t s[2];
 };
 
-// Where a pair's rows lie: code offsets of the lane's rows in instructions 0
-// and 2 (8 rows further on in 1 and 3) and scale offsets of its operand rows.
-// Chunk c is c * 128 code and c * 16 (group16) or c * 8 scale bytes on.
+// Where a pair's rows lie: wave-uniform addresses of the two tiles' first rows
+// (codes and scales).  The lane's place in a tile is the same for every tile:
+// LaneOff.  Chunk c is c * 128 code and c * 16 (group16) or c * 8 scale bytes on.
 struct WSrc {
-  GPtr codes, sf;
-  uint32_t o0, o1, step8, f0, f1;
+  GPtr c0, c1, f0, f1;
 };
+struct LaneOff {
+  uint32_t lo, hi, sf;  // rows lane / 8 and 8 + lane / 8, 16 bytes; scales of row r16
+};
+__device__ __forceinline__ LaneOff lane_offsets(int lane, uint32_t row_bytes, uint32_t sf_bytes, int mode) {
+  const uint32_t lo = (lane >> 3) * row_bytes + 16 * (lane & 7);
+  return LaneOff{lo, lo + 8 * row_bytes, (lane & 15) * sf_bytes + (lane >> 4) * (mode == 0 ? 4u : 2u)};
+}
 
 template <int MODE>
-__device__ __forceinline__ void load_pair(WPair& w, const WSrc& s, uint32_t c) {
-  w.c[0] = gload_nt(s.codes, s.o0 + c * 128);
-  w.c[1] = gload_nt(s.codes, s.o0 + s.step8 + c * 128);
-  w.c[2] = gload_nt(s.codes, s.o1 + c * 128);
-  w.c[3] = gload_nt(s.codes, s.o1 + s.step8 + c * 128);
+__device__ __forceinline__ void load_pair(WPair& w, const WSrc& s, const LaneOff& o, uint32_t c) {
+  w.c[0] = gload_nt(s.c0 + c * 128, o.lo);
+  w.c[1] = gload_nt(s.c0 + c * 128, o.hi);
+  w.c[2] = gload_nt(s.c1 + c * 128, o.lo);
+  w.c[3] = gload_nt(s.c1 + c * 128, o.hi);
   if (MODE == 0) {
-    w.s[0] = gload<uint32_t>(s.sf, s.f0 + c * 16);
-    w.s[1] = gload<uint32_t>(s.sf, s.f1 + c * 16);
+    w.s[0] = gload<uint32_t>(s.f0 + c * 16, o.sf);
+    w.s[1] = gload<uint32_t>(s.f1 + c * 16, o.sf);
   } else {
-    w.s[0] = gload<uint16_t>(s.sf, s.f0 + c * 8);
-    w.s[1] = gload<uint16_t>(s.sf, s.f1 + c * 8);
+    w.s[0] = gload<uint16_t>(s.f0 + c * 8, o.sf);
+    w.s[1] = gload<uint16_t>(s.f1 + c * 8, o.sf);
   }
 }
 
@@ -283,12 +290,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][(MODE == 0 ? 4 : 8) * kHRow];
   __shared__ int s_ids[kFewTokens * kFewMaxK];
   __shared__ float s_tw[kFewTokens * kFewMaxK];
-  __shared__ short s_rank[kMaxExperts], s_act[kMaxExperts];
-  __shared__ uint8_t s_col[kMaxExperts * kFewTokens];  // [active][token]: place of the expert in the token's list
-  __shared__ uint8_t s_idx[kMaxExperts * kFewTokens];  // [active][token]: the token's number among the expert's
-  __shared__ __attribute__((aligned(16))) uint16_t s_slot[kMaxExperts * kFewTokens];  // [active][number]: its h row
-  __shared__ uint8_t s_ne[kMaxExperts];                // [active]: tokens
-  __shared__ float s_gs13[kMaxExperts], s_gs2[kMaxExperts], s_xs[kFewTokens];
+  // per active expert: its id and tokens, and per token
+  __shared__ short s_rank[kMaxExperts];
+  __shared__ uint8_t s_col[kActive * kFewTokens];  // [active][token]: place of the expert in the token's list
+  __shared__ uint8_t s_idx[kActive * kFewTokens];  // [active][token]: the token's number among the expert's
+  __shared__ __attribute__((aligned(16))) uint16_t s_slot[kActive * kFewTokens];  // [active][number]: its h row
+  __shared__ float s_wt[kActive * kFewTokens];     // [active][token]: router weight times w2's global scale, 0: none
+  __shared__ int s_en[kActive];                    // expert | tokens << 16
+  __shared__ float s_gs13[kActive], s_xs[kFewTokens];
   __shared__ int s_cnt[kWaves], s_claim[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -309,7 +318,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
 
   // ---- selection, by every workgroup for itself
   for (int i = tid; i < kMaxExperts; i += kThreads) s_rank[i] = 0;
-  for (int i = tid; i < kMaxExperts * kFewTokens / 4; i += kThreads) reinterpret_cast<uint32_t*>(s_col)[i] = ~0u;
+  for (int i = tid; i < kActive * kFewTokens / 4; i += kThreads) reinterpret_cast<uint32_t*>(s_col)[i] = ~0u;
   for (int t = wave; t < T; t += kWaves) {
     const float* row = a.logits + (size_t)t * a.ld;
     auto emit = [&](int j, int id, float w) __attribute__((always_inline)) {
@@ -364,10 +373,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   nact = __builtin_amdgcn_readfirstlane(nact);
   if ((on >> lane) & 1) {
     const int rank = before + __popcll(on & ((1ull << lane) - 1ull));
-    s_act[rank] = (short)tid;
+    s_en[rank] = tid;
     s_rank[tid] = (short)rank;
     s_gs13[rank] = a.w13_gs ? a.w13_gs[tid] : 1.0f;
-    s_gs2[rank] = a.w2_gs ? a.w2_gs[tid] : 1.0f;
   }
   if (tid < kFewTokens) s_xs[tid] = MODE == 0 && tid < T ? a.xs[tid] : 1.0f;
   __syncthreads();
@@ -390,15 +398,19 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     return;
   }
   __syncthreads();
-  if (tid < nact) {
-    int n = 0;
-    for (int t = 0; t < T; ++t) {
-      s_idx[tid * kFewTokens + t] = (uint8_t)n;
-      const int col = s_col[tid * kFewTokens + t];
-      if (col != 255) s_slot[tid * kFewTokens + n++] = (uint16_t)(t * kt + col);
-    }
-    s_ne[tid] = (uint8_t)n;
-    for (; n < kFewTokens; ++n) s_slot[tid * kFewTokens + n] = s_slot[tid * kFewTokens];  // (any row that exists)
+  // 16 lanes per active expert, a token each
+  for (int i = tid; i < nact * kFewTokens; i += kThreads) {
+    const int act = i >> 4, t = i & 15, col = s_col[i];
+    const uint32_t has = (uint32_t)(ballot(col != 255) >> (lane & 48)) & 0xFFFFu;
+    const int n = __popc(has & ((1u << t) - 1u)), ne = __popc(has), first = __builtin_ctz(has);
+    const int e = s_en[act] & 0xFFFF;  // (lane t = 0 writes the count beside it)
+    s_idx[i] = (uint8_t)n;
+    s_wt[i] = col != 255 ? s_tw[t * kt + col] * (a.w2_gs ? a.w2_gs[e] : 1.0f) : 0.0f;
+    // h rows in token order; past the last, the first again
+    if (col != 255) s_slot[act * kFewTokens + n] = (uint16_t)(t * kt + col);
+    const int c0 = s_col[act * kFewTokens + first];
+    if (t >= ne) s_slot[act * kFewTokens + t] = (uint16_t)(first * kt + c0);
+    if (t == 0) s_en[act] = e | (ne << 16);
   }
   __syncthreads();
 
@@ -408,19 +420,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const uint32_t rowb = (uint32_t)(H >> 1), rows = (uint32_t)(MODE == 0 ? H >> 4 : H >> 5);
   const size_t A = (size_t)T * kt;
   WPair w1[NC];
-  auto expert = [&](int act) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((int)s_act[act]); };
+  auto expert = [&](int act) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(s_en[act]) & 0xFFFF; };
+  // (past the last item: the first one's rows, for loads that are issued all
+  // the same and whose data is not used)
+  const LaneOff off1 = lane_offsets(lane, rowb, rows, MODE);
   auto src1 = [&](int it) __attribute__((always_inline)) -> WSrc {
     const int i0 = it < n1 ? it : 0;
-    const int act = i0 / npt, pt = i0 - act * npt, e = expert(act);
-    // (past the last item the lanes' offsets collapse to one line: loads that
-    // are issued all the same and whose data is not used)
-    const uint32_t on = it < n1 ? 1u : 0u;
-    const uint32_t g0 = (uint32_t)(pt * 16) + (a.w13_order ? (uint32_t)I : 0u);
-    const uint32_t u0 = (uint32_t)(pt * 16) + (a.w13_order ? 0u : (uint32_t)I);
-    const uint32_t co = 16 * (lane & 7), so = MODE == 0 ? 4 * q : 2 * q;
-    return WSrc{uniform_ptr(a.w13 + (size_t)e * 2 * I * rowb), uniform_ptr(a.w13_sf + (size_t)e * 2 * I * rows),
-                on * ((g0 + (lane >> 3)) * rowb + co), on * ((u0 + (lane >> 3)) * rowb + co), on * 8 * rowb,
-                on * ((g0 + r16) * rows + so), on * ((u0 + r16) * rows + so)};
+    const int act = i0 / npt, pt = i0 - act * npt;
+    const size_t r = (size_t)expert(act) * 2 * I + pt * 16;
+    const size_t g = r + (a.w13_order ? I : 0), u = r + (a.w13_order ? 0 : I);
+    return WSrc{uniform_ptr(a.w13 + g * rowb), uniform_ptr(a.w13 + u * rowb), uniform_ptr(a.w13_sf + g * rows),
+                uniform_ptr(a.w13_sf + u * rows)};
   };
   const Turn turn = turn_offsets(lane);
   uint8_t* const my_turn = s_turn[wave];
@@ -436,7 +446,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     const WSrc src = src1(item);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      load_pair<MODE>(w1[i], src, ck1[i]);
+      load_pair<MODE>(w1[i], src, off1, ck1[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
     // (the activations, requested earlier, have arrived: without this they
@@ -455,7 +465,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       use_from_here(w1[i]);
       turn_pair(w1[i], my_turn, turn);
       mfma_pair<MODE, 1>(w1[i], acc, [&](int j, int) __attribute__((always_inline)) { return xb[i][j]; });
-      load_pair<MODE>(w1[i], src, ck1[i]);
+      load_pair<MODE>(w1[i], src, off1, ck1[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
     s_red[buf][wave][0][lane] = float4{acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
@@ -544,7 +554,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const uint32_t total = (uint32_t)(nrb * ns);  // total * nwg < 2^31 (checked by the launch)
   const uint32_t G = min((uint32_t)a.nwg, total);
   const uint32_t wg = blockIdx.x;
-  drain_memory();  // this wave's stores of h are complete
+  // This workgroup's stores of h are complete, and said to be before its first
+  // weights of FC2 are requested: those fill the CU's queues, and the last
+  // workgroup's word would come 3 us later.
+  drain_memory();
+  lds_barrier();
+  if (tid == 0 && mine) __hip_atomic_fetch_add(dones + xcd * kLine, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const bool works = wg < G;
   const int begin = works ? (int)(wg * total / G) : 0, end = works ? (int)((wg + 1) * total / G) : 0;
   const uint32_t rowb2 = (uint32_t)(I >> 1), rows2 = (uint32_t)(MODE == 0 ? I >> 4 : I >> 5);
@@ -560,32 +575,37 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     const int rb = s / ns, st = s - rb * ns;
     return Group{rb, st, min(NS, min(ns - st, end - s))};
   };
-  // the unit of step st that this wave takes (where the last step of a block
-  // has fewer than 8, a unit that exists, whose product is not added)
-  auto unit = [&](int st, int* act, int* c) __attribute__((always_inline)) {
-    int f = st * kWaves + wave;
-    f = f < units ? f : units - 1;
-    *act = f / nch2;
-    *c = f - *act * nch2;
+  // The unit (expert, chunk) that this wave takes of a step: units are counted
+  // on from step to step, 8 at a time (no divisions).  Where the last step of a
+  // block has fewer than 8, the last unit stands in; its product is not added.
+  const int d_act = kWaves / nch2, d_c = kWaves - d_act * nch2;
+  struct Unit { int act, c; };
+  auto unit = [&](int st) __attribute__((always_inline)) -> Unit {
+    const int f = st * kWaves + wave, act = f / nch2;
+    return Unit{act, f - act * nch2};
   };
-  // Step k of a group.  Loads of steps that the group does not have are issued
-  // too, all lanes from one line (see FC1).
-  auto load_w2 = [&](const Group& g, int k, WPair& w) __attribute__((always_inline)) {
-    const uint32_t on = k < g.n ? 1u : 0u;
-    int act, c;
-    unit(on ? g.st + k : g.st, &act, &c);
-    const int e = expert(act);
-    const uint32_t r0 = (uint32_t)(g.rb * 32), co = 16 * (lane & 7), so = MODE == 0 ? 4 * q : 2 * q;
-    load_pair<MODE>(w, WSrc{uniform_ptr(a.w2 + (size_t)e * H * rowb2), uniform_ptr(a.w2_sf + (size_t)e * H * rows2),
-                            on * ((r0 + (lane >> 3)) * rowb2 + co), on * ((r0 + 16 + (lane >> 3)) * rowb2 + co),
-                            on * 8 * rowb2, on * ((r0 + r16) * rows2 + so), on * ((r0 + 16 + r16) * rows2 + so)}, c);
+  auto next_unit = [&](Unit u) __attribute__((always_inline)) -> Unit {
+    u.act += d_act;
+    u.c += d_c;
+    return u.c >= nch2 ? Unit{u.act + 1, u.c - nch2} : u;
+  };
+  auto there = [&](Unit u) __attribute__((always_inline)) -> Unit { return u.act < nact ? u : Unit{nact - 1, nch2 - 1}; };
+  // Loads of steps that a group does not have are issued too, from the group's
+  // last unit again.
+  const LaneOff off2 = lane_offsets(lane, rowb2, rows2, MODE);
+  auto load_w2 = [&](int rb, Unit u, WPair& w) __attribute__((always_inline)) {
+    u = there(u);
+    const size_t r = (size_t)expert(u.act) * H + rb * 32;
+    const uint8_t *c = a.w2 + r * rowb2, *f = a.w2_sf + r * rows2;
+    load_pair<MODE>(w, WSrc{uniform_ptr(c), uniform_ptr(c + 16 * rowb2), uniform_ptr(f), uniform_ptr(f + 16 * rows2)}, off2,
+                    u.c);
   };
   // h of the expert's tokens n0 .. n0 + kHalf - 1, a token's 512 bytes per
-  // load (and per part); loads for tokens it does not have collapse likewise.
-  // (Offsets in 32 bits: h is below 2 GB.)
-  auto h_rows = [&](int act, int c, int n0, bool on, uint64_t (&b)[NB][kHalf]) __attribute__((always_inline)) {
+  // load (and per part); loads for tokens it does not have collapse to one
+  // line.  (Offsets in 32 bits: h is below 2 GB.)
+  auto h_rows = [&](int act, int c, int n0, uint64_t (&b)[NB][kHalf]) __attribute__((always_inline)) {
     const uint2 four = *reinterpret_cast<const uint2*>(s_slot + act * kFewTokens + n0);
-    const int ne = on ? __builtin_amdgcn_readfirstlane((int)s_ne[act]) : 0;
+    const int ne = __builtin_amdgcn_readfirstlane(s_en[act]) >> 16;
     const uint32_t pair[2] = {(uint32_t)__builtin_amdgcn_readfirstlane((int)four.x),
                               (uint32_t)__builtin_amdgcn_readfirstlane((int)four.y)};
 #pragma unroll
@@ -596,28 +616,28 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       for (int p = 0; p < NB; ++p) b[p][n] = ld_agent(reinterpret_cast<const uint8_t*>(a.h + p * A * I) + o);
     }
   };
-  auto load_h = [&](const Group& g, int k, uint64_t (&b)[NB][kHalf], uint32_t& x) __attribute__((always_inline)) {
-    const bool on = k < g.n;
-    int act, c;
-    unit(on ? g.st + k : g.st, &act, &c);
-    h_rows(act, c, 0, on, b);
+  auto load_h = [&](Unit u, uint64_t (&b)[NB][kHalf], uint32_t& x) __attribute__((always_inline)) {
+    u = there(u);
+    h_rows(u.act, u.c, 0, b);
     if (MODE == 0) {
-      const int col = s_col[act * kFewTokens + r16];
-      const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[act * kFewTokens];
-      const uint32_t o = slot * (uint32_t)(I >> 4) + c * 16 + 4 * q;
+      const int col = s_col[u.act * kFewTokens + r16];
+      const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[u.act * kFewTokens];
+      const uint32_t o = slot * (uint32_t)(I >> 4) + u.c * 16 + 4 * q;
       x = __hip_atomic_load(reinterpret_cast<const uint32_t*>(a.hexp + o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   };
   Group cur = group(begin);
+  const Unit first_unit = unit(cur.st);
+  {
+    Unit u = first_unit;
 #pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    load_w2(cur, k, w2[k]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int k = 0; k < NS; ++k) {
+      load_w2(cur.rb, u, w2[k]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + 1 < cur.n) u = next_unit(u);
+    }
   }
-  lds_barrier();  // (every wave's stores are complete)
   if (wave == 0) {
-    if (mine && lane == 0)
-      __hip_atomic_fetch_add(dones + xcd * kLine, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
     while (works) {
       int d = __hip_atomic_load(dones + (lane & (kQueues - 1)) * kLine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -633,10 +653,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
   }
   lds_barrier();
+  {
+    Unit u = first_unit;
 #pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    load_h(cur, k, hb[k], hx[k]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int k = 0; k < NS; ++k) {
+      load_h(u, hb[k], hx[k]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + 1 < cur.n) u = next_unit(u);
+    }
   }
 
   float oacc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -716,20 +740,29 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     arrived(hb[k]);
     if (MODE == 0) asm volatile("" : "+v"(hx[k]));
   }
+  Unit cu = first_unit;
   for (int s = begin; s < end;) {
     const int after = s + cur.n;
-    // (past the end: the last group's place, with no steps)
-    Group nxt = group(after < end ? after : s);
-    nxt.n = after < end ? nxt.n : 0;
+    // (past the end: this group's rows again)
+    Group nxt = cur;
+    Unit nu = cu;
+    if (after < end) {
+      nxt = group(after);
+      nu = unit(nxt.st);
+    }
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
       use_from_here(w2[k]);
       if (k < cur.n) {
-        int act, c;
-        unit(cur.st + k, &act, &c);
-        const int ne = __builtin_amdgcn_readfirstlane((int)s_ne[act]);
-        const int col = s_col[act * kFewTokens + r16], idx = s_idx[act * kFewTokens + r16];
-        float cs = s_gs2[act] * s_tw[r16 * kt + (col != 255 ? col : 0)];
+        const Unit u = there(cu);
+        const int act = u.act, c = u.c;
+        const bool counts = cu.act < nact;
+        if (k + 1 < cur.n) cu = next_unit(cu);
+        const int ne = __builtin_amdgcn_readfirstlane(s_en[act]) >> 16;
+        const int idx = s_idx[act * kFewTokens + r16];
+        // (0: not this token's expert, or a unit that only stands in)
+        float cs = counts ? s_wt[act * kFewTokens + r16] : 0.0f;
+        const bool chosen = counts && s_col[act * kFewTokens + r16] != 255;
         turn_pair(w2[k], my_turn, turn);
         _Float16 f4[4];
         if constexpr (MODE == 0) {
@@ -746,13 +779,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f4[i] = (_Float16)__builtin_ldexpf(1.0f, p[i] - P);
         }
-        const bool valid = col != 255 && (cur.st + k) * kWaves + wave < units;
         // kHalf tokens at a time (more of one expert: once again, their h
         // fetched on the spot)
 #pragma unroll 1
         for (int n0 = 0; n0 < ne; n0 += kHalf) {
           if (n0 > 0) {
-            h_rows(act, c, n0, true, hb[k]);
+            h_rows(act, c, n0, hb[k]);
             arrived(hb[k]);
           }
 #pragma unroll
@@ -769,7 +801,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
             if constexpr (MODE == 0) return __builtin_bit_cast(v8h, v) * f4[j >> 1];
             else return v;
           });
-          if (valid && r >= 0 && r < kHalf) {
+          if (chosen && r >= 0 && r < kHalf) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               oacc[i] = __builtin_fmaf(acc[0][i], cs, oacc[i]);
@@ -778,13 +810,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
           }
         }
       }
-      load_w2(nxt, k, w2[k]);
-      load_h(nxt, k, hb[k], hx[k]);
+      load_w2(nxt.rb, nu, w2[k]);
+      load_h(nu, hb[k], hx[k]);
+      if (k + 1 < nxt.n) nu = next_unit(nu);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (cur.st + cur.n == ns || after >= end) flush(cur.rb);
     s = after;
     cur = nxt;
+    cu = unit(cur.st);
   }
 }
 

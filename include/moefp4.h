@@ -253,7 +253,7 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
 /* A whole mixture-of-experts layer on bfloat16 x: moe_fp4_gate, then
  * moe_fp4_forward with the ids and weights it gives (p->E counts the routed
  * experts and the g->shared last ones, p->top_k = g->top_k + g->shared).
- * Up to 16 tokens of BF16 activations (and H <= 6144, top_k <= 64) run in two
+ * Up to 16 tokens of BF16 activations (and H <= 6144, top_k <= 16) run in two
  * launches: router logits, then one persistent kernel for selection, FC1, FC2
  * and the weighted sum.  That form keeps h to at least 11 significant bits
  * between FC1 and FC2 (moe_fp4_forward rounds it to bfloat16); all its waits
