@@ -613,7 +613,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       const uint32_t slot = (pair[n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
       const uint32_t o = 2 * (slot * (uint32_t)I + c * 256) + (n0 + n < ne ? 8 * lane : 0);
 #pragma unroll
-      for (int p = 0; p < NB; ++p) b[p][n] = ld_agent(reinterpret_cast<const uint8_t*>(a.h + p * A * I) + o);
+      for (int p = 0; p < NB; ++p) b[p][n] = gload<uint64_t>((GPtr)(a.h + p * A * I), o);
     }
   };
   auto load_h = [&](Unit u, uint64_t (&b)[NB][kHalf], uint32_t& x) __attribute__((always_inline)) {
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       const int col = s_col[u.act * kFewTokens + r16];
       const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[u.act * kFewTokens];
       const uint32_t o = slot * (uint32_t)(I >> 4) + u.c * 16 + 4 * q;
-      x = __hip_atomic_load(reinterpret_cast<const uint32_t*>(a.hexp + o), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      x = gload<uint32_t>((GPtr)a.hexp, o);
     }
   };
   Group cur = group(begin);
@@ -651,6 +651,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       }
       __builtin_amdgcn_s_sleep(4);
     }
+    // (what this CU and XCD cached of h before is dropped: h is read through
+    // the caches from here on)
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   }
   lds_barrier();
   {
