@@ -51,8 +51,10 @@ constexpr int kThreads = 64 * kWaves;
 // conflicts).
 constexpr int kHRow = 512 + 16;
 
-// Longest wait for FC1, in ticks of the 100 MHz real-time counter (50 ms).
-constexpr uint64_t kFewMaxWait = 5000000;
+// Looks at FC1's counters before a wait is given up: about a microsecond each,
+// 0.3 s in all.  (Counted, not timed: a clock goes on while the queue is
+// switched out for another process's.)
+constexpr int kFewMaxPolls = 1 << 18;
 
 // bf16 row -> fp16 * 2**-p (exact down to 2**-24 of the row's maximum, which
 // lands in [2**14, 2**15)) by 256 threads.
@@ -638,14 +640,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
   }
   if (wave == 0) {
-    const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
-    while (works) {
+    for (int polls = 0; works; ++polls) {
       int d = __hip_atomic_load(dones + (lane & (kQueues - 1)) * kLine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       d += __shfl_xor(d, 1, 64);
       d += __shfl_xor(d, 2, 64);
       d += __shfl_xor(d, 4, 64);
       if (__builtin_amdgcn_readfirstlane(d) >= n1) break;
-      if (__builtin_amdgcn_s_memrealtime() - t0 > kFewMaxWait) {
+      if (polls == kFewMaxPolls) {
         if (lane == 0) __hip_atomic_fetch_add(a.flags + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         break;
       }

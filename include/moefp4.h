@@ -257,8 +257,8 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
  * launches: router logits, then one persistent kernel for selection, FC1, FC2
  * and the weighted sum.  That form keeps h to at least 11 significant bits
  * between FC1 and FC2 (moe_fp4_forward rounds it to bfloat16); all its waits
- * are bounded, and if one ever exceeded its 50 ms, the workspace's second word
- * is nonzero and the result is not valid.  Other sizes and formats run
+ * are bounded, and if one ever exceeded its bound (0.3 s of its own running
+ * time), the workspace's second word is nonzero and the result is not valid.  Other sizes and formats run
  * moe_fp4_gate and moe_fp4_forward one after the other.
  * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
