@@ -445,7 +445,7 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
     """A whole mixture-of-experts layer on bfloat16 x [T, H]: gate() with
     gate_w [E - shared, H], then forward() over the E experts of the weight
     tensors, the last `shared` of which every token takes with weight 1.  Up
-    to 16 tokens run in two launches (moe_fp4_layer).  quantize_x, w_layout,
+    to 8 tokens (2 with group32 weights) run in two launches (moe_fp4_layer).  quantize_x, w_layout,
     w13_order and out_dtype as for forward(); topk_ids / topk_w
     [T, top_k + shared]: optional outputs for the selection.  Returns out
     [T, H]."""

@@ -430,9 +430,8 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
   st = gate_check(g, p->T, p->E - g->shared, p->H, &P->gate);
   if (st != MOEFP4_OK) return st;
   const size_t T = p->T, H = p->H, I = p->I, A = T * p->top_k;
-  // (both forms at 16 tokens: see the launcher's comment)
-  P->few = p->T >= 1 && p->T <= moefp4::kFewTokens && p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH &&
-           p->top_k <= moefp4::kFewMaxK;
+  P->few = p->T >= 1 && p->T <= (p->gran_k == 16 ? moefp4::kFewTokens : moefp4::kFewTokensG32) &&
+           p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH && p->top_k <= moefp4::kFewMaxK;
   P->nwg = moefp4::cu_count();
   // (launch 2 counts FC2's steps times workgroups in 31 bits)
   if (P->few && (H / 32) * ((size_t)p->E * (I / 256) / 8 + 1) * P->nwg >= (1ull << 31)) P->few = false;

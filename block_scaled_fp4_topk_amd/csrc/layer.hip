@@ -1,4 +1,4 @@
-// A whole mixture-of-experts layer for at most 16 tokens, in two launches:
+// A whole mixture-of-experts layer for at most 8 tokens, in two launches:
 // router logits, then one persistent kernel that selects the experts, runs
 // FC1 + SwiGLU and FC2 over their FP4 weights and writes the weighted sum.
 //
@@ -8,7 +8,7 @@
 //
 // * Every activation a wavefront needs for FC1 stays in its registers.  A
 //   wave owns a fixed slice of H (1/8 of it: at most 3 chunks of 256), whose
-//   MFMA operands for all 16 token columns are loaded once (32 registers per
+//   MFMA operands for all token columns are loaded once (32 registers per
 //   chunk) and serve every expert; the weights come straight from HBM into
 //   registers, are decoded there and multiplied.  No operand passes through
 //   LDS; it only sums the 8 waves' partial tiles.  Columns of tokens that did
@@ -44,6 +44,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kQueues = kFewQueues, kLine = kFewLine;
+constexpr int kCols = 16;                       // columns of a matrix instruction: tokens' places
 constexpr int kActive = kFewTokens * kFewMaxK;  // most experts that have a token
 constexpr int kThreads = 64 * kWaves;
 
@@ -290,16 +291,16 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ float4 s_red[2][kWaves][2][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[kWaves][4096];
   __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][(MODE == 0 ? 4 : 8) * kHRow];
-  __shared__ int s_ids[kFewTokens * kFewMaxK];
-  __shared__ float s_tw[kFewTokens * kFewMaxK];
+  __shared__ int s_ids[kActive];
+  __shared__ float s_tw[kActive];
   // per active expert: its id and tokens, and per token
   __shared__ short s_rank[kMaxExperts];
-  __shared__ uint8_t s_col[kActive * kFewTokens];  // [active][token]: place of the expert in the token's list
-  __shared__ uint8_t s_idx[kActive * kFewTokens];  // [active][token]: the token's number among the expert's
-  __shared__ __attribute__((aligned(16))) uint16_t s_slot[kActive * kFewTokens];  // [active][number]: its h row
-  __shared__ float s_wt[kActive * kFewTokens];     // [active][token]: router weight times w2's global scale, 0: none
+  __shared__ uint8_t s_col[kActive * kCols];  // [active][token]: place of the expert in the token's list
+  __shared__ uint8_t s_idx[kActive * kCols];  // [active][token]: the token's number among the expert's
+  __shared__ __attribute__((aligned(16))) uint16_t s_slot[kActive * kCols];  // [active][number]: its h row
+  __shared__ float s_wt[kActive * kCols];     // [active][token]: router weight times w2's global scale, 0: none
   __shared__ int s_en[kActive];                    // expert | tokens << 16
-  __shared__ float s_gs13[kActive], s_xs[kFewTokens];
+  __shared__ float s_gs13[kActive], s_xs[kCols];
   __shared__ int s_cnt[kWaves], s_claim[2];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
 
   // ---- selection, by every workgroup for itself
   for (int i = tid; i < kMaxExperts; i += kThreads) s_rank[i] = 0;
-  for (int i = tid; i < kActive * kFewTokens / 4; i += kThreads) reinterpret_cast<uint32_t*>(s_col)[i] = ~0u;
+  for (int i = tid; i < kActive * kCols / 4; i += kThreads) reinterpret_cast<uint32_t*>(s_col)[i] = ~0u;
   for (int t = wave; t < T; t += kWaves) {
     const float* row = a.logits + (size_t)t * a.ld;
     auto emit = [&](int j, int id, float w) __attribute__((always_inline)) {
@@ -379,12 +380,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     s_rank[tid] = (short)rank;
     s_gs13[rank] = a.w13_gs ? a.w13_gs[tid] : 1.0f;
   }
-  if (tid < kFewTokens) s_xs[tid] = MODE == 0 && tid < T ? a.xs[tid] : 1.0f;
+  if (tid < kCols) s_xs[tid] = MODE == 0 && tid < T ? a.xs[tid] : 1.0f;
   __syncthreads();
   int none = 0;
   for (int i = tid; i < T * kt; i += kThreads) {
     const int id = s_ids[i], t = i / kt;
-    if (id >= 0) s_col[s_rank[id] * kFewTokens + t] = (uint8_t)(i - t * kt);
+    if (id >= 0) s_col[s_rank[id] * kCols + t] = (uint8_t)(i - t * kt);
     if (blockIdx.x == 0) {
       none += id < 0;
       if (a.ids) a.ids[i] = id;
@@ -401,7 +402,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   }
   __syncthreads();
   // 16 lanes per active expert, a token each
-  for (int i = tid; i < nact * kFewTokens; i += kThreads) {
+  for (int i = tid; i < nact * kCols; i += kThreads) {
     const int act = i >> 4, t = i & 15, col = s_col[i];
     const uint32_t has = (uint32_t)(ballot(col != 255) >> (lane & 48)) & 0xFFFFu;
     const int n = __popc(has & ((1u << t) - 1u)), ne = __popc(has), first = __builtin_ctz(has);
@@ -409,9 +410,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     s_idx[i] = (uint8_t)n;
     s_wt[i] = col != 255 ? s_tw[t * kt + col] * (a.w2_gs ? a.w2_gs[e] : 1.0f) : 0.0f;
     // h rows in token order; past the last, the first again
-    if (col != 255) s_slot[act * kFewTokens + n] = (uint16_t)(t * kt + col);
-    const int c0 = s_col[act * kFewTokens + first];
-    if (t >= ne) s_slot[act * kFewTokens + t] = (uint16_t)(first * kt + c0);
+    if (col != 255) s_slot[act * kCols + n] = (uint16_t)(t * kt + col);
+    const int c0 = s_col[act * kCols + first];
+    if (t >= ne) s_slot[act * kCols + t] = (uint16_t)(first * kt + c0);
     if (t == 0) s_en[act] = e | (ne << 16);
   }
   __syncthreads();
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       }
       const int act = item / npt, pt = item - act * npt;
       const float cs = s_gs13[act] * s_xs[r16];
-      const int col = s_col[act * kFewTokens + r16];
+      const int col = s_col[act * kCols + r16];
       float h[4];
       float amax = 0.0f;
 #pragma unroll
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   // load (and per part); loads for tokens it does not have collapse to one
   // line.  (Offsets in 32 bits: h is below 2 GB.)
   auto h_rows = [&](int act, int c, int n0, uint64_t (&b)[NB][kHalf]) __attribute__((always_inline)) {
-    const uint2 four = *reinterpret_cast<const uint2*>(s_slot + act * kFewTokens + n0);
+    const uint2 four = *reinterpret_cast<const uint2*>(s_slot + act * kCols + n0);
     const int ne = __builtin_amdgcn_readfirstlane(s_en[act]) >> 16;
     const uint32_t pair[2] = {(uint32_t)__builtin_amdgcn_readfirstlane((int)four.x),
                               (uint32_t)__builtin_amdgcn_readfirstlane((int)four.y)};
@@ -622,8 +623,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     u = there(u);
     h_rows(u.act, u.c, 0, b);
     if (MODE == 0) {
-      const int col = s_col[u.act * kFewTokens + r16];
-      const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[u.act * kFewTokens];
+      const int col = s_col[u.act * kCols + r16];
+      const uint32_t slot = col != 255 ? (uint32_t)(r16 * kt + col) : s_slot[u.act * kCols];
       const uint32_t o = slot * (uint32_t)(I >> 4) + u.c * 16 + 4 * q;
       x = gload<uint32_t>((GPtr)a.hexp, o);
     }
@@ -763,10 +764,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         const bool counts = cu.act < nact;
         if (k + 1 < cur.n) cu = next_unit(cu);
         const int ne = __builtin_amdgcn_readfirstlane(s_en[act]) >> 16;
-        const int idx = s_idx[act * kFewTokens + r16];
+        const int idx = s_idx[act * kCols + r16];
         // (0: not this token's expert, or a unit that only stands in)
-        float cs = counts ? s_wt[act * kFewTokens + r16] : 0.0f;
-        const bool chosen = counts && s_col[act * kFewTokens + r16] != 255;
+        float cs = counts ? s_wt[act * kCols + r16] : 0.0f;
+        const bool chosen = counts && s_col[act * kCols + r16] != 255;
         turn_pair(w2[k], my_turn, turn);
         _Float16 f4[4];
         if constexpr (MODE == 0) {

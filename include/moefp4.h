@@ -253,13 +253,14 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
 /* A whole mixture-of-experts layer on bfloat16 x: moe_fp4_gate, then
  * moe_fp4_forward with the ids and weights it gives (p->E counts the routed
  * experts and the g->shared last ones, p->top_k = g->top_k + g->shared).
- * Up to 16 tokens of BF16 activations (and H <= 6144, top_k <= 16) run in two
- * launches: router logits, then one persistent kernel for selection, FC1, FC2
- * and the weighted sum.  That form keeps h to at least 11 significant bits
- * between FC1 and FC2 (moe_fp4_forward rounds it to bfloat16); all its waits
- * are bounded, and if one ever exceeded its bound (0.3 s of its own running
- * time), the workspace's second word is nonzero and the result is not valid.  Other sizes and formats run
- * moe_fp4_gate and moe_fp4_forward one after the other.
+ * Up to 8 tokens (2 with group32 weights) of BF16 activations (and H <= 6144,
+ * top_k <= 16) run in two launches: router logits, then one persistent kernel
+ * for selection, FC1, FC2 and the weighted sum.  That form keeps h to at least
+ * 11 significant bits between FC1 and FC2 (moe_fp4_forward rounds it to
+ * bfloat16); all its waits are bounded, and if one ever exceeded its bound
+ * (0.3 s of its own running time), the workspace's second word is nonzero and
+ * the result is not valid.  Other sizes and formats run moe_fp4_gate and
+ * moe_fp4_forward one after the other.
  * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
  * rows); topk_ids / topk_w [T, top_k] receive the selection, NULL if it is

@@ -1,6 +1,6 @@
 """The whole layer (moe_fp4_layer) against a plain FP64 implementation, with
-a bound on every element worked out from the arithmetic (moe_plain.layer): at
-most 16 tokens in the two-launch form (h to 11 bits or more), more tokens as
+a bound on every element worked out from the arithmetic (moe_plain.layer): up
+to FEW tokens in the two-launch form (h to 11 bits or more), more tokens as
 gate + forward (h to bfloat16)."""
 
 import numpy as np
@@ -15,6 +15,7 @@ from test_gpu_gate import grid_inputs, plain_gate
 pytestmark = pytest.mark.gpu
 
 HREL = {16: mp.U16, 32: 2.0 ** -17}
+FEW = {16: 8, 32: 2}
 
 
 class Layer:
@@ -47,8 +48,10 @@ class Layer:
                               None if bias is None else bias.astype(np.float64), shared=shared, **kw)
         assert np.array_equal(ids.cpu().numpy(), rids)
         assert np.allclose(wts.cpu().numpy(), rw, rtol=1024 * mp.U32, atol=0)
+        if hrel is None:
+            hrel = HREL[self.gran] if T <= FEW[self.gran] else mp.UBF
         ref, bound = mp.layer(self.x[:T], rids, rw, self.w13, self.w13_sf, self.w13_gs, self.w2, self.w2_sf,
-                              self.w2_gs, self.gran, order, HREL[self.gran] if hrel is None else hrel)
+                              self.w2_gs, self.gran, order, hrel)
         got = f32.cpu().numpy().astype(np.float64)
         err = np.abs(got - ref)
         rms = max(np.sqrt(np.mean(ref ** 2)), 1e-30)
@@ -71,7 +74,9 @@ def test_few_tokens(shape, gran):
     L = Layer(E, H, I, gran, 1, gs=gran == 16)
     bias = (0.05 * np.random.default_rng(2).standard_normal(E - shared)).astype(np.float32)
     L.check(1, k, shared)
+    L.check(2, k, shared, bias=bias)
     L.check(3, k, shared, order="up_gate", scoring="sigmoid", renormalize=True, scale=2.5)
+    L.check(8, k, shared, bias=bias, renormalize=True)
     L.check(16, k, shared, bias=bias, scoring="sigmoid")
 
 
@@ -161,23 +166,24 @@ def test_workspace_holds_anything_and_results_repeat():
         assert int(ws[4:8].view(torch.int32)) == 0
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("gran,T", [(16, 4), (32, 2), (32, 4)])
+def test_captured_and_replayed(gran, T):
     require_gpu()
-    L = Layer(16, 1024, 512, 32, 10)
-    x, gw = L.args(4, 0)
+    L = Layer(16, 1024, 512, gran, 10)
+    x, gw = L.args(T, 0)
     other = torch.roll(x, 1, 0).contiguous()
-    want = [moe.layer(v, gw, 3, *L.d, 32) for v in (x, other)]
+    want = [moe.layer(v, gw, 3, *L.d, gran) for v in (x, other)]
     buf = x.clone()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        out = moe.layer(buf, gw, 3, *L.d, 32)
+        out = moe.layer(buf, gw, 3, *L.d, gran)
     for k in range(6):
         buf.copy_((x, other)[k & 1])
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[k & 1])
-        moe.layer(x, gw, 2, *L.d, 32)
+        moe.layer(x, gw, 2, *L.d, gran)
 
 
 def test_two_streams_at_once():
