@@ -494,8 +494,8 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
   const bool few = p->T <= moefp4::kProjectFew;
-  P->x16 = take(few ? Tg * p->K * 2 : p->gran_k == 16 ? T * p->K * 2 : 0);
-  P->xs = take(p->gran_k == 16 ? T * 4 : 0);
+  P->x16 = take(few ? Tg * p->K * 2 : 0);
+  P->xs = take(few && p->gran_k == 16 ? T * 4 : 0);
   P->ku = p->adapters > 0 ? moefp4::project_u_parts(p->T, p->K, p->rank) : 1;
   P->u = take(p->adapters > 0 ? P->ku * T * p->rank * 4 : 0);
   const int parts = few || T == 0 ? 1 : moefp4::project_gemm_plan(p->T, p->N, p->K).parts;

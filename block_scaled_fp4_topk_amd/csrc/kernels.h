@@ -163,8 +163,8 @@ struct ProjectArgs {
   const float* scale;     // [L]
   void* out;
   // workspace
-  uint16_t* x16;  // x as the products read it (fp16 * 2**-p for group16)
-  float* xs;      // group16: 2**p [T]
+  uint16_t* x16;  // few tokens: x as the products read it (fp16 * 2**-p for group16)
+  float* xs;      // few tokens, group16: 2**p [T]
   float* u;       // [ku][T, R]
   int ku;
   float* part;    // [parts][T, N] of the tiled product

@@ -2,19 +2,21 @@
 // requests beside it: y[t] = W x[t] + s_l B_l (A_l x[t]), l = the token's
 // adapter (none for ids outside [0, L)).
 //
-//  1. project_prep: x as the products read it, and for few tokens the low-rank
-//     activations u = s_l A_l x (one workgroup per token and 4 ranks).
-//     group16 weights multiply in fp16, x as fp16 * 2**-p (exact down to 2**-24
-//     of the row's maximum); group32 weights in bfloat16, x as it is.
-//     (More tokens: grouped by adapter as the router groups by expert, and
-//     project_shrink computes u with matrix instructions.)
+//  1. up to 128 tokens, project_prep: x in the order project_few's lanes read,
+//     for group16 weights as fp16 * 2**-p (exact down to 2**-24 of the row's
+//     maximum), for group32 as it is, and the low-rank activations u =
+//     s_l A_l x (one workgroup per token and 4 ranks).  (More tokens: grouped
+//     by adapter as the router groups by expert, and project_shrink computes u
+//     with matrix instructions.)
 //  2. up to 128 tokens, project_few: the FP4 stream bounds it (an N x K matrix
 //     is read once for N K / 2 bytes).  A workgroup owns 16 output rows, its 8
 //     waves an eighth of K each; the weights come as whole 128-byte lines into
 //     registers, all requested before the first is used.
-//     more, project_gemm: matrix instructions bound it.  128 rows x 128 tokens
-//     per workgroup; the weights are decoded once per workgroup into LDS,
-//     beside x's tile, double-buffered.
+//     more, project_gemm: matrix instructions bound it, and the LDS that feeds
+//     them.  256 rows x 256 tokens per workgroup where that fills the chip;
+//     the weights are decoded once per workgroup into LDS, beside x's tile,
+//     double-buffered.  Both formats multiply in bfloat16 there, x as it is (an
+//     E2M1 code times an E4M3 scale has 6 significant bits: exact).
 //  u stays FP32 up to the product with B: added in FP32 (few), or split into a
 //  high and a low bfloat16 (16 bits) for the matrix instructions (gemm).
 //  An adapter's product is added to its own tokens only (not multiplied by
@@ -53,9 +55,9 @@ __device__ __forceinline__ size_t frag_at(int t, int k, int K) {
   return ((((size_t)(t >> 4) * (K >> 8) + c) * 8 + j) * 64 + q * 16 + (t & 15)) * 8;
 }
 
-// One token's row by 256 threads.  F16: to fp16 * 2**-p with *scale = 2**p;
-// FRAG: in fragment order, else in place order.
-template <bool F16, bool FRAG>
+// One token's row, in that order, by 256 threads.  F16: as fp16 * 2**-p, with
+// xs = 2**p.
+template <bool F16>
 __device__ __forceinline__ void prep_row(const ProjectArgs& a, int t, uint32_t* s_max) {
   const int tid = threadIdx.x, K = a.K;
   const uint16_t* row = a.x + (size_t)t * K;
@@ -96,8 +98,7 @@ __device__ __forceinline__ void prep_row(const ProjectArgs& a, int t, uint32_t* 
         w[j] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
       }
     }
-    const size_t at = FRAG ? frag_at(t, i, K) : (size_t)t * K + i;
-    *reinterpret_cast<uint4*>(a.x16 + at) = uint4{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<uint4*>(a.x16 + frag_at(t, i, K)) = uint4{w[0], w[1], w[2], w[3]};
   }
 }
 
@@ -140,13 +141,13 @@ __device__ __forceinline__ void shrink_dot(const ProjectArgs& a, int t, int r0, 
 
 // Workgroups [0, prep): a token's row each; then (shrink) one per token and
 // 4 ranks.
-template <bool F16, bool FRAG>
+template <bool F16>
 __global__ __launch_bounds__(256) void project_prep_kernel(ProjectArgs a, int prep) {
   __shared__ uint32_t s_max[4];
   __shared__ float s_red[4 * kShrinkRanks];
   const int b = blockIdx.x;
   if (b < prep) {
-    prep_row<F16, FRAG>(a, b, s_max);
+    prep_row<F16>(a, b, s_max);
   } else {
     const int nr = a.R / kShrinkRanks, i = b - prep;
     shrink_dot(a, i / nr, (i % nr) * kShrinkRanks, s_red);
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
 // ---------------------------------------------------------------------------
 // 2b. many tokens
 
-constexpr int kTile = 128;  // weight rows per workgroup
+constexpr int kTile = 128;  // weight rows per workgroup (256 x 256 tiles: 256)
 constexpr int kGK = 64;     // K elements per stage
 
 // LDS rows of 128 bytes; 16-byte segment s of row r sits at s ^ ((r >> 1) & 7),
@@ -498,35 +499,63 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
   }
 }
 
+// Eight E2M1 codes times an E4M3 scale -> bfloat16, exact (6 significant bits):
+// multiplied as floats, whose upper halves are the result.
+__device__ __forceinline__ u32x4 dq8_scaled_bf16(uint32_t codes, float scale) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  const v2f p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0),
+                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
+                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2),
+                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3)};
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(f2u(p[i][1] * scale), f2u(p[i][0] * scale), 0x07060302u);
+  return v;
+}
+
 // 16 bytes per lane from memory to consecutive places in LDS.
 __device__ __forceinline__ void direct_load(const uint16_t* src, uint8_t* lds) {
   __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
 }
 
-// TT: tokens per workgroup, 128 (waves of 64 rows x 64 tokens) or 64 (32 x 64).
+// TT: tokens per workgroup, 256 (x 256 rows, 8 waves of 128 rows x 64 tokens),
+// 128 (x 128 rows, 4 waves of 64 x 64) or 64 (x 128, 32 x 64).  The larger a
+// wave's tile, the fewer LDS bytes per product: 12 reads of 1 KB for 32 matrix
+// instructions at 256, 8 for 16 at 128, where LDS (128 bytes per cycle) and not
+// the matrix units would be full.  N = 4096, K = 6144, group32: 8192 tokens 345
+// us (1.2 PFLOP/s) at 256, 451 us at 128, 605 us at 64; 2048 tokens, which fill
+// half the chip at 256, 173, 118 and 155 us.
 // blockIdx.y: the part of K (stages [y * per, + per)); with more than one part
 // the products go to a.part as float32, which project_sum adds up.
 //
 // Two ways to the next stage.  TT = 64, where few workgroups hide each other's
 // waits: x, codes and scales through registers, two stages ahead, with a
 // barrier that leaves the loads in flight (N = 4096, K = 6144, 256 tokens: 29
-// us against 62 us with direct loads).  TT = 128, where the traffic through LDS
-// and the number of requests count: x by direct loads to LDS one stage ahead,
-// the weights of two stages per load (8192 tokens: 411 us against 446 us).
+// us against 62 us with direct loads).  Else, where the traffic through LDS and
+// the number of requests count: x by direct loads to LDS one stage ahead, the
+// weights of two stages per load.
 template <int MODE, int TT>
-__global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int row_tiles, int per) {
-  constexpr int NI = TT == 128 ? 4 : 2;  // 16-row tiles of a wave
-  constexpr int XD = TT / 32;            // 16-byte pieces of x per thread and stage
-  constexpr bool DIRECT = TT == 128;
+__global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void project_gemm_kernel(ProjectArgs a, int row_tiles, int per) {
+  constexpr int RW = TT == 256 ? 256 : kTile;  // weight rows per workgroup
+  constexpr int NW = RW / 32;                  // waves
+  constexpr int NH = TT == 256 ? 2 : 1;        // a wave's rows: NH times NI 16-row tiles
+  constexpr int NI = TT == 64 ? 2 : 4;
+  constexpr int NP = TT == 256 ? 2 : 1, NJ = 4 / NP;  // its 64 tokens: NP times NJ 16-token tiles
+  constexpr int XD = TT / NW / 8;              // 16-byte pieces of x per thread and stage
+  constexpr bool DIRECT = TT != 64;
   // (x's two buffers are objects of their own: reads of one do not wait for
   // direct loads into the other)
-  __shared__ __attribute__((aligned(16))) uint8_t s_x0[TT * 128], s_x1[TT * 128], s_w[2][kTile * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x0[TT * 128], s_x1[TT * 128], s_w[2][RW * 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K, N = a.N, T = a.T;
-  const int n0 = (blockIdx.x % row_tiles) * kTile, t0 = (blockIdx.x / row_tiles) * TT;
-  const int wn = TT == 128 ? (wave & 1) * 64 : wave * 32, wt = TT == 128 ? (wave >> 1) * 64 : 0;
-  const uint16_t* xsrc = MODE == 0 ? a.x16 : a.x;
+  // TT = 256: tiles in order of tokens, an eighth of them per XCD, so that
+  // workgroups that share x share an L2 (8192 tokens 345 us against 354 us; the
+  // smaller tiles lose 1 to 4% that way)
+  const int nt = gridDim.x, xcd = blockIdx.x & 7;
+  const int tile = TT == 256 ? xcd * (nt >> 3) + min(xcd, nt & 7) + (blockIdx.x >> 3) : blockIdx.x;
+  const int n0 = (tile % row_tiles) * RW, t0 = (tile / row_tiles) * TT;
+  const int wn = TT == 64 ? wave * 32 : (wave & 1) * 64 * NH, wt = TT == 64 ? 0 : (wave >> 1) * 64;
   const int s_begin = blockIdx.y * per, s_end = min(K / kGK, s_begin + per);
 
   // x: eight whole 128-byte rows per instruction (rows past T repeat the last
@@ -535,9 +564,9 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
   uint32_t xat[XD];
 #pragma unroll
   for (int i = 0; i < XD; ++i) {
-    const int r = TT / 4 * wave + 8 * i + (lane >> 3);
+    const int r = TT / NW * wave + 8 * i + (lane >> 3);
     // (direct loads land in lane order: the swizzle is in what they fetch)
-    xr[i] = xsrc + (size_t)min(t0 + r, T - 1) * K + 8 * (DIRECT ? (lane & 7) ^ pswz(r) : lane & 7);
+    xr[i] = a.x + (size_t)min(t0 + r, T - 1) * K + 8 * (DIRECT ? (lane & 7) ^ pswz(r) : lane & 7);
     xat[i] = r * 128 + 16 * ((lane & 7) ^ pswz(r));
   }
   // weights: thread = (row, half of the stage's 32 bytes), with the scales of its 32 K
@@ -565,17 +594,19 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       u32x4 v;
-      if constexpr (MODE == 0) v = __builtin_bit_cast(u32x4, dq8_f16(r.c[j], e4m3_to_h2((r.s >> (8 * (j >> 1))) & 0xFFu)));
+      if constexpr (MODE == 0) v = dq8_scaled_bf16(r.c[j], e4m3_to_f32((r.s >> (8 * (j >> 1))) & 0xFFu));
       else v = __builtin_bit_cast(u32x4, dq8_bf16(r.c[j], ue8m0_to_f32(r.s)));
       *reinterpret_cast<u32x4*>(s_w[buf] + wat + 16 * ((4 * half + j) ^ wsz)) = v;
     }
   };
 
-  v4f acc[NI][4];
+  v4f acc[NH][NP][NI][NJ];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int h = 0; h < NH; ++h)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[h][j / NJ][i][j % NJ] = v4f{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](int buf) __attribute__((always_inline)) {
     const uint8_t *sx = buf ? s_x1 : s_x0, *sw = s_w[buf];
 #pragma unroll
@@ -587,19 +618,18 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
         B[j] = *reinterpret_cast<const u32x4*>(sx + r * 128 + 16 * ((4 * ks + q) ^ pswz(r)));
       }
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = wn + 16 * i + r16;
-        const u32x4 A = *reinterpret_cast<const u32x4*>(sw + r * 128 + 16 * ((4 * ks + q) ^ pswz(r)));
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (MODE == 0)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, A), __builtin_bit_cast(v8h, B[j]),
-                                                               acc[i][j], 0, 0, 0);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, A),
-                                                                __builtin_bit_cast(v8bf, B[j]), acc[i][j], 0, 0, 0);
+        for (int i = 0; i < NI; ++i) {
+          const int r = wn + 16 * (NI * h + i) + r16;
+          const u32x4 A = *reinterpret_cast<const u32x4*>(sw + r * 128 + 16 * ((4 * ks + q) ^ pswz(r)));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v4f& c = acc[h][j / NJ][i][j % NJ];
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, A), __builtin_bit_cast(v8bf, B[j]), c, 0,
+                                                        0, 0);
+          }
         }
-      }
     }
   };
 
@@ -607,7 +637,7 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
     if (DIRECT && s < s_end) {
 #pragma unroll
       for (int i = 0; i < XD; ++i)
-        direct_load(xr[i] + s * kGK, (buf ? s_x1 : s_x0) + (TT / 4 * wave + 8 * i) * 128);
+        direct_load(xr[i] + s * kGK, (buf ? s_x1 : s_x0) + (TT / NW * wave + 8 * i) * 128);
     }
   };
   // The barrier that hands a stage over: with direct loads every wave first
@@ -675,20 +705,26 @@ __global__ __launch_bounds__(256, 2) void project_gemm_kernel(ProjectArgs a, int
 
   const float gs = a.w_gs ? a.w_gs[0] : 1.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int t = t0 + wt + 16 * j + r16;
-    const float cs = gs * (MODE == 0 && t < T ? a.xs[t] : 1.0f);
+  for (int h = 0; h < NH; ++h) {
+    const int nh = n0 + wn + 16 * NI * h;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) acc[i][j] *= cs;
-    if (gridDim.y > 1 && t < T) {
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + wt + 16 * j + r16;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int n = n0 + wn + 16 * i + 4 * q;
-        if (n < N) *reinterpret_cast<v4f*>(a.part + ((size_t)blockIdx.y * T + t) * N + n) = acc[i][j];
+      for (int i = 0; i < NI; ++i) acc[h][j / NJ][i][j % NJ] *= gs;
+      if (gridDim.y > 1 && t < T) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int n = nh + 16 * i + 4 * q;
+          if (n < N) *reinterpret_cast<v4f*>(a.part + ((size_t)blockIdx.y * T + t) * N + n) = acc[h][j / NJ][i][j % NJ];
+        }
       }
     }
+    if (gridDim.y == 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) adapt_and_store<NI, NJ>(a, acc[h][p], t0 + wt + 16 * NJ * p, nh);
+    }
   }
-  if (gridDim.y == 1) adapt_and_store<NI, 4>(a, acc, t0 + wt, n0 + wn);
 }
 
 // out = the sum of the parts, in order, and the adapters' part: 16 tokens x 256
@@ -719,11 +755,10 @@ template <int MODE>
 hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
   const bool few = a.T <= kProjectFew;
   const bool dot = a.L > 0 && project_dot(a.T, a.K, a.R);
-  const int prep = few || MODE == 0 ? a.T : 0;
+  const int prep = few ? a.T : 0;
   const int blocks = prep + (dot ? a.T * (a.R / kShrinkRanks) : 0);
   if (blocks > 0) {
-    if (few) hipLaunchKernelGGL((project_prep_kernel<MODE == 0, true>), dim3(blocks), dim3(256), 0, s, a, prep);
-    else hipLaunchKernelGGL((project_prep_kernel<MODE == 0, false>), dim3(blocks), dim3(256), 0, s, a, prep);
+    hipLaunchKernelGGL(project_prep_kernel<MODE == 0>, dim3(blocks), dim3(256), 0, s, a, prep);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -751,9 +786,10 @@ hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
     else launch_few_tokens<MODE, 8>(a, s);
   } else {
     const ProjectGemm g = project_gemm_plan(a.T, a.N, a.K);
-    const int rt = (a.N + kTile - 1) / kTile;
+    const int rows = g.tt == 256 ? 256 : kTile, rt = (a.N + rows - 1) / rows;
     const dim3 grid(rt * ((a.T + g.tt - 1) / g.tt), g.parts);
-    if (g.tt == 128) hipLaunchKernelGGL((project_gemm_kernel<MODE, 128>), grid, dim3(256), 0, s, a, rt, g.per);
+    if (g.tt == 256) hipLaunchKernelGGL((project_gemm_kernel<MODE, 256>), grid, dim3(512), 0, s, a, rt, g.per);
+    else if (g.tt == 128) hipLaunchKernelGGL((project_gemm_kernel<MODE, 128>), grid, dim3(256), 0, s, a, rt, g.per);
     else hipLaunchKernelGGL((project_gemm_kernel<MODE, 64>), grid, dim3(256), 0, s, a, rt, g.per);
     if (g.parts > 1) {
       const hipError_t err = hipGetLastError();
@@ -766,12 +802,20 @@ hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// 128 tokens per workgroup where that fills the chip twice over (two
-// workgroups per CU), else 64, and K in parts of at least 8 stages.
+// 64 tokens per workgroup, and K in parts of at least 8 stages, where 128 would
+// not fill the chip twice over (two workgroups per CU); beyond, rounds of 512
+// tiles at 128 against rounds of 256 four times as large at 256, which take 1.5
+// times as long (118 us and 173 us a round at N = 4096, K = 6144).
 ProjectGemm project_gemm_plan(long long T, long long N, long long K) {
   ProjectGemm g;
   const long long rt = (N + kTile - 1) / kTile;
-  g.tt = rt * ((T + 127) / 128) >= 512 ? 128 : 64;
+  const long long t128 = rt * ((T + 127) / 128), t256 = (N + 255) / 256 * ((T + 255) / 256);
+  g.tt = t128 < 512 ? 64 : 3 * ((t256 + 255) / 256) <= 2 * ((t128 + 511) / 512) ? 256 : 128;
+  if (g.tt == 256) {
+    g.per = (int)(K / kGK);
+    g.parts = 1;
+    return g;
+  }
   const long long tiles = rt * ((T + g.tt - 1) / g.tt), nst = K / kGK;
   long long parts = 512 / tiles;
   parts = parts > nst / 8 ? nst / 8 : parts;

@@ -78,6 +78,16 @@ def test_project(shape, gran):
 
 
 @pytest.mark.parametrize("gran", [16, 32])
+@pytest.mark.parametrize("shape", [(4090, 2032, 256, 5, 24), (4101, 2064, 256, 3, 8), (4101, 2064, 512, 0, 8)],
+                         ids=lambda s: "T%d-N%d-K%d-L%d-R%d" % s)
+def test_many_tokens(shape, gran):
+    """Tiles of 128 x 128 and of 256 x 256, the last of both sides ragged."""
+    require_gpu()
+    T, N, K, L, R = shape
+    Case(T, N, K, gran, L, R, seed=6, mix="sorted" if L == 3 else "each").check()
+
+
+@pytest.mark.parametrize("gran", [16, 32])
 @pytest.mark.parametrize("T", [1, 40, 100, 300])
 def test_no_adapters(T, gran):
     require_gpu()
