@@ -462,7 +462,7 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
 struct ProjectPlan {
   size_t x16, xs, u, part, total;
   bool group;  // u by matrix instructions
-  size_t counts, offsets, sorted, slot_of, tiles, ntiles, flags, hist;
+  size_t ids, counts, offsets, sorted, slot_of, tiles, ntiles, flags, hist;
   int chunk, chunks, ku;
 };
 
@@ -476,8 +476,9 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
   if (p->adapters < 0) return fail(MOEFP4_EINVAL, "adapters must be >= 0, got %d", p->adapters);
   if (p->adapters > 0 && (p->rank <= 0 || p->rank % 8))
     return fail(MOEFP4_EINVAL, "rank must be a positive multiple of 8, got %d", p->rank);
-  if (p->adapters > moefp4::kMaxExperts)
-    return fail(MOEFP4_EUNSUPPORTED, "adapters must be at most %d, got %d", moefp4::kMaxExperts, p->adapters);
+  // (tokens without one are grouped as one more)
+  if (p->adapters >= moefp4::kMaxExperts)
+    return fail(MOEFP4_EUNSUPPORTED, "adapters must be below %d, got %d", moefp4::kMaxExperts, p->adapters);
   if (p->adapters > 0 && p->rank > 128) return fail(MOEFP4_EUNSUPPORTED, "rank must be at most 128, got %d", p->rank);
   if (p->K % 256 || p->N % 16)
     return fail(MOEFP4_EUNSUPPORTED, "K must be a multiple of 256 and N of 16, got K=%lld N=%lld", (long long)p->K,
@@ -503,12 +504,13 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
   P->group = p->adapters > 0 && !moefp4::project_dot(p->T, p->K, p->rank);
   P->chunk = P->chunks = 0;
   if (P->group) {
-    const size_t L = p->adapters;
+    const size_t L = p->adapters + 1;
     // (one workgroup takes 21 us to group 8192 tokens)
     if (p->T > 2048) {
       P->chunk = p->T > moefp4::kRouteSingleMax ? moefp4::route_chunk(p->T) : 1024;
       P->chunks = (int)((p->T + P->chunk - 1) / P->chunk);
     }
+    P->ids = take(T * 4);
     P->counts = take(L * 4);
     P->offsets = take((L + 1) * 4);
     P->sorted = take(T * 4);
@@ -753,6 +755,7 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
   a.ku = P.ku;
   a.part = at<float>(workspace, P.part);
   if (P.group) {
+    a.ids = at<int32_t>(workspace, P.ids);
     a.route.counts = at<int32_t>(workspace, P.counts);
     a.route.offsets = at<int32_t>(workspace, P.offsets);
     a.route.sorted_assign = at<int32_t>(workspace, P.sorted);
@@ -763,6 +766,7 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
     a.route.nchunks = P.chunks;
     a.route.chunk = P.chunk;
     a.route.hist = P.chunks ? at<int32_t>(workspace, P.hist) : nullptr;
+    if (p->T > moefp4::kProjectFew) a.order = a.route.sorted_assign;
   }
   st = hip_status(moefp4::launch_project(a, stream), "project");
   return st == MOEFP4_OK ? ok() : st;

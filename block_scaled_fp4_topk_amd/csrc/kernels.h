@@ -169,6 +169,8 @@ struct ProjectArgs {
   int ku;
   float* part;    // [parts][T, N] of the tiled product
   RouteOut route; // u by matrix instructions: tokens grouped by adapter, tiles of 32
+  int32_t* ids;   // [T] what they are grouped by
+  const int32_t* order;  // [T] tokens in that order (route.sorted_assign), or null
 };
 // The tiled product: tokens per workgroup, parts of K and their 64-element
 // stages.

@@ -154,6 +154,13 @@ __global__ __launch_bounds__(256) void project_prep_kernel(ProjectArgs a, int pr
   }
 }
 
+// The adapters to group the tokens by: L for tokens without one, which come
+// last.
+__global__ __launch_bounds__(256) void project_ids_kernel(ProjectArgs a) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t < a.T) a.ids[t] = (unsigned)a.id[t] < (unsigned)a.L ? a.id[t] : a.L;
+}
+
 // u of many tokens with matrix instructions: the tokens grouped by adapter (the
 // router's stable grouping), a tile of up to 32 tokens of one adapter per
 // workgroup, K split over its 8 waves and, where there are few tiles, over
@@ -168,6 +175,7 @@ __global__ __launch_bounds__(512, NT >= 8 ? 2 : 4) void project_shrink_kernel(Pr
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K, R = a.R;
   const int l = a.route.tiles[2 * blockIdx.x], m0 = a.route.tiles[2 * blockIdx.x + 1];
+  if (l >= a.L) return;
   const int ne = a.route.counts[l], oe = a.route.offsets[l];
   int tok[2];
 #pragma unroll
@@ -401,22 +409,31 @@ constexpr int kGK = 64;     // K elements per stage
 // so that the 16 rows a lane group reads touch all 64 banks.
 __device__ __forceinline__ int pswz(int r) { return (r >> 1) & 7; }
 
-// One wave's 16 NJ tokens from t0 on x 16 NI rows from n0 on (lane: token r16 of
-// each 16, rows 4 q .. + 3 of each 16): the adapters that occur among the
+// The token at place t of the order that the tiled product takes them in:
+// grouped by adapter, where they have been grouped for u, so that a tile's
+// tokens share theirs (8192 tokens of 16 adapters of rank 64 in random order,
+// N = 4096, K = 6144: ORDERED us against UNORDERED us).
+__device__ __forceinline__ int token_at(const ProjectArgs& a, int t) { return a.order ? a.order[t] : t; }
+
+// One wave's 16 NJ tokens from place t0 on x 16 NI rows from n0 on (lane: token
+// r16 of each 16, rows 4 q .. + 3 of each 16): the adapters that occur among the
 // tokens added, one after the other, and the result stored.  u enters as two
 // bfloat16 parts; a token takes its own adapter's product and nothing of the
 // others'.
 template <int NI, int NJ>
 __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[NI][NJ], int t0, int n0) {
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4, N = a.N;
+  int tok[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int t = t0 + 16 * j + r16;
+    tok[j] = t < a.T ? token_at(a, t) : -1;
+  }
   if (a.L > 0) {
     int id[NJ];
     uint64_t left[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int t = t0 + 16 * j + r16;
-      id[j] = t < a.T ? a.id[t] : -1;
-    }
+    for (int j = 0; j < NJ; ++j) id[j] = tok[j] >= 0 ? a.id[tok[j]] : -1;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) left[j] = __ballot((unsigned)id[j] < (unsigned)a.L && q == 0);
     for (;;) {
@@ -449,7 +466,7 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
         for (int j = 0; j < NJ; ++j) {
           u[j][0] = u[j][1] = v4f{0.f, 0.f, 0.f, 0.f};
           if (id[j] == l && r < a.R) {
-            const float* p = a.u + (size_t)(t0 + 16 * j + r16) * a.R + r;
+            const float* p = a.u + (size_t)tok[j] * a.R + r;
             u[j][0] = *reinterpret_cast<const v4f*>(p);
             u[j][1] = *reinterpret_cast<const v4f*>(p + 4);
           }
@@ -482,13 +499,12 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int t = t0 + 16 * j + r16;
-    if (t >= a.T) continue;
+    if (tok[j] < 0) continue;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int n = n0 + 16 * i + 4 * q;
       if (n >= N) continue;  // (N is a multiple of 16)
-      const size_t at = (size_t)t * N + n;
+      const size_t at = (size_t)tok[j] * N + n;
       const v4f v = o[i][j];
       if (a.out_f32)
         *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
@@ -566,7 +582,7 @@ __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void project_gemm_kernel(
   for (int i = 0; i < XD; ++i) {
     const int r = TT / NW * wave + 8 * i + (lane >> 3);
     // (direct loads land in lane order: the swizzle is in what they fetch)
-    xr[i] = a.x + (size_t)min(t0 + r, T - 1) * K + 8 * (DIRECT ? (lane & 7) ^ pswz(r) : lane & 7);
+    xr[i] = a.x + (size_t)token_at(a, min(t0 + r, T - 1)) * K + 8 * (DIRECT ? (lane & 7) ^ pswz(r) : lane & 7);
     xat[i] = r * 128 + 16 * ((lane & 7) ^ pswz(r));
   }
   // weights: thread = (row, half of the stage's 32 bytes), with the scales of its 32 K
@@ -763,9 +779,12 @@ hipError_t launch_mode(const ProjectArgs& a, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   if (a.L > 0 && !dot) {
-    hipError_t err = launch_route(a.id, a.T, a.L, 32, a.route, s);
+    hipLaunchKernelGGL(project_ids_kernel, dim3((a.T + 255) / 256), dim3(256), 0, s, a);
+    hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const dim3 grid((a.T + 31) / 32 + a.L, a.ku);
+    err = launch_route(a.ids, a.T, a.L + 1, 32, a.route, s);
+    if (err != hipSuccess) return err;
+    const dim3 grid((a.T + 31) / 32 + a.L + 1, a.ku);
     if (a.R <= 16) hipLaunchKernelGGL(project_shrink_kernel<1>, grid, dim3(512), 0, s, a);
     else if (a.R <= 32) hipLaunchKernelGGL(project_shrink_kernel<2>, grid, dim3(512), 0, s, a);
     else if (a.R <= 64) hipLaunchKernelGGL(project_shrink_kernel<4>, grid, dim3(512), 0, s, a);

@@ -294,7 +294,7 @@ moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* by
  * int32, scale [adapters] float32, all device memory; x, w, w_sf, lora_a,
  * lora_b and out 16-byte aligned, the workspace 256-byte aligned.  K a
  * multiple of 32 and rank a positive multiple of 8 (EINVAL otherwise); K a
- * multiple of 256 and N of 16, rank up to 128, up to 512 adapters, T below
+ * multiple of 256 and N of 16, rank up to 128, up to 511 adapters, T below
  * 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38 (EUNSUPPORTED
  * otherwise).
  * Enqueued on `stream`. */

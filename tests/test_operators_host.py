@@ -168,7 +168,7 @@ def project_ws(L, p):
     (dict(T=0), m.OK),
     (dict(T=1, N=16, K=256, adapters=0, rank=0), m.OK),
     (dict(adapters=0, rank=-3), m.OK),                         # rank is ignored without adapters
-    (dict(adapters=512, rank=128), m.OK),
+    (dict(adapters=511, rank=128), m.OK),
     (dict(T=8192, adapters=16, rank=64), m.OK),
     (dict(T=(1 << 24) - 1, N=16, K=256), m.OK),
     (dict(T=-1), m.EINVAL),
@@ -182,12 +182,12 @@ def project_ws(L, p):
     (dict(rank=12), m.EINVAL),
     (dict(K=288), m.EUNSUPPORTED),
     (dict(N=4104), m.EUNSUPPORTED),
-    (dict(adapters=513), m.EUNSUPPORTED),
+    (dict(adapters=512), m.EUNSUPPORTED),
     (dict(rank=136), m.EUNSUPPORTED),
     (dict(T=1 << 24), m.EUNSUPPORTED),
     (dict(N=1 << 20, K=1 << 12), m.EUNSUPPORTED),
     (dict(N=1 << 62, K=1 << 62), m.EUNSUPPORTED),
-    (dict(N=1 << 19, K=256, adapters=512, rank=16), m.EUNSUPPORTED),
+    (dict(N=1 << 19, K=256, adapters=511, rank=24), m.EUNSUPPORTED),
     (dict(T=1 << 23, N=1 << 20, K=256, adapters=0), m.EUNSUPPORTED),
 ])
 def test_project_sizes(L, kw, status):
