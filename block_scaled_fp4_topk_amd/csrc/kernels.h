@@ -150,8 +150,12 @@ int cu_count();
 // us, 128 tokens 23.7 against 27.6; N = 1968, K = 2048: 128 tokens 11.7 against
 // 15.2.  (256 tokens in the few form: 117 us against 35.)
 constexpr int kProjectFew = 128;
-// u by dot products (every token reads its adapter's A for itself)?
-inline bool project_dot(long long T, long long K, long long R) { return T <= 64 || T * K * R <= (120ll << 20); }
+// u by dot products (every token reads its adapter's A for itself), or with
+// matrix instructions, the tokens grouped by adapter?  Whole calls, dot / grouped,
+// us: K = 6144, rank 16, 512 tokens (50 M) 68/70, 700 (69 M) 106/100; rank 64,
+// 128 tokens (50 M) 41/55, 200 (79 M) 58/53; K = 2048, rank 8, 512 tokens (8 M)
+// 27/39, 4096 (67 M) 69/72, 8192 (134 M) 117/100.
+inline bool project_dot(long long T, long long K, long long R) { return T * K * R <= (64ll << 20); }
 struct ProjectArgs {
   int T, N, K, L, R;   // L = 0: no adapters
   bool g16, out_f32;

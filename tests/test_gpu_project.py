@@ -78,6 +78,14 @@ def test_project(shape, gran):
 
 
 @pytest.mark.parametrize("gran", [16, 32])
+def test_few_tokens_grouped_by_adapter(gran):
+    """Long rows of high rank: few tokens' low-rank activations with matrix instructions too."""
+    require_gpu()
+    Case(40, 64, 16384, gran, 3, 128, seed=7).check()
+    Case(200, 48, 4096, gran, 4, 96, seed=8).check()
+
+
+@pytest.mark.parametrize("gran", [16, 32])
 @pytest.mark.parametrize("shape", [(4090, 2032, 256, 5, 24), (4101, 2064, 256, 3, 8), (4101, 2064, 512, 0, 8)],
                          ids=lambda s: "T%d-N%d-K%d-L%d-R%d" % s)
 def test_many_tokens(shape, gran):
