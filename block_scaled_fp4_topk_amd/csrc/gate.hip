@@ -57,18 +57,19 @@ constexpr int kGK = 64;     // K elements per stage
 // so that the 16 rows a lane group reads touch all 64 banks.
 __device__ __forceinline__ int gswz(int r) { return (r >> 1) & 7; }
 
-// Stages rows [0, 128) x K [k0, k0 + 64) of a row-major bf16 matrix; wave w
-// loads rows 32 w .. + 32, eight whole rows per instruction.  Rows past the
+// Stages rows [0, 128) x K [k0, k0 + 64) of a row-major bf16 matrix; each of
+// the NW waves loads 128 / NW rows, eight whole ones per instruction.  Rows past the
 // last one repeat it (their results are not stored); K past H is zero.
+template <int NW>
 __device__ __forceinline__ void gate_stage(const uint16_t* __restrict__ src, int row0, int rows, int H, int k0,
                                            uint8_t* lds, int wave, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 32 * wave + 8 * i + (lane >> 3);
+  for (int i = 0; i < 16 / NW; ++i) {
+    const int r = 128 / NW * wave + 8 * i + (lane >> 3);
     const int seg = (lane & 7) ^ gswz(r);
     const int k = k0 + 8 * seg;
     const int row = min(row0 + r, rows - 1);
-    uint8_t* base = lds + (32 * wave + 8 * i) * 128;
+    uint8_t* base = lds + (128 / NW * wave + 8 * i) * 128;
     if (k < H)
       __builtin_amdgcn_global_load_lds(src + (size_t)row * H + k, base, 16, 0, 0);
     else
@@ -77,9 +78,10 @@ __device__ __forceinline__ void gate_stage(const uint16_t* __restrict__ src, int
 }
 
 // One 128 x 128 tile over K stages [blockIdx.z * per, + per): part z of the
-// logits.  4 waves of 64 experts x 64 tokens; WP planes of W.
-template <int WP>
-__global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ x,
+// logits.  NW waves of 64 (4 of them) or 32 (8) experts x 64 tokens; WP planes of
+// W.
+template <int WP, int NW>
+__global__ __launch_bounds__(64 * NW) void gate_gemm_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ x,
                                                         int T, int E, int ld, int H, int per,
                                                         float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint8_t s[2][(WP + 1) * kTile * 128];
@@ -89,16 +91,17 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
   const int t0 = blockIdx.x * kTile, e0 = blockIdx.y * kTile;
   const int nst = (H + kGK - 1) / kGK;
   const int s0 = blockIdx.z * per, s1 = min(nst, s0 + per);
-  const int we = (wave & 1) * 64, wt = (wave >> 1) * 64;
+  constexpr int NI = 16 / NW;  // 16-expert tiles of a wave
+  const int we = (wave % (NW / 2)) * 16 * NI, wt = wave / (NW / 2) * 64;
   auto stage = [&](int c, uint8_t* b) __attribute__((always_inline)) {
-    gate_stage(x, t0, T, H, c * kGK, b, wave, lane);
+    gate_stage<NW>(x, t0, T, H, c * kGK, b, wave, lane);
 #pragma unroll
     for (int p = 0; p < WP; ++p)
-      gate_stage(w + (size_t)p * E * H, e0, E, H, c * kGK, b + (p + 1) * kTile * 128, wave, lane);
+      gate_stage<NW>(w + (size_t)p * E * H, e0, E, H, c * kGK, b + (p + 1) * kTile * 128, wave, lane);
   };
-  v4f acc[4][4];
+  v4f acc[NI][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   if (s0 < s1) stage(s0, s[0]);
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
 #pragma unroll
       for (int p = 0; p < WP; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NI; ++i) {
           const int r = we + 16 * i + r16;
           const v8bf A = *reinterpret_cast<const v8bf*>(b + (p + 1) * kTile * 128 + r * 128 +
                                                         16 * ((4 * ks + q) ^ gswz(r)));
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(256) void gate_gemm_kernel(const uint16_t* __restri
     const int t = t0 + wt + 16 * j + r16;
     if (t >= T) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int e = e0 + we + 16 * i + 4 * q;
       if (e < ld) *reinterpret_cast<v4f*>(out + (size_t)t * ld + e) = acc[i][j];
     }
@@ -236,9 +239,9 @@ hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool 
                          static_cast<const float*>(w), n, planes);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;
-      hipLaunchKernelGGL(gate_gemm_kernel<3>, grid, dim3(256), 0, s, planes, x, T, E, p.ld, H, p.per, part);
+      hipLaunchKernelGGL((gate_gemm_kernel<3, 8>), grid, dim3(512), 0, s, planes, x, T, E, p.ld, H, p.per, part);
     } else {
-      hipLaunchKernelGGL(gate_gemm_kernel<1>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(w), x, T, E, p.ld,
+      hipLaunchKernelGGL((gate_gemm_kernel<1, 8>), grid, dim3(512), 0, s, static_cast<const uint16_t*>(w), x, T, E, p.ld,
                          H, p.per, part);
     }
   }
