@@ -167,12 +167,7 @@ __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restric
     else l[i] = sum[i];
   }
   const int kt = g.top_k + g.shared;
-  auto again = [&](int e) __attribute__((always_inline)) {
-    float v = 0.0f;
-    for (int s = 0; s < nparts; ++s) v += part[((size_t)s * T + t) * (64 * NI) + e];
-    return v;
-  };
-  gate_select<NI>(l, g, lane, again, [&](int j, int id, float w) __attribute__((always_inline)) {
+  gate_select<NI>(l, g, lane, [&](int j, int id, float w) __attribute__((always_inline)) {
     ids[(size_t)t * kt + j] = id;
     wts[(size_t)t * kt + j] = w;
   });

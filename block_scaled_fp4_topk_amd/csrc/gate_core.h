@@ -79,54 +79,43 @@ __device__ __forceinline__ void take_top(S (&sel)[NI], int n, int lane, F&& take
 }
 
 // The 64-bit selection of gate_select's biased form: the expert and score of
-// place j to lane j.  It runs for few tokens and is written to be small (the
-// code of a launch comes from memory too): every round reads the logits again,
-// logit_of(e), and forms the scores anew.
-template <int NI, class L>
-__device__ __forceinline__ void gate_select64(const GateSel& g, int lane, L&& logit_of, int* expert, float* score) {
+// place j to lane j.  (No loop over the lane's experts that is not unrolled: the
+// arrays would be indexed in memory, for which every launch of the few-token
+// layer, with or without such a token, pays 6 to 11 us at its start.)
+template <int NI>
+__device__ __forceinline__ void gate_select64(const float (&l)[NI], const float (&bias)[NI], const GateSel& g, int lane,
+                                              int* expert, float* score) {
   const double kNone = -__builtin_inf();
   const bool softmax = g.scoring == MOEFP4_SCORE_SOFTMAX;
-  const int e0 = lane * NI, e1 = min(e0 + NI, g.E);
-  double m = 0, inv = 1, sum = 0;
-  if (softmax) {
-    m = kNone;
-#pragma unroll 1
-    for (int e = e0; e < e1; ++e) {
-      const float v = logit_of(e);
-      if (__builtin_isfinite(v)) m = max_of(m, (double)v);
-    }
-    m = wave_max(m);
+  double m = kNone, sum = 0, p[NI], sel[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    if (lane * NI + i < g.E && __builtin_isfinite(l[i])) m = max_of(m, (double)l[i]);
+  if (softmax) m = wave_max(m);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const bool fin = lane * NI + i < g.E && __builtin_isfinite(l[i]);
+    const double x = exp(softmax ? (double)l[i] - m : -(double)l[i]);
+    p[i] = !fin ? 0.0 : softmax ? x : 1.0 / (1.0 + x);
+    sum += p[i];
   }
-  uint32_t taken = 0;
+  const double inv = softmax ? 1.0 / wave_sum(sum) : 1.0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    p[i] *= inv;
+    const double s = p[i] + (double)bias[i];
+    sel[i] = lane * NI + i < g.E && __builtin_isfinite(l[i]) && s > kNone ? s : kNone;
+  }
   int my = -1;
   float mine = 0.0f;
-  // round -1 sums the softmax, round j takes place j
-#pragma unroll 1
-  for (int j = softmax ? -1 : 0; j < g.top_k; ++j) {
-    double best = kNone, bp = 0;
-    int be = 0;
-#pragma unroll 1
-    for (int e = e0; e < e1; ++e) {
-      const float v = logit_of(e);
-      if (!__builtin_isfinite(v)) continue;
-      const double x = exp(softmax ? (double)v - m : -(double)v);
-      const double p = softmax ? x * inv : 1.0 / (1.0 + x);
-      sum += p;
-      const double s = p + (double)g.bias[e];
-      if (!((taken >> (e - e0)) & 1) && s > best) best = s, bp = p, be = e;
-    }
-    if (j < 0) {
-      inv = 1.0 / wave_sum(sum);
-      continue;
-    }
-    const double top = wave_max(best);
-    if (!(top > kNone)) break;
-    const int who = __builtin_ctzll(ballot(best == top));
-    const float ps = __shfl((float)bp, who, 64);
-    const int we = __shfl(be, who, 64);
-    if (lane == who) taken |= 1u << (we - e0);
-    if (lane == j) mine = ps, my = we;
-  }
+  take_top<NI>(sel, g.top_k, lane, [&](int j, int who, int wi, double) __attribute__((always_inline)) {
+    float ps = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (i == wi) ps = (float)p[i];
+    const float at = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ps), who));
+    if (lane == j) mine = at, my = who * NI + wi;
+  });
   *expert = my;
   *score = mine;
 }
@@ -149,12 +138,12 @@ __device__ __forceinline__ void gate_select64(const GateSel& g, int lane, L&& lo
 // selected again in 64 bits.  (All in 64 bits measured 19.5 us against 11.9 us
 // for 8192 tokens of 256 experts.)
 //
-// l: the lane's logits; logit_of(e): expert e's, read again.
+// l: the lane's logits.
 // emit(j, id, weight) is called by lane j with place j's expert and its
 // weight: the score, divided by the selected scores' sum if renorm, times
 // scale.
-template <int NI, class L, class F>
-__device__ __forceinline__ void gate_select(const float (&l)[NI], const GateSel& g, int lane, L&& logit_of, F&& emit) {
+template <int NI, class F>
+__device__ __forceinline__ void gate_select(const float (&l)[NI], const GateSel& g, int lane, F&& emit) {
   const float kNone = -__builtin_inff();
   const bool softmax = g.scoring == MOEFP4_SCORE_SOFTMAX, biased = g.bias != nullptr;
   float p[NI], sel[NI], bias[NI];
@@ -199,7 +188,7 @@ __device__ __forceinline__ void gate_select(const float (&l)[NI], const GateSel&
     ps = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ps), who));
     if (lane == j && j < g.top_k) mine = ps, my = who * NI + wi;
   });
-  if (narrow) gate_select64<NI>(g, lane, logit_of, &my, &mine);
+  if (narrow) gate_select64<NI>(l, bias, g, lane, &my, &mine);
   float f = g.scale;
   if (g.renorm) {
     const float total = wave_sum(lane < g.top_k ? mine : 0.0f);

@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       const float4 v = *reinterpret_cast<const float4*>(row + lane * NI + i);
       l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
     }
-    gate_select<NI>(l, a.g, lane, [&](int e) __attribute__((always_inline)) { return row[e]; }, emit);
+    gate_select<NI>(l, a.g, lane, emit);
     for (int j = lane; j < a.g.shared; j += 64) {
       s_ids[t * kt + a.g.top_k + j] = a.g.E + j;
       s_tw[t * kt + a.g.top_k + j] = 1.0f;
