@@ -191,7 +191,8 @@ def _arg(t, name, dtypes, shape, device):
 def _first(t, name, dtypes, dims):
     """The argument the others are measured by: its type, number of dimensions, layout and (the current) device."""
     import torch
-    _dev(t, name, dtypes)
+    if _dev(t, name, dtypes) is None:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
     if t.device.index != torch.cuda.current_device():
@@ -458,7 +459,8 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
     u8, f32 = (torch.uint8,), (torch.float32,)
     E, kt = routed + shared, top_k + shared
-    _dev(w13, "w13", u8)
+    if _dev(w13, "w13", u8) is None:
+        raise TypeError("w13 must be a CUDA (HIP) tensor")
     I = w13.shape[1] // 2 if w13.dim() == 3 else 0
     weights = (_arg(w13, "w13", u8, (E, 2 * I, H // 2), dev), _arg(w13_sf, "w13_sf", u8, (E, 2 * I, H // gran_k), dev),
                _arg(w13_gs, "w13_gs", f32, (E,), dev), _arg(w2, "w2", u8, (E, H, I // 2), dev),

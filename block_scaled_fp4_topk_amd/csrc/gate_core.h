@@ -135,8 +135,8 @@ __device__ __forceinline__ void gate_select64(const float (&l)[NI], const float 
 // behind the last one) is wider than 2^-20 of the larger of 1 and the score,
 // several times what expf, the division and the addition can be off together;
 // a token with a narrower gap (about 1 in 300 of 256 sigmoid scores) is
-// selected again in 64 bits.  (All in 64 bits measured 19.5 us against 11.9 us
-// for 8192 tokens of 256 experts.)
+// selected again in 64 bits.  (All in 64 bits: 26 us against 17 us for 8192
+// tokens of 256 experts.)
 //
 // l: the lane's logits.
 // emit(j, id, weight) is called by lane j with place j's expert and its

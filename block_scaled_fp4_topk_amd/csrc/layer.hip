@@ -153,8 +153,8 @@ __device__ __forceinline__ void drain_memory() { asm volatile("s_waitcnt vmcnt(0
 // A wave-uniform pointer to memory in scalar registers, for loads with a
 // 32-bit per-lane offset.  (The address space is kept in the type: a generic
 // pointer's loads also count as LDS accesses, and the waits for LDS would then
-// wait for every weight in flight: measured 91 us instead of XX us for one
-// token of the 256-expert layer.)
+// wait for every weight in flight: 62 us instead of 60 us for one token of the
+// 256-expert layer.)
 typedef const __attribute__((address_space(1))) uint8_t* GPtr;
 __device__ __forceinline__ GPtr uniform_ptr(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);

@@ -174,7 +174,8 @@ moefp4_status moe_fp4_gate_workspace_bytes(const moefp4_gate* g, int64_t T, int6
  * float32, all device memory, x and w 16-byte aligned, the workspace 256-byte
  * aligned.  H a multiple of 8, 1 <= top_k <= E, shared >= 0 (EINVAL
  * otherwise); E + shared <= 512, top_k <= 64, T <= 2^24, T*E and T*H below
- * 2^40 and H <= 2^24 (EUNSUPPORTED otherwise).  Enqueued on `stream`. */
+ * 2^40 and H <= 2^24 (EUNSUPPORTED otherwise).  No output overlaps an input.
+ * Enqueued on `stream`. */
 moefp4_status moe_fp4_gate(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, const void* x, const void* w,
                            const float* bias, int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes,
                            hipStream_t stream);
@@ -264,8 +265,8 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
  * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
  * rows); topk_ids / topk_w [T, top_k] receive the selection, NULL if it is
- * not wanted; the rest as for moe_fp4_forward.  The workspace's first word
- * then holds the number of places without an expert. */
+ * not wanted; the rest as for moe_fp4_forward; out overlaps no input.  The
+ * workspace's first word then holds the number of places without an expert. */
 moefp4_status moe_fp4_layer_workspace_bytes(const moefp4_problem* p, const moefp4_gate* g, size_t* bytes);
 moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const void* x, const void* gate_w,
                             const float* bias, const uint8_t* w13, const uint8_t* w13_sf, const float* w13_gs,
@@ -296,8 +297,7 @@ moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* by
  * multiple of 32 and rank a positive multiple of 8 (EINVAL otherwise); K a
  * multiple of 256 and N of 16, rank up to 128, up to 511 adapters, T below
  * 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38 (EUNSUPPORTED
- * otherwise).
- * Enqueued on `stream`. */
+ * otherwise).  out overlaps no input.  Enqueued on `stream`. */
 moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8_t* w, const uint8_t* w_sf,
                               const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
                               const float* scale, void* out, void* workspace, size_t ws_bytes, hipStream_t stream);

@@ -234,6 +234,9 @@ def test_binding_takes_gpu_tensors_only():
         m.layer(x, w, 2, u8(4, 512, 128), u8(4, 512, 16), None, u8(4, 256, 128), u8(4, 256, 16), None, 16)
     with pytest.raises(TypeError):
         m.project(x, u8(16, 128), u8(16, 16), None, 16)
+    for call in (lambda: m.gate(None, w, 2), lambda: m.project(None, u8(16, 128), u8(16, 16), None, 16)):
+        with pytest.raises(TypeError):
+            call()
 
 
 def test_make_gate():
