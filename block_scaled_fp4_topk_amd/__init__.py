@@ -188,34 +188,40 @@ def _arg(t, name, dtypes, shape, device):
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _first(t, name, dtypes, dims):
-    """The argument the others are measured by: its type, number of dimensions, layout and (the current) device."""
-    import torch
+def _dims(t, name, dtypes, dims):
+    """A tensor whose sizes others are measured by: its type, number of dimensions and layout."""
     if _dev(t, name, dtypes) is None:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.device.index != torch.cuda.current_device():
+    return t.shape
+
+
+def _current(t):
+    """The tensor's device, which must be the current one."""
+    import torch
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return t.device
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for work on ``stream`` (allocated on it, so that the allocator does not hand it to another one)."""
-    import torch
+def _empty(like, shape, dtype, stream):
+    """Memory on like's device for work on ``stream`` (allocated on it, so that the allocator does not hand it to
+    another one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(workspace, need, device, stream):
+def _scratch(workspace, need, like, stream):
     import torch
     if workspace is None:
-        return _empty(max(need, 256), torch.uint8, device, stream)
+        return _empty(like, max(need, 256), torch.uint8, stream)
     _dev(workspace, "workspace", (torch.uint8,))
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if workspace.device != like.device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
     return workspace
 
 
@@ -295,10 +301,9 @@ def make_gate(top_k, scoring="softmax", renormalize=False, scale=1.0, shared=0, 
 def _router_args(x, gate_w, bias):
     """(T, E, H, w_fmt, device, addresses) of a router's tensors, checked."""
     import torch
-    dev = _first(x, "x", (torch.bfloat16,), 2)
     wt = (torch.bfloat16, torch.float32)
-    _dev(gate_w, "gate_w", wt)
-    (T, H), E = x.shape, len(gate_w)
+    (T, H), (E, _) = _dims(x, "x", (torch.bfloat16,), 2), _dims(gate_w, "gate_w", wt, 2)
+    dev = _current(x)
     at = x.data_ptr(), _arg(gate_w, "gate_w", wt, (E, H), dev), _arg(bias, "bias", (torch.float32,), (E,), dev)
     return T, E, H, GATE_W_F32 if gate_w.dtype is torch.float32 else GATE_W_BF16, dev, at
 
@@ -318,10 +323,10 @@ def gate(x, gate_w, top_k, bias=None, scoring="softmax", renormalize=False, scal
     need = _gate_need(top_k, shared, scoring, w_fmt, T, E, H)
     shape = (T, top_k + shared)
     if topk_ids is None:
-        topk_ids = _empty(shape, torch.int32, dev, stream)
+        topk_ids = _empty(x, shape, torch.int32, stream)
     if topk_w is None:
-        topk_w = _empty(shape, torch.float32, dev, stream)
-    ws = _scratch(workspace, need, dev, stream)
+        topk_w = _empty(x, shape, torch.float32, stream)
+    ws = _scratch(workspace, need, x, stream)
     _check(_lib.moe_fp4_gate(ctypes.byref(g), T, E, H, *at, _arg(topk_ids, "topk_ids", (torch.int32,), shape, dev),
                              _arg(topk_w, "topk_w", (torch.float32,), shape, dev), ws.data_ptr(), ws.numel(),
                              _raw_stream(stream, dev)))
@@ -459,9 +464,7 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
     u8, f32 = (torch.uint8,), (torch.float32,)
     E, kt = routed + shared, top_k + shared
-    if _dev(w13, "w13", u8) is None:
-        raise TypeError("w13 must be a CUDA (HIP) tensor")
-    I = w13.shape[1] // 2 if w13.dim() == 3 else 0
+    I = _dims(w13, "w13", u8, 3)[1] // 2
     weights = (_arg(w13, "w13", u8, (E, 2 * I, H // 2), dev), _arg(w13_sf, "w13_sf", u8, (E, 2 * I, H // gran_k), dev),
                _arg(w13_gs, "w13_gs", f32, (E,), dev), _arg(w2, "w2", u8, (E, H, I // 2), dev),
                _arg(w2_sf, "w2_sf", u8, (E, H, I // gran_k), dev), _arg(w2_gs, "w2_gs", f32, (E,), dev))
@@ -474,8 +477,8 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
                _LAYOUTS.get(w_layout, w_layout))
     need = _layer_need(dev, top_k, shared, scoring, w_fmt, *problem)
     if out is None:
-        out = _empty((T, H), out_dtype, dev, stream)
-    ws = _scratch(workspace, need, dev, stream)
+        out = _empty(x, (T, H), out_dtype, stream)
+    ws = _scratch(workspace, need, x, stream)
     _check(_lib.moe_fp4_layer(ctypes.byref(Problem(*problem)), ctypes.byref(g), *at, *weights,
                               _arg(out, "out", (out_dtype,), (T, H), dev),
                               _arg(topk_ids, "topk_ids", (torch.int32,), (T, kt), dev),
@@ -494,11 +497,10 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     None.  Returns out [T, N] bfloat16 (default) or float32."""
     import torch
     u8, f32, bf = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
-    dev = _first(x, "x", bf, 2)
-    _dev(w, "w", u8)
+    (T, K), (N, _) = _dims(x, "x", bf, 2), _dims(w, "w", u8, 2)
+    dev = _current(x)
     if gran_k not in (16, 32):
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
-    (T, K), N = x.shape, len(w)
     at = (x.data_ptr(), _arg(w, "w", u8, (N, K // 2), dev), _arg(w_sf, "w_sf", u8, (N, K // gran_k), dev),
           _arg(w_gs, "w_gs", f32, (1,), dev))
     adapters = rank = 0
@@ -506,10 +508,9 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     if lora_a is not None:
         if lora_b is None or lora_id is None or lora_scale is None:
             raise ValueError("lora_a, lora_b, lora_id and lora_scale go together")
-        _dev(lora_a, "lora_a", bf)
-        if lora_a.dim() != 3 or len(lora_a) < 1:
+        adapters, rank, _ = _dims(lora_a, "lora_a", bf, 3)
+        if adapters < 1:
             raise ValueError("lora_a must be [L, R, K] with L >= 1")
-        adapters, rank = lora_a.shape[:2]
         lora = (_arg(lora_a, "lora_a", bf, (adapters, rank, K), dev), _arg(lora_b, "lora_b", bf, (adapters, N, rank), dev),
                 _arg(lora_id, "lora_id", (torch.int32,), (T,), dev),
                 _arg(lora_scale, "lora_scale", f32, (adapters,), dev))
@@ -522,8 +523,8 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     linear = (T, N, K, gran_k, OUT_F32 if out_dtype is torch.float32 else OUT_BF16, adapters, rank)
     need = _project_need(*linear)
     if out is None:
-        out = _empty((T, N), out_dtype, dev, stream)
-    ws = _scratch(workspace, need, dev, stream)
+        out = _empty(x, (T, N), out_dtype, stream)
+    ws = _scratch(workspace, need, x, stream)
     _check(_lib.moe_fp4_project(ctypes.byref(Linear(*linear)), *at, *lora, _arg(out, "out", (out_dtype,), (T, N), dev),
                                 ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return out
