@@ -156,6 +156,8 @@ __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restric
   const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
   using vec = typename std::conditional<NI == 1, float, float __attribute__((ext_vector_type(NI)))>::type;
+  float bias[NI];
+  gate_bias<NI>(g, lane, bias);
   vec sum = 0.0f;
   const float* row = part + (size_t)t * (64 * NI) + lane * NI;
 #pragma unroll 8
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(256) void gate_select_kernel(const float* __restric
     else l[i] = sum[i];
   }
   const int kt = g.top_k + g.shared;
-  gate_select<NI>(l, g, lane, [&](int j, int id, float w) __attribute__((always_inline)) {
+  gate_select<NI>(l, bias, g, lane, [&](int j, int id, float w) __attribute__((always_inline)) {
     ids[(size_t)t * kt + j] = id;
     wts[(size_t)t * kt + j] = w;
   });

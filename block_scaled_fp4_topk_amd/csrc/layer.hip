@@ -322,8 +322,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   // ---- selection, by every workgroup for itself
   for (int i = tid; i < kMaxExperts; i += kThreads) s_rank[i] = 0;
   for (int i = tid; i < kActive * kCols / 4; i += kThreads) reinterpret_cast<uint32_t*>(s_col)[i] = ~0u;
-  for (int t = wave; t < T; t += kWaves) {
+  static_assert(kFewTokens <= kWaves, "a wave per token");
+  if (wave < T) {
+    const int t = wave;
     const float* row = a.logits + (size_t)t * a.ld;
+    float bias[NI];
+    gate_bias<NI>(a.g, lane, bias);
     auto emit = [&](int j, int id, float w) __attribute__((always_inline)) {
       s_ids[t * kt + j] = id;
       s_tw[t * kt + j] = w;
@@ -335,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       const float4 v = *reinterpret_cast<const float4*>(row + lane * NI + i);
       l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
     }
-    gate_select<NI>(l, a.g, lane, emit);
+    gate_select<NI>(l, bias, a.g, lane, emit);
     for (int j = lane; j < a.g.shared; j += 64) {
       s_ids[t * kt + a.g.top_k + j] = a.g.E + j;
       s_tw[t * kt + a.g.top_k + j] = 1.0f;
