@@ -9,9 +9,10 @@
 //     by adapter as the router groups by expert, and project_shrink computes u
 //     with matrix instructions.)
 //  2. up to 128 tokens, project_few: the FP4 stream bounds it (an N x K matrix
-//     is read once for N K / 2 bytes).  A workgroup owns 16 output rows, its 8
-//     waves an eighth of K each; the weights come as whole 128-byte lines into
-//     registers, all requested before the first is used.
+//     is read once for N K / 2 bytes), and the reading of x by every workgroup.
+//     A workgroup owns 16 or 32 output rows, its 8 waves an eighth of K each;
+//     the weights come as whole 128-byte lines into registers, the wave's first
+//     one to three chunks requested before any is used.
 //     more, project_gemm: matrix instructions bound it, and the LDS that feeds
 //     them.  256 rows x 256 tokens per workgroup where that fills the chip;
 //     the weights are decoded once per workgroup into LDS, beside x's tile,
@@ -259,42 +260,47 @@ struct WTile {
   uint32_t s;
 };
 
-// NG: 16-token groups; NC: chunks of K in flight per wave.
-template <int MODE, int NG, int NC>
+// NG: 16-token groups; NC: chunks of K in flight per wave; NR: 16-row tiles of a
+// workgroup.
+template <int MODE, int NG, int NC, int NR>
 __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
   constexpr int GP = NG < 4 ? NG : 4;  // groups summed over the waves at a time
-  __shared__ float4 s_red[8][GP][64];
+  constexpr int ROWS = 16 * NR, TS = 512 / ROWS;  // rows, and tokens that the threads store at a time
+  __shared__ float4 s_red[8][GP][NR][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[8][2048];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K;
-  const int n0 = blockIdx.x * 16, nch = K >> 8;
+  const int n0 = blockIdx.x * ROWS, nch = K >> 8;
   const uint32_t rowb = K >> 1, rows = MODE == 0 ? K >> 4 : K >> 5;
-  const uint8_t* codes = a.w + (size_t)n0 * rowb;
-  const uint8_t* sf = a.w_sf + (size_t)n0 * rows;
   const uint32_t o0 = (lane >> 3) * rowb + 16 * (lane & 7), step8 = 8 * rowb;
   const uint32_t f0 = r16 * rows + (MODE == 0 ? 4 * q : 2 * q);
   // (no load is conditional: chunks past the end repeat the last one, and
-  // their products are not added)
-  auto load = [&](int c, WTile& w) __attribute__((always_inline)) {
+  // their products are not added; a tile past the last row repeats the first)
+  auto load = [&](int c, WTile (&w)[NR]) __attribute__((always_inline)) {
     c = c < nch ? c : nch - 1;
-    w.c[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + o0 + c * 128));
-    w.c[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + o0 + step8 + c * 128));
-    if (MODE == 0) w.s = *reinterpret_cast<const uint32_t*>(sf + f0 + c * 16);
-    else w.s = *reinterpret_cast<const uint16_t*>(sf + f0 + c * 8);
+#pragma unroll
+    for (int t = 0; t < NR; ++t) {
+      const size_t n = n0 + 16 * t < a.N ? n0 + 16 * t : n0;
+      const uint8_t *codes = a.w + n * rowb, *sf = a.w_sf + n * rows;
+      w[t].c[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + o0 + c * 128));
+      w[t].c[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + o0 + step8 + c * 128));
+      if (MODE == 0) w[t].s = *reinterpret_cast<const uint32_t*>(sf + f0 + c * 16);
+      else w[t].s = *reinterpret_cast<const uint16_t*>(sf + f0 + c * 8);
+    }
   };
-  WTile w[NC];
+  WTile w[NC][NR];
 #pragma unroll
   for (int i = 0; i < NC; ++i) load(wave + 8 * i, w[i]);
 
-  // the adapters' part of output (row rn, token rt + 32 p): for few groups
+  // the adapters' part of output (row rn, token rt + TS p): for few groups
   // while the weights come, else behind the products
-  const int rn = tid & 15, rt = tid >> 4;
-  constexpr int NP = (NG + 1) / 2;
+  const int rn = tid & (ROWS - 1), rt = tid / ROWS;
+  constexpr int NP = (16 * NG + TS - 1) / TS;
   auto adapted = [&](int p) __attribute__((always_inline)) {
     float s = 0.0f;
-    const int t = rt + 32 * p;
-    if (a.L > 0 && t < a.T) {
+    const int t = rt + TS * p;
+    if (a.L > 0 && t < a.T && n0 + rn < a.N) {
       const int l = a.id[t];
       if ((unsigned)l < (unsigned)a.L) {
         const uint16_t* B = a.b + ((size_t)l * a.N + n0 + rn) * a.R;
@@ -311,9 +317,11 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
 #pragma unroll
   for (int p = 0; p < NP; ++p) lora[p] = NG <= 4 ? adapted(p) : 0.0f;
 
-  v4f acc[NG];
+  v4f acc[NR][NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) acc[g] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NR; ++t)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[t][g] = v4f{0.f, 0.f, 0.f, 0.f};
   uint8_t* turn = s_turn[wave];
   const int wr = lane >> 3, seg = lane & 7;
   const uint32_t tw0 = wr * 128 + 16 * (seg ^ (wr >> 1)), tw1 = (wr + 8) * 128 + 16 * (seg ^ ((wr + 8) >> 1));
@@ -330,27 +338,30 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = c0 + wave + 8 * i;
-      asm volatile("" : "+v"(w[i].c[0]), "+v"(w[i].c[1]), "+v"(w[i].s));
-      // the codes turned into operand order through the wave's own LDS
-      *reinterpret_cast<u32x4*>(turn + tw0) = w[i].c[0];
-      *reinterpret_cast<u32x4*>(turn + tw1) = w[i].c[1];
-      const u32x4 c4[2] = {*reinterpret_cast<const u32x4*>(turn + tr0), *reinterpret_cast<const u32x4*>(turn + tr1)};
-      const uint32_t sc = w[i].s;
-      if (c < nch) {
-        u32x4 A[8];
+      u32x4 A[NR][8];
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        asm volatile("" : "+v"(w[i][t].c[0]), "+v"(w[i][t].c[1]), "+v"(w[i][t].s));
+        // the codes turned into operand order through the wave's own LDS
+        *reinterpret_cast<u32x4*>(turn + tw0) = w[i][t].c[0];
+        *reinterpret_cast<u32x4*>(turn + tw1) = w[i][t].c[1];
+        const u32x4 c4[2] = {*reinterpret_cast<const u32x4*>(turn + tr0), *reinterpret_cast<const u32x4*>(turn + tr1)};
+        const uint32_t sc = w[i][t].s;
         if constexpr (MODE == 0) {
           const v2h lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sc, 1.0f, false);
           const v2h hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sc, 1.0f, true);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const _Float16 s = j < 2 ? lo[0] : j < 4 ? lo[1] : j < 6 ? hi[0] : hi[1];
-            A[j] = __builtin_bit_cast(u32x4, dq8_f16(c4[j >> 2][j & 3], v2h{s, s}));
+            A[t][j] = __builtin_bit_cast(u32x4, dq8_f16(c4[j >> 2][j & 3], v2h{s, s}));
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            A[j] = __builtin_bit_cast(u32x4, dq8_bf16(c4[j >> 2][j & 3], ue8m0_to_f32((sc >> (8 * (j >> 2))) & 0xFFu)));
+            A[t][j] = __builtin_bit_cast(u32x4, dq8_bf16(c4[j >> 2][j & 3], ue8m0_to_f32((sc >> (8 * (j >> 2))) & 0xFFu)));
         }
+      }
+      if (c < nch) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           u32x4 (&xb)[8] = x_ahead[(i * NG + g) & 1];
@@ -359,14 +370,16 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
           else load_x(0, i + 1 < NC ? c + 8 : c0 + 8 * NC + wave, x_ahead[(i * NG + g + 1) & 1]);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if constexpr (MODE == 0)
-              acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, A[j]),
-                                                              __builtin_bit_cast(v8h, xb[j]), acc[g], 0, 0, 0);
-            else
-              acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, A[j]),
-                                                               __builtin_bit_cast(v8bf, xb[j]), acc[g], 0, 0, 0);
-          }
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int t = 0; t < NR; ++t) {
+              if constexpr (MODE == 0)
+                acc[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, A[t][j]),
+                                                                   __builtin_bit_cast(v8h, xb[j]), acc[t][g], 0, 0, 0);
+              else
+                acc[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(v8bf, A[t][j]), __builtin_bit_cast(v8bf, xb[j]), acc[t][g], 0, 0, 0);
+            }
         }
       }
       if (c0 + 8 * NC < nch) load(c + 8 * NC, w[i]);
@@ -381,16 +394,21 @@ __global__ __launch_bounds__(512, 2) void project_few_kernel(ProjectArgs a) {
   for (int g0 = 0; g0 < NG; g0 += GP) {
     if (g0 > 0) __syncthreads();  // (the groups before are summed)
 #pragma unroll
-    for (int g = 0; g < GP; ++g) s_red[wave][g][lane] = float4{acc[g0 + g][0], acc[g0 + g][1], acc[g0 + g][2], acc[g0 + g][3]};
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        const v4f v = acc[t][g0 + g];
+        s_red[wave][g][t][lane] = float4{v[0], v[1], v[2], v[3]};
+      }
     __syncthreads();
 #pragma unroll
-    for (int p = g0 / 2; p < (g0 + GP + 1) / 2; ++p) {
-      const int t = rt + 32 * p;
-      if (t >= a.T) continue;
+    for (int p = 16 * g0 / TS; p < (16 * (g0 + GP) + TS - 1) / TS; ++p) {
+      const int t = rt + TS * p;
+      if (t >= a.T || n0 + rn >= a.N) continue;
       float s = 0.0f;
 #pragma unroll
       for (int v = 0; v < 8; ++v)
-        s += reinterpret_cast<const float*>(&s_red[v][(t >> 4) - g0][(t & 15) + 16 * (rn >> 2)])[rn & 3];
+        s += reinterpret_cast<const float*>(&s_red[v][(t >> 4) - g0][rn >> 4][(t & 15) + 16 * ((rn & 15) >> 2)])[rn & 3];
       s = __builtin_fmaf(s, gs * (MODE == 0 ? a.xs[t] : 1.0f), NG <= 4 ? lora[p] : adapted(p));
       const size_t at = (size_t)t * a.N + n0 + rn;
       if (a.out_f32) static_cast<float*>(a.out)[at] = s;
@@ -760,11 +778,22 @@ __global__ __launch_bounds__(256) void project_sum_kernel(ProjectArgs a, int par
   adapt_and_store<4, 1>(a, o, blockIdx.x * 16, n0);
 }
 
+template <int MODE, int NG, int NR>
+void launch_few_rows(const ProjectArgs& a, hipStream_t s) {
+  const dim3 grid((a.N + 16 * NR - 1) / (16 * NR)), block(512);
+  if (a.K <= 2048) hipLaunchKernelGGL((project_few_kernel<MODE, NG, 1, NR>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((project_few_kernel<MODE, NG, NR == 1 ? 3 : NG <= 4 ? 2 : 1, NR>), grid, block, 0, s, a);
+}
+
+// 32 rows per workgroup where 16 would give a CU more than one workgroup: each
+// reads all of x from the L2.  16 / 32 rows, us: N = 6144, K = 6144, group16: 1
+// token 14.4/13.3, 37 tokens 24.3/20.7, 128 tokens 41.4/31.1; N = 16384, K =
+// 4096: 20.3/16.4, 33.3/24.2, 56.5/39.1; N = 4096, K = 6144: 10.0/12.7,
+// 15.9/20.3, 25.5/30.8.
 template <int MODE, int NG>
 void launch_few_tokens(const ProjectArgs& a, hipStream_t s) {
-  const dim3 grid(a.N / 16), block(512);
-  if (a.K <= 2048) hipLaunchKernelGGL((project_few_kernel<MODE, NG, 1>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((project_few_kernel<MODE, NG, 3>), grid, block, 0, s, a);
+  if (a.N > 16 * 256) launch_few_rows<MODE, NG, 2>(a, s);
+  else launch_few_rows<MODE, NG, 1>(a, s);
 }
 
 template <int MODE>

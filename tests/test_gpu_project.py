@@ -78,6 +78,15 @@ def test_project(shape, gran):
 
 
 @pytest.mark.parametrize("gran", [16, 32])
+@pytest.mark.parametrize("K", [256, 2304])
+@pytest.mark.parametrize("T", [1, 17, 37, 128])
+def test_few_tokens_many_rows(T, K, gran):
+    """32 rows per workgroup, the last workgroup with 16."""
+    require_gpu()
+    Case(T, 4112, K, gran, 3, 8, seed=9).check()
+
+
+@pytest.mark.parametrize("gran", [16, 32])
 def test_few_tokens_grouped_by_adapter(gran):
     """Long rows of high rank: few tokens' low-rank activations with matrix instructions too."""
     require_gpu()
