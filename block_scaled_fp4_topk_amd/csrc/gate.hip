@@ -204,7 +204,7 @@ void gate_split_k(int T, int E, int H, bool w_f32, int* per, int* parts) {
 
 GatePlan gate_plan(int T, int E, int H, bool w_f32) {
   GatePlan p;
-  p.dot = T <= kGateDotMax;
+  p.dot = T <= (w_f32 ? kGateDotMaxF32 : kGateDotMax);
   p.per = 0;
   p.parts = 1;
   if (!p.dot) gate_split_k(T, E, H, w_f32, &p.per, &p.parts);

@@ -19,11 +19,15 @@ struct GateSel {
   const float* bias;
 };
 constexpr int kGateMaxTopK = 64;   // one lane per selected expert
-// Most tokens the dot form is used for.  Both forms, with the selection, for
-// 256 experts: H = 6144 10.8 us against 12.1 us for 16 tokens, 13.3 against
-// 12.6 for 32, 17.3 against 13.2 for 64; H = 2048 9.3 against 9.4 for 16, 10.5
-// against 9.6 for 32.
-constexpr int kGateDotMax = 16;
+// Most tokens the dot form is used for, with bfloat16 and with FP32 weights
+// (which the tiled form splits first).  Both forms, dot / tiled, with the
+// selection, for 256 experts, us:
+//                     8 tokens   16         32         64
+//   bf16, H = 6144   10.6/10.8  11.1/10.9  13.4/11.2
+//         H = 2048    9.2/8.6    9.6/8.7   10.6/9.0
+//   FP32, H = 6144   10.7/20.9  11.0/20.8  13.8/21.0  17.5/21.9
+//         H = 2048    9.2/13.0   9.6/12.9  10.6/13.2  13.1/13.9
+constexpr int kGateDotMax = 8, kGateDotMaxF32 = 64;
 
 // Logits of T tokens: one dot product per expert and token (dot), or a tiled
 // product with K split in `parts` of `per` stages.  part_bytes: the logits
