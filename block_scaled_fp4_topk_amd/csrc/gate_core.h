@@ -154,6 +154,13 @@ __device__ __forceinline__ void gate_bias(const GateSel& g, int lane, float (&bi
 // emit(j, id, weight) is called by lane j with place j's expert and its
 // weight: the score, divided by the selected scores' sum if renorm, times
 // scale.
+//
+// The quotient of two scores can be an ordinary number where the scores
+// themselves are below FP32's range (sigmoids of logits below -87, softmax
+// scores beside masked experts that hold all of the mass).  Below a sum of
+// 2^-100 the weights are formed from the logits, relative to the largest
+// selected one: a softmax's scores are e^l times the same factor, and so are
+// sigmoids down there (1 + e^l is 1 to 2^-100).
 template <int NI, class F>
 __device__ __forceinline__ void gate_select(const float (&l)[NI], const float (&bias)[NI], const GateSel& g, int lane,
                                             F&& emit) {
@@ -204,8 +211,20 @@ __device__ __forceinline__ void gate_select(const float (&l)[NI], const float (&
   if (narrow) gate_select64<NI>(l, bias, g, lane, &my, &mine);
   float f = g.scale;
   if (g.renorm) {
-    const float total = wave_sum(lane < g.top_k ? mine : 0.0f);
+    float total = wave_sum(mine);  // (lanes without a place hold 0)
+    if (total < 0x1p-100f) {
+      float z = kNone;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float v = __shfl(l[i], my < 0 ? 0 : my / NI, 64);
+        if (my >= 0 && my % NI == i) z = v;
+      }
+      const float most = wave_max(z);
+      mine = my >= 0 ? expf(z - most) : 0.0f;
+      total = wave_sum(mine);
+    }
     f = total > 0.0f ? f / total : 0.0f;
+    if (!__builtin_isfinite(f)) mine /= total, f = g.scale;  // (the weights are at most the scale)
   }
   if (lane < g.top_k) emit(lane, my, mine * f);
 }

@@ -158,6 +158,9 @@ moefp4_status moe_fp4_route(const moefp4_problem* p, const int32_t* topk_ids,
  * (a bias of -inf masks an expert), is never selected, and a logit that is
  * not finite takes no part in the softmax; places for which no expert is
  * left get id -1 (which route and forward drop and count) and weight 0.
+ * Renormalised weights are the quotients of the scores also where the scores
+ * themselves are too small for FP32 (very negative logits, or a softmax whose
+ * mass lies with masked experts).
  * With a bias the scores are formed and compared in 64 bits. */
 typedef enum moefp4_score { MOEFP4_SCORE_SOFTMAX = 0, MOEFP4_SCORE_SIGMOID = 1 } moefp4_score;
 typedef enum moefp4_gate_fmt { MOEFP4_GATE_W_BF16 = 0, MOEFP4_GATE_W_F32 = 1 } moefp4_gate_fmt;
