@@ -91,6 +91,9 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return u >> 16;
 }
 
+// The largest finite bfloat16.
+constexpr float kBf16Max = 0x1.FEp127f;
+
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) { return u2f(bits16 << 16); }
 
 // silu(z) * u in f32.

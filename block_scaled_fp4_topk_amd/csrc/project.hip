@@ -437,7 +437,8 @@ __device__ __forceinline__ int token_at(const ProjectArgs& a, int t) { return a.
 // r16 of each 16, rows 4 q .. + 3 of each 16): the adapters that occur among the
 // tokens added, one after the other, and the result stored.  u enters as two
 // bfloat16 parts; a token takes its own adapter's product and nothing of the
-// others'.
+// others'.  (The high part is the largest bfloat16 where rounding would make it
+// infinite: a finite u stays finite, and an infinite one is in the low part.)
 template <int NI, int NJ>
 __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[NI][NJ], int t0, int n0) {
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4, N = a.N;
@@ -496,9 +497,8 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
             const float f = u[j][v >> 2][v & 3];
-            hi[v] = (__bf16)f;
-            const float rest = f - (float)hi[v];
-            lo[v] = __builtin_isfinite(rest) ? (__bf16)rest : (__bf16)0.0f;
+            hi[v] = (__bf16)__builtin_amdgcn_fmed3f(f, -kBf16Max, kBf16Max);
+            lo[v] = (__bf16)(f - (float)hi[v]);
           }
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
