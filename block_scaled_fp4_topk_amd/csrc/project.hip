@@ -433,44 +433,58 @@ __device__ __forceinline__ int pswz(int r) { return (r >> 1) & 7; }
 // N = 4096, K = 6144: 437 us against 716 us).
 __device__ __forceinline__ int token_at(const ProjectArgs& a, int t) { return a.order ? a.order[t] : t; }
 
-// One wave's 16 NJ tokens from place t0 on x 16 NI rows from n0 on (lane: token
-// r16 of each 16, rows 4 q .. + 3 of each 16): the adapters that occur among the
-// tokens added, one after the other, and the result stored.  u enters as two
-// bfloat16 parts; a token takes its own adapter's product and nothing of the
-// others'.  (The high part is the largest bfloat16 where rounding would make it
-// infinite: a finite u stays finite, and an infinite one is in the low part.)
-template <int NI, int NJ>
-__device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[NI][NJ], int t0, int n0) {
-  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4, N = a.N;
-  int tok[NJ];
+// The tokens that lane r16 has of each 16 from place t0 on, -1 past the last.
+template <int NJ>
+__device__ __forceinline__ void tokens_at(const ProjectArgs& a, int t0, int (&tok)[NJ]) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int t = t0 + 16 * j + r16;
+    const int t = t0 + 16 * j + (threadIdx.x & 15);
     tok[j] = t < a.T ? token_at(a, t) : -1;
   }
-  if (a.L > 0) {
-    int id[NJ];
-    uint64_t left[NJ];
+}
+
+// One wave's 16 NJ tokens x 16 NI rows from n0 on (lane: token r16 of each 16,
+// rows 4 q .. + 3 of each 16): the adapters that occur among the tokens added to
+// o, one after the other.  u enters as two bfloat16 parts; a token takes its own
+// adapter's product and nothing of the others'.  (The high part is the largest
+// bfloat16 where rounding would make it infinite: a finite u stays finite, and
+// an infinite one is in the low part.)
+//
+// An infinity of B times u's two parts is NaN where their signs differ or the
+// low one is 0, and so is a product past FP32's range.  EXACT: where an
+// adapter's sum is NaN it is formed again from parts of one sign (u / 2, the
+// high one taken off but for 1/64), which give an infinity's own sign, and NaN
+// only where the product is NaN; what is finite counts from the first pass.
+template <int NI, int NJ, bool EXACT>
+__device__ __forceinline__ void add_adapters(const ProjectArgs& a, v4f (&o)[NI][NJ], const int (&tok)[NJ], int n0) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4, N = a.N;
+  int id[NJ];
+  uint64_t left[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) id[j] = tok[j] >= 0 ? a.id[tok[j]] : -1;
+  for (int j = 0; j < NJ; ++j) id[j] = tok[j] >= 0 ? a.id[tok[j]] : -1;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) left[j] = __ballot((unsigned)id[j] < (unsigned)a.L && q == 0);
-    for (;;) {
-      int l = -1;
+  for (int j = 0; j < NJ; ++j) left[j] = __ballot((unsigned)id[j] < (unsigned)a.L && q == 0);
+  for (;;) {
+    int l = -1;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (l < 0 && left[j]) l = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
-      if (l < 0) break;
-      bool some[NJ];
+    for (int j = 0; j < NJ; ++j)
+      if (l < 0 && left[j]) l = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(left[j]));
+    if (l < 0) break;
+    bool some[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const uint64_t mine = __ballot(id[j] == l);
+      some[j] = mine != 0;
+      left[j] &= ~mine;
+    }
+#pragma unroll 1
+    for (int pass = 0;; pass = 1) {
+      const float whole = pass ? 0.5f : 1.0f, off = pass ? 0x1.F8p-1f : 1.0f;  // (1 - 2^-6)
       v4f add[NI][NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint64_t mine = __ballot(id[j] == l);
-        some[j] = mine != 0;
-        left[j] &= ~mine;
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < NI; ++i) add[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-      }
       for (int r0 = 0; r0 < a.R; r0 += 32) {
         const int r = r0 + 8 * q;
         v8bf B[NI];
@@ -496,9 +510,9 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
           v8bf hi, lo;
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
-            const float f = u[j][v >> 2][v & 3];
+            const float f = EXACT ? u[j][v >> 2][v & 3] * whole : u[j][v >> 2][v & 3];
             hi[v] = (__bf16)__builtin_amdgcn_fmed3f(f, -kBf16Max, kBf16Max);
-            lo[v] = (__bf16)(f - (float)hi[v]);
+            lo[v] = (__bf16)(EXACT ? __builtin_fmaf((float)hi[v], -off, f) : f - (float)hi[v]);
           }
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
@@ -507,22 +521,50 @@ __device__ __forceinline__ void adapt_and_store(const ProjectArgs& a, v4f (&o)[N
           }
         }
       }
+      bool odd = false;
+      if constexpr (EXACT) {
+        odd = pass != 0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; v += 2) odd |= id[j] == l && __builtin_isunordered(add[i][j][v], add[i][j][v + 1]);
+      }
+      if (!EXACT || __ballot(odd) == 0) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if (id[j] == l) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) o[i][j] += add[i][j];
+          }
+        break;
+      }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        if (id[j] == l) {
 #pragma unroll
-          for (int i = 0; i < NI; ++i) o[i][j] += add[i][j];
-        }
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            // (of the second pass what is not finite, of the first all but NaN)
+            if (id[j] == l && __builtin_amdgcn_classf(add[i][j][v], pass ? 0x207 : 0x3FC)) o[i][j][v] += add[i][j][v];
+      if (pass) break;
     }
   }
+}
+
+// What a wave holds as above, stored.
+template <int NI, int NJ>
+__device__ __forceinline__ void store_rows(const ProjectArgs& a, const v4f (&o)[NI][NJ], const int (&tok)[NJ], int n0) {
+  const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     if (tok[j] < 0) continue;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int n = n0 + 16 * i + 4 * q;
-      if (n >= N) continue;  // (N is a multiple of 16)
-      const size_t at = (size_t)tok[j] * N + n;
+      if (n >= a.N) continue;  // (N is a multiple of 16)
+      const size_t at = (size_t)tok[j] * a.N + n;
       const v4f v = o[i][j];
       if (a.out_f32)
         *reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at) = v;
@@ -754,9 +796,17 @@ __global__ __launch_bounds__(TT == 256 ? 512 : 256, 2) void project_gemm_kernel(
         }
       }
     }
-    if (gridDim.y == 1) {
+  }
+  if (gridDim.y == 1) {
 #pragma unroll
-      for (int p = 0; p < NP; ++p) adapt_and_store<NI, NJ>(a, acc[h][p], t0 + wt + 16 * NJ * p, nh);
+    for (int p = 0; p < NP; ++p) {
+      int tok[NJ];
+      tokens_at(a, t0 + wt + 16 * NJ * p, tok);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if (a.L > 0) add_adapters<NI, NJ, true>(a, acc[h][p], tok, n0 + wn + 16 * NI * h);
+        store_rows(a, acc[h][p], tok, n0 + wn + 16 * NI * h);
+      }
     }
   }
 }
@@ -767,15 +817,33 @@ __global__ __launch_bounds__(256) void project_sum_kernel(ProjectArgs a, int par
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   const int t = blockIdx.x * 16 + r16, n0 = blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
   if (n0 >= a.N) return;
+  int tok[1];
+  tokens_at(a, blockIdx.x * 16, tok);
   v4f o[4][1];
+  auto sum = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i][0] = v4f{0.f, 0.f, 0.f, 0.f};
-  const float* p = a.part + (size_t)min(t, a.T - 1) * a.N;
+    for (int i = 0; i < 4; ++i) o[i][0] = v4f{0.f, 0.f, 0.f, 0.f};
+    const float* p = a.part + (size_t)min(t, a.T - 1) * a.N;
 #pragma unroll 2
-  for (int z = 0; z < parts; ++z, p += (size_t)a.T * a.N)
+    for (int z = 0; z < parts; ++z, p += (size_t)a.T * a.N)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i][0] += *reinterpret_cast<const v4f*>(p + min(n0 + 16 * i + 4 * q, a.N - 4));
-  adapt_and_store<4, 1>(a, o, blockIdx.x * 16, n0);
+      for (int i = 0; i < 4; ++i) o[i][0] += *reinterpret_cast<const v4f*>(p + min(n0 + 16 * i + 4 * q, a.N - 4));
+  };
+  sum();
+  if (a.L > 0) {
+    // (the test for NaN behind all adapters, and then from the start: in the
+    // chain of their products it costs 300 tokens 1.5 us of 40)
+    add_adapters<4, 1, false>(a, o, tok, n0);
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      odd |= __builtin_isunordered(o[i][0][0], o[i][0][1]) || __builtin_isunordered(o[i][0][2], o[i][0][3]);
+    if (__ballot(odd) != 0) {
+      sum();
+      add_adapters<4, 1, true>(a, o, tok, n0);
+    }
+  }
+  store_rows(a, o, tok, n0);
 }
 
 template <int MODE, int NG, int NR>
