@@ -518,9 +518,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         uint64_t hi = 0, lo = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t b = bf16_bits(h[i]);
+#pragma clang fp contract(off)  // (the low part is of h as rounded, not of its factors)
+          // (the high part stays finite where rounding would not; an infinite h
+          // is in the low one)
+          const uint32_t b = bf16_bits(__builtin_amdgcn_fmed3f(h[i], -kBf16Max, kBf16Max));
           hi |= (uint64_t)b << (16 * i);
-          if (__builtin_isfinite(h[i])) lo |= (uint64_t)bf16_bits(h[i] - bf16_to_f32(b)) << (16 * i);
+          lo |= (uint64_t)bf16_bits(h[i] - bf16_to_f32(b)) << (16 * i);
         }
         if (r16 < T && col != 255) {
           st_agent(a.h + at, hi);
