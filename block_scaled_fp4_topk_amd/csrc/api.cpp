@@ -520,7 +520,8 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
     P->flags = take(64);
     P->hist = take((size_t)P->chunks * (L + 1) * 4);
   }
-  P->total = o;
+  // (never 0: a caller that allocates what it is told has something to pass)
+  P->total = o > 0 ? o : kAlign;
   return MOEFP4_OK;
 }
 

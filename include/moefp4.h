@@ -290,7 +290,7 @@ typedef struct moefp4_linear {
   int32_t gran_k, out_fmt, adapters, rank;
 } moefp4_linear;
 
-/* Workspace of moe_fp4_project. */
+/* Workspace of moe_fp4_project (never 0 bytes: the call needs one). */
 moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* bytes);
 
 /* x [T, K] bfloat16, w [N, K/2], w_sf [N, K/gran], w_gs [1] float32 or NULL,
