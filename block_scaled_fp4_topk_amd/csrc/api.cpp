@@ -403,6 +403,9 @@ moefp4_status gate_check(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, 
   return MOEFP4_OK;
 }
 
+// Workspace of the router: the logits, then the planes of FP32 weights.
+size_t gate_need(const moefp4::GatePlan& p) { return align_up(p.most_bytes) + align_up(p.planes_bytes); }
+
 moefp4::GateSel gate_sel(const moefp4_gate* g, int E, const float* bias) {
   return moefp4::GateSel{E, g->top_k, g->shared, g->scoring, g->renormalize != 0, g->scale, bias};
 }
@@ -430,32 +433,46 @@ moefp4_status layer_plan(const moefp4_problem* p, const moefp4_gate* g, LayerPla
   st = gate_check(g, p->T, p->E - g->shared, p->H, &P->gate);
   if (st != MOEFP4_OK) return st;
   const size_t T = p->T, H = p->H, I = p->I, A = T * p->top_k;
-  P->few = p->T >= 1 && p->T <= (p->gran_k == 16 ? moefp4::kFewTokens : moefp4::kFewTokensG32) &&
-           p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH && p->top_k <= moefp4::kFewMaxK;
+  const int most = p->gran_k == 16 ? moefp4::kFewTokens : moefp4::kFewTokensG32;
+  bool small = p->act_fmt == MOEFP4_ACT_BF16 && p->H <= moefp4::kFewMaxH && p->top_k <= moefp4::kFewMaxK;
   P->nwg = moefp4::cu_count();
   // (launch 2 counts FC2's steps times workgroups in 31 bits)
-  if (P->few && (H / 32) * ((size_t)p->E * (I / 256) / 8 + 1) * P->nwg >= (1ull << 31)) P->few = false;
-  if (P->few && A * I * 4 >= (1ull << 31)) P->few = false;
+  if ((H / 32) * ((size_t)p->E * (I / 256) / 8 + 1) * P->nwg >= (1ull << 31)) small = false;
+  P->few = small && T >= 1 && p->T <= most && A * I * 4 < (1ull << 31);
+  // The total is the most that T or fewer tokens need, so that a workspace
+  // serves the batches below the one it was made for.
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
-  if (P->few) {
+  P->total = 0;
+  if (small) {
+    const size_t t = p->T < most ? T : most, a = t * p->top_k;
     P->ld = p->E - g->shared <= 256 ? 256 : 512;
     P->flags = take(64);
-    P->logits = take(T * P->ld * 4);
-    P->xs = take(P->L.g16_a16 ? T * 4 : 0);
-    P->x16 = take(P->L.g16_a16 ? T * H * 2 : 0);
-    P->h = take(P->L.g16_a16 ? A * I * 2 : A * I * 4);
-    P->hexp = take(P->L.g16_a16 ? A * (I / 16) : 0);
+    P->logits = take(t * P->ld * 4);
+    P->xs = take(P->L.g16_a16 ? t * 4 : 0);
+    P->x16 = take(P->L.g16_a16 ? t * H * 2 : 0);
+    P->h = take(P->L.g16_a16 ? a * I * 2 : a * I * 4);
+    P->hexp = take(P->L.g16_a16 ? a * (I / 16) : 0);
     P->sync = take((size_t)moefp4::few_sync_words(p->H) * 4);
     P->parts = take((size_t)P->nwg * 2 * 512 * 4);
-  } else {
+    P->total = o;
+  }
+  if (!P->few) {
     o = P->L.total;
     P->ids = take(A * 4);
     P->wts = take(A * 4);
-    P->part = take(P->gate.part_bytes);
+    P->part = take(P->gate.most_bytes);
     P->planes = take(P->gate.planes_bytes);
+    // (what of the forward's own shrinks with T: the tiles and counters of its
+    // 16-row form, the chunks of its grouping)
+    const size_t active = A < (size_t)p->E ? A : p->E, tiles = A / 16 + active;
+    o += align_up(tiles * 8) - align_up((size_t)P->L.max_tiles * 8);
+    o += align_up((moefp4::decode_sync_words((int)tiles) + (P->L.g16_a16 ? A : 0)) * 4) -
+         align_up((size_t)P->L.zero_words * 4);
+    o += align_up((size_t)(A > moefp4::kRouteSingleMax ? moefp4::kRouteMaxChunks : 0) * (p->E + 1) * 4) -
+         align_up((size_t)P->L.route_chunks * (p->E + 1) * 4);
+    if (o > P->total) P->total = o;
   }
-  P->total = o;
   return MOEFP4_OK;
 }
 
@@ -490,17 +507,18 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
     return fail(MOEFP4_EUNSUPPORTED,
                 "T must be below 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38, got T=%lld N=%lld K=%lld",
                 (long long)p->T, (long long)p->N, (long long)p->K);
+  // Every size is the most that T or fewer tokens need, so that a workspace
+  // serves the batches below the one it was made for.
   // (few tokens: rows for whole groups of 16, as many as the launch multiplies)
   const size_t T = (size_t)p->T, Tg = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
-  const bool few = p->T <= moefp4::kProjectFew;
-  P->x16 = take(few ? Tg * p->K * 2 : 0);
-  P->xs = take(few && p->gran_k == 16 ? T * 4 : 0);
+  static_assert(moefp4::kProjectFew == 128, "Tg");
+  P->x16 = take(Tg * p->K * 2);
+  P->xs = take(p->gran_k == 16 ? Tg * 4 : 0);
   P->ku = p->adapters > 0 ? moefp4::project_u_parts(p->T, p->K, p->rank) : 1;
-  P->u = take(p->adapters > 0 ? P->ku * T * p->rank * 4 : 0);
-  const int parts = few || T == 0 ? 1 : moefp4::project_gemm_plan(p->T, p->N, p->K).parts;
-  P->part = take(parts > 1 ? (size_t)parts * T * p->N * 4 : 0);
+  P->u = take(p->adapters > 0 ? moefp4::project_u_rows(p->T, p->K, p->rank) * p->rank * 4 : 0);
+  P->part = take((size_t)moefp4::project_part_rows(p->T, p->N, p->K) * p->N * 4);
   P->group = p->adapters > 0 && !moefp4::project_dot(p->T, p->K, p->rank);
   P->chunk = P->chunks = 0;
   if (P->group) {
@@ -518,7 +536,7 @@ moefp4_status project_check(const moefp4_linear* p, ProjectPlan* P) {
     P->tiles = take((T / 32 + L) * 8);
     P->ntiles = take(4);
     P->flags = take(64);
-    P->hist = take((size_t)P->chunks * (L + 1) * 4);
+    P->hist = take((size_t)(p->T > moefp4::kRouteSingleMax ? moefp4::kRouteMaxChunks : P->chunks) * (L + 1) * 4);
   }
   // (never 0: a caller that allocates what it is told has something to pass)
   P->total = o > 0 ? o : kAlign;
@@ -571,7 +589,7 @@ moefp4_status moe_fp4_gate_workspace_bytes(const moefp4_gate* g, int64_t T, int6
   moefp4::GatePlan P;
   moefp4_status st = gate_check(g, T, E, H, &P);
   if (st != MOEFP4_OK) return st;
-  *bytes = align_up(P.part_bytes) + align_up(P.planes_bytes);
+  *bytes = gate_need(P);
   return ok();
 }
 
@@ -586,7 +604,7 @@ moefp4_status moe_fp4_gate(const moefp4_gate* g, int64_t T, int64_t E, int64_t H
     return fail(MOEFP4_EINVAL, "x, w, topk_ids and topk_w must be non-NULL");
   if (misaligned(x, 16) || misaligned(w, 16) || misaligned(bias, 4) || misaligned(topk_ids, 4) || misaligned(topk_w, 4))
     return fail(MOEFP4_EINVAL, "x and w must be 16-byte aligned, bias, topk_ids and topk_w 4-byte");
-  const size_t need = align_up(P.part_bytes) + align_up(P.planes_bytes);
+  const size_t need = gate_need(P);
   if (!workspace || ws_bytes < need)
     return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", need, workspace ? ws_bytes : (size_t)0);
   if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");

@@ -211,6 +211,19 @@ GatePlan gate_plan(int T, int E, int H, bool w_f32) {
   p.planes_bytes = !p.dot && w_f32 ? (size_t)3 * E * H * 2 : 0;
   p.ld = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512;
   p.part_bytes = (size_t)p.parts * T * p.ld * 4;
+  // Fewer tokens can have more parts.  n parts of t tokens, in ce tiles per 128
+  // of them, take less than n t rows: 32768 / ce with FP32 weights, as n times
+  // the tiles is at most 256; t + 127 more with bfloat16 ones, where it is below
+  // 256 plus the tiles and n > 1 only below 256 tiles.
+  size_t rows = T;
+  if (!p.dot) {
+    const size_t nst = (H + kGK - 1) / kGK, most = nst / 2 < 1 ? 1 : nst / 2 > 16 ? 16 : nst / 2;
+    const size_t full = 32768 / ((E + kTile - 1) / kTile);
+    const size_t cap = w_f32 ? full : full + (rows < full ? rows : full) + 127;
+    const size_t split = most * rows < cap ? most * rows : cap;
+    rows = rows > split ? rows : split;
+  }
+  p.most_bytes = rows * p.ld * 4;
   return p;
 }
 

@@ -31,11 +31,12 @@ constexpr int kGateDotMax = 8, kGateDotMaxF32 = 64;
 
 // Logits of T tokens: one dot product per expert and token (dot), or a tiled
 // product with K split in `parts` of `per` stages.  part_bytes: the logits
-// [parts][T][ld] float32; planes_bytes: FP32 weights as bfloat16 planes.
+// [parts][T][ld] float32, most_bytes: the most that T or fewer tokens need for
+// them; planes_bytes: FP32 weights as bfloat16 planes.
 struct GatePlan {
   bool dot;
   int per, parts, ld;
-  size_t planes_bytes, part_bytes;
+  size_t planes_bytes, part_bytes, most_bytes;
 };
 GatePlan gate_plan(int T, int E, int H, bool w_f32);
 hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool w_f32, const uint16_t* x, int T, int H,
@@ -76,8 +77,9 @@ struct RouteOut {
 // Assignments per chunk of the multi-workgroup route (T * k above
 // kRouteSingleMax uses it).
 constexpr int kRouteSingleMax = 8192;
+constexpr int kRouteMaxChunks = 64;
 inline int route_chunk(long long A) {
-  long long c = (A + 63) / 64;
+  long long c = (A + kRouteMaxChunks - 1) / kRouteMaxChunks;
   c = (c + 1023) / 1024 * 1024;
   return (int)(c < 4096 ? 4096 : c);
 }
@@ -188,6 +190,10 @@ struct ProjectGemm {
 // parts of K in which u is computed
 int project_u_parts(long long T, long long K, long long R);
 ProjectGemm project_gemm_plan(long long T, long long N, long long K);
+// The most rows that u and the tiled product's parts (0: it has one) take for T
+// or fewer tokens.
+long long project_u_rows(long long T, long long K, long long R);
+long long project_part_rows(long long T, long long N, long long K);
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
 
 struct FcArgs {

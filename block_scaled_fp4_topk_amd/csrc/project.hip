@@ -948,6 +948,21 @@ int project_u_parts(long long T, long long K, long long R) {
   return n;
 }
 
+// (more than one part: at most 256 tiles of 32 tokens, parts times tiles)
+long long project_u_rows(long long T, long long K, long long R) {
+  if (project_dot(T, K, R)) return T;
+  const long long split = 8 * T < 256 * 32 ? 8 * T : 256 * 32;
+  return T > split ? T : split;
+}
+
+// (more than one part: at most 512 tiles of 64 tokens, parts times tiles; none
+// where 129 tokens fill 256 tiles)
+long long project_part_rows(long long T, long long N, long long K) {
+  const long long rt = (N + kTile - 1) / kTile, most = K / kGK / 8;
+  if (T <= kProjectFew || most < 2 || 3 * rt > 256) return 0;
+  return most * T < 512 * 64 / rt ? most * T : 512 * 64 / rt;
+}
+
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   return a.g16 ? launch_mode<0>(a, s) : launch_mode<1>(a, s);
 }

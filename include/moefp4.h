@@ -169,7 +169,8 @@ typedef struct moefp4_gate {
   float scale;
 } moefp4_gate;
 
-/* Workspace of moe_fp4_gate for T tokens, E routed experts and hidden size H. */
+/* Workspace of moe_fp4_gate for T tokens, E routed experts and hidden size H;
+ * it serves smaller T as well. */
 moefp4_status moe_fp4_gate_workspace_bytes(const moefp4_gate* g, int64_t T, int64_t E, int64_t H, size_t* bytes);
 
 /* x [T, H] bfloat16, w [E, H] bfloat16 or float32 (g->w_fmt), bias [E] float32
@@ -269,7 +270,8 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
  * rows); topk_ids / topk_w [T, top_k] receive the selection, NULL if it is
  * not wanted; the rest as for moe_fp4_forward; out overlaps no input.  The
- * workspace's first word then holds the number of places without an expert. */
+ * workspace's first word then holds the number of places without an expert.
+ * A workspace for T tokens serves smaller T as well. */
 moefp4_status moe_fp4_layer_workspace_bytes(const moefp4_problem* p, const moefp4_gate* g, size_t* bytes);
 moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const void* x, const void* gate_w,
                             const float* bias, const uint8_t* w13, const uint8_t* w13_sf, const float* w13_gs,
@@ -290,7 +292,8 @@ typedef struct moefp4_linear {
   int32_t gran_k, out_fmt, adapters, rank;
 } moefp4_linear;
 
-/* Workspace of moe_fp4_project (never 0 bytes: the call needs one). */
+/* Workspace of moe_fp4_project (never 0 bytes: the call needs one); it serves
+ * smaller T as well. */
 moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* bytes);
 
 /* x [T, K] bfloat16, w [N, K/2], w_sf [N, K/gran], w_gs [1] float32 or NULL,
