@@ -31,7 +31,7 @@ import os
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
            "forward_problem", "forward_static", "layer", "project",
            "requant_gran_k", "prepare_gemm_weights", "prepare_gemm_weights_g16", "quantize_act", "quantize_act_fp4",
-           "dropped_assignments", "LIB_PATH"]
+           "dropped_assignments", "abandoned_waits", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoefp4.so")
 
@@ -133,6 +133,8 @@ def lib():
         L.moefp4_mfma_peak_probe.restype = st
         L.moefp4_set_stage_events.argtypes = [_P, ctypes.c_int32]
         L.moefp4_set_stage_events.restype = st
+        L.moefp4_set_wait_looks.argtypes = [ctypes.c_int32]
+        L.moefp4_set_wait_looks.restype = st
         L.moefp4_version.argtypes = []
         L.moefp4_version.restype = ctypes.c_char_p
         _lib = L
@@ -454,7 +456,8 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
     to 8 tokens (2 with group32 weights) run in two launches (moe_fp4_layer).  quantize_x, w_layout,
     w13_order and out_dtype as for forward(); topk_ids / topk_w
     [T, top_k + shared]: optional outputs for the selection.  Returns out
-    [T, H]."""
+    [T, H]; NaN stands where a wait inside the two-launch form exceeded its
+    bound (abandoned_waits counts them)."""
     import torch
     T, routed, H, w_fmt, dev, at = _router_args(x, gate_w, bias)
     act = _LAYER_ACT.get(quantize_x)
@@ -645,7 +648,21 @@ def set_stage_events(events_array, n: int):
     _check(lib().moefp4_set_stage_events(events_array, n))
 
 
+def set_wait_looks(looks: int):
+    """Test hook (moefp4_set_wait_looks): how often later layer() calls of this
+    thread look at FC1's counters before they give a wait up; negative: the
+    default."""
+    _check(lib().moefp4_set_wait_looks(looks))
+
+
 def dropped_assignments(workspace) -> int:
     """Number of assignments with an expert id outside [0, E) in the last
     route / forward call that used ``workspace`` (synchronises)."""
     return int(workspace[:4].view(dtype=__import__("torch").int32).item())
+
+
+def abandoned_waits(workspace) -> int:
+    """Number of waits inside the last layer or fused forward call that used
+    ``workspace`` that exceeded their bound (synchronises).  A layer's outputs
+    behind such a wait are NaN."""
+    return int(workspace[4:8].view(dtype=__import__("torch").int32).item())

@@ -17,6 +17,7 @@ namespace {
 
 thread_local std::string g_err;
 thread_local hipEvent_t* g_stage_events = nullptr;
+thread_local int g_wait_looks = moefp4::kFewLooks;
 
 
 moefp4_status fail(moefp4_status st, const char* fmt, ...) {
@@ -718,6 +719,7 @@ moefp4_status moe_fp4_layer(const moefp4_problem* p, const moefp4_gate* g, const
   a.sync = at<int32_t>(workspace, P.sync);
   a.part = at<float>(workspace, P.parts);
   a.nwg = P.nwg;
+  a.looks = g_wait_looks;
   st = hip_status(moefp4::launch_few(a, stream), "layer");
   return st == MOEFP4_OK ? ok() : st;
 }
@@ -950,6 +952,11 @@ moefp4_status moefp4_mfma_peak_probe(int32_t a4, int32_t iters, int32_t blocks, 
 moefp4_status moefp4_set_stage_events(hipEvent_t* events, int32_t n) {
   if (events && n < 6) return fail(MOEFP4_EINVAL, "stage events need an array of 6, got %d", n);
   g_stage_events = events;
+  return ok();
+}
+
+moefp4_status moefp4_set_wait_looks(int32_t looks) {
+  g_wait_looks = looks < 0 ? moefp4::kFewLooks : looks;
   return ok();
 }
 

@@ -140,7 +140,11 @@ struct FewArgs {
   int32_t* sync;          // [few_sync_words]
   float* part;            // [workgroups][2][64 lanes][8] partial outputs
   int nwg;
+  int looks;              // at FC1's counters before a wait is given up
 };
+// About a microsecond each, 0.3 s in all.  (Counted, not timed: a clock goes on
+// while the queue is switched out for another process's.)
+constexpr int kFewLooks = 1 << 18;
 // launch 2's counters: a queue and a count of finished items per XCD, a line
 // each, then one word per 32 outputs
 constexpr int kFewQueues = 8, kFewLine = 32;

@@ -52,11 +52,6 @@ constexpr int kThreads = 64 * kWaves;
 // conflicts).
 constexpr int kHRow = 512 + 16;
 
-// Looks at FC1's counters before a wait is given up: about a microsecond each,
-// 0.3 s in all.  (Counted, not timed: a clock goes on while the queue is
-// switched out for another process's.)
-constexpr int kFewMaxPolls = 1 << 18;
-
 // bf16 row -> fp16 * 2**-p (exact down to 2**-24 of the row's maximum, which
 // lands in [2**14, 2**15)) by 256 threads.
 __device__ void few_row_to_f16(const uint16_t* __restrict__ row, int H, uint16_t* __restrict__ out, float* scale) {
@@ -301,7 +296,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ float s_wt[kActive * kCols];     // [active][token]: router weight times w2's global scale, 0: none
   __shared__ int s_en[kActive];                    // expert | tokens << 16
   __shared__ float s_gs13[kActive], s_xs[kCols];
-  __shared__ int s_cnt[kWaves], s_claim[2];
+  __shared__ int s_cnt[kWaves], s_claim[2], s_late;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -648,18 +643,21 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
   }
   if (wave == 0) {
-    for (int polls = 0; works; ++polls) {
+    int late = 0;
+    for (int looks = 0; works; ++looks) {
+      if (looks == a.looks) {
+        late = 1;
+        if (lane == 0) __hip_atomic_fetch_add(a.flags + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        break;
+      }
       int d = __hip_atomic_load(dones + (lane & (kQueues - 1)) * kLine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       d += __shfl_xor(d, 1, 64);
       d += __shfl_xor(d, 2, 64);
       d += __shfl_xor(d, 4, 64);
       if (__builtin_amdgcn_readfirstlane(d) >= n1) break;
-      if (polls == kFewMaxPolls) {
-        if (lane == 0) __hip_atomic_fetch_add(a.flags + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        break;
-      }
       __builtin_amdgcn_s_sleep(4);
     }
+    if (lane == 0) s_late = late;
     // (what this CU and XCD cached of h before is dropped: h is read through
     // the caches from here on)
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -675,7 +673,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     }
   }
 
-  float oacc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // (NaN where the wait was given up: nothing that this workgroup adds to is a
+  // number then, whoever looks or does not look at the flags)
+  const float from = __builtin_amdgcn_readfirstlane(s_late) ? __builtin_nanf("") : 0.0f;
+  float oacc[8] = {from, from, from, from, from, from, from, from};
   int first = 1;  // still in the run's first row block
   int flushes = 0;
   // the row block's sum over the waves, and on to the output: directly where
@@ -684,7 +685,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     s_red[buf][wave][0][lane] = float4{oacc[0], oacc[1], oacc[2], oacc[3]};
     s_red[buf][wave][1][lane] = float4{oacc[4], oacc[5], oacc[6], oacc[7]};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) oacc[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) oacc[i] = from;
     lds_barrier();
     if (wave == (flushes & (kWaves - 1))) {
       float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

@@ -263,8 +263,8 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
  * for selection, FC1, FC2 and the weighted sum.  That form keeps h to at least
  * 11 significant bits between FC1 and FC2 (moe_fp4_forward rounds it to
  * bfloat16); all its waits are bounded, and if one ever exceeded its bound
- * (0.3 s of its own running time), the workspace's second word is nonzero and
- * the result is not valid.  Other sizes and formats run moe_fp4_gate and
+ * (0.3 s of its own running time), the outputs it was for are NaN and the
+ * workspace's second word is nonzero.  Other sizes and formats run moe_fp4_gate and
  * moe_fp4_forward one after the other.
  * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
@@ -406,6 +406,11 @@ moefp4_status moe_fp4_quantize_act_fp4(int64_t T, int64_t H, const void* x, uint
  * (hipEventCreate) and may change the array between calls.  events = NULL
  * turns recording off.  n in 1..5 is EINVAL. */
 moefp4_status moefp4_set_stage_events(hipEvent_t* events, int32_t n);
+
+/* Test hook.  How often later moe_fp4_layer calls on this thread look at FC1's
+ * counters before they give a wait up: 0 gives every wait up at once, whatever
+ * FC1 has done; a negative number restores the bound. */
+moefp4_status moefp4_set_wait_looks(int32_t looks);
 
 /* Measurement helper (not part of the forward): enqueues a register-only
  * loop of the block-scaled matrix instruction the prefill kernels issue

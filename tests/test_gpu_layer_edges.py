@@ -44,3 +44,26 @@ def test_h_near_the_largest_float(gran, T):
     # silu and the product 16 half steps, h's rounding, one product and the sum over zeros
     assert np.all(np.abs(got - want) <= (HREL[gran] + (16 + 64) * mp.U32) * np.abs(want)), np.abs(got - want).max()
     assert np.all(got[:, 17] == 0)
+
+
+@pytest.mark.parametrize("gran,T", [(16, 1), (16, 8), (32, 2)])
+def test_a_wait_that_is_given_up_shows_in_the_output(gran, T):
+    """Every wait given up at once (the kernel itself runs to its end): no output of an unfinished FC1 looks like a
+    number, and the calls after it are whole again."""
+    require_gpu()
+    from test_gpu_layer import Layer
+    L = Layer(16, 1024, 512, gran, 41)
+    x, gw = L.args(T, 0)
+    ws = torch.zeros(16 << 20, dtype=torch.uint8, device="cuda")
+    want = moe.layer(x, gw, 4, *L.d, gran, workspace=ws)
+    assert moe.abandoned_waits(ws) == 0 and bool(want.isfinite().all())
+    torch.cuda.synchronize()
+    try:
+        moe.set_wait_looks(0)
+        for dt in (torch.bfloat16, torch.float32):
+            out = moe.layer(x, gw, 4, *L.d, gran, workspace=ws, out_dtype=dt)
+            torch.cuda.synchronize()
+            assert moe.abandoned_waits(ws) > 0 and bool(out.isnan().all())
+    finally:
+        moe.set_wait_looks(-1)
+    assert torch.equal(moe.layer(x, gw, 4, *L.d, gran, workspace=ws), want) and moe.abandoned_waits(ws) == 0
