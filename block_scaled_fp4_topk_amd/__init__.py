@@ -199,11 +199,14 @@ def _dims(t, name, dtypes, dims):
     return t.shape
 
 
-def _current(t):
-    """The tensor's device, which must be the current one."""
+def _current(t, stream):
+    """The tensor's device, which must be the current one and the stream's (a kernel is launched on the current
+    device)."""
     import torch
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device_index != t.get_device():
+        raise ValueError(f"tensors are on {t.device}, but the stream is on cuda:{stream.device_index}")
     return t.device
 
 
@@ -300,12 +303,12 @@ def make_gate(top_k, scoring="softmax", renormalize=False, scale=1.0, shared=0, 
     return Gate(top_k, shared, scoring, 1 if renormalize else 0, w_fmt, scale)
 
 
-def _router_args(x, gate_w, bias):
+def _router_args(x, gate_w, bias, stream):
     """(T, E, H, w_fmt, device, addresses) of a router's tensors, checked."""
     import torch
     wt = (torch.bfloat16, torch.float32)
     (T, H), (E, _) = _dims(x, "x", (torch.bfloat16,), 2), _dims(gate_w, "gate_w", wt, 2)
-    dev = _current(x)
+    dev = _current(x, stream)
     at = x.data_ptr(), _arg(gate_w, "gate_w", wt, (E, H), dev), _arg(bias, "bias", (torch.float32,), (E,), dev)
     return T, E, H, GATE_W_F32 if gate_w.dtype is torch.float32 else GATE_W_BF16, dev, at
 
@@ -320,7 +323,7 @@ def gate(x, gate_w, top_k, bias=None, scoring="softmax", renormalize=False, scal
     E, E + 1, ... with weight 1.  Places without an expert (everything masked,
     or logits that are not finite) hold id -1 and weight 0."""
     import torch
-    T, E, H, w_fmt, dev, at = _router_args(x, gate_w, bias)
+    T, E, H, w_fmt, dev, at = _router_args(x, gate_w, bias, stream)
     g = make_gate(top_k, scoring, renormalize, scale, shared, w_fmt)
     need = _gate_need(top_k, shared, scoring, w_fmt, T, E, H)
     shape = (T, top_k + shared)
@@ -459,7 +462,7 @@ def layer(x, gate_w, top_k, w13, w13_sf, w13_gs, w2, w2_sf, w2_gs, gran_k, bias=
     [T, H]; NaN stands where a wait inside the two-launch form exceeded its
     bound (abandoned_waits counts them)."""
     import torch
-    T, routed, H, w_fmt, dev, at = _router_args(x, gate_w, bias)
+    T, routed, H, w_fmt, dev, at = _router_args(x, gate_w, bias, stream)
     act = _LAYER_ACT.get(quantize_x)
     if act is None:
         raise ValueError(f"quantize_x must be False, True, 'fp8' or 'fp4', got {quantize_x!r}")
@@ -501,7 +504,7 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     import torch
     u8, f32, bf = (torch.uint8,), (torch.float32,), (torch.bfloat16,)
     (T, K), (N, _) = _dims(x, "x", bf, 2), _dims(w, "w", u8, 2)
-    dev = _current(x)
+    dev = _current(x, stream)
     if gran_k not in (16, 32):
         raise ValueError(f"gran_k must be 16 or 32, got {gran_k}")
     at = (x.data_ptr(), _arg(w, "w", u8, (N, K // 2), dev), _arg(w_sf, "w_sf", u8, (N, K // gran_k), dev),
