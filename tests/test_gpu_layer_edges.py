@@ -67,3 +67,39 @@ def test_a_wait_that_is_given_up_shows_in_the_output(gran, T):
     finally:
         moe.set_wait_looks(-1)
     assert torch.equal(moe.layer(x, gw, 4, *L.d, gran, workspace=ws), want) and moe.abandoned_waits(ws) == 0
+
+
+@pytest.mark.parametrize("shared", [0, 1])
+@pytest.mark.parametrize("gran,T", [(16, 8), (32, 2)])
+def test_sixteen_experts_per_token_all_different(gran, T, shared):
+    """The most experts that the two-launch form holds: 16 per token, with no routed one in common."""
+    require_gpu()
+    from test_gpu_layer import Layer
+    E, k = 16 * T + shared, 16 - shared
+    L = Layer(E, 512, 256, gran, 42, gs=gran == 16, T=T)
+    L.gw[:] = 0
+    for e in range(E - shared):
+        L.gw[e, e // 16 if e < 16 * T else 0] = 8 + (e % 16) / 8
+    L.x[:, :T] = np.eye(T)
+    out = L.check(T, k, shared, renormalize=True)
+    assert bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("gran", [16, 32])
+@pytest.mark.parametrize("I", [2304, 4096, 6400])
+def test_long_intermediate_rows(I, gran):
+    """More than 8 chunks of an expert's rows in FC2: a step's 8 waves end inside one."""
+    require_gpu()
+    from test_gpu_layer import Layer
+    L = Layer(5, 512, I, gran, 43, gs=gran == 16, T=8)
+    for T in (1, 2, 8):
+        L.check(T, 3, 1, scoring="sigmoid", renormalize=True)
+
+
+@pytest.mark.parametrize("gran", [16, 32])
+def test_512_experts(gran):
+    require_gpu()
+    from test_gpu_layer import Layer
+    L = Layer(512, 256, 256, gran, 44, gs=gran == 16, T=8)
+    for T in (1, 2, 8):
+        L.check(T, 8, 2, renormalize=True)
