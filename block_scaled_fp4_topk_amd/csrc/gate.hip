@@ -52,24 +52,24 @@ __global__ __launch_bounds__(256) void gate_split_kernel(const float* __restrict
 
 constexpr int kTile = 128;  // experts and tokens per workgroup
 constexpr int kGK = 64;     // K elements per stage
+constexpr int kGWaves = 8;
 
 // LDS rows of 128 bytes; 16-byte segment s of row r sits at s ^ ((r >> 1) & 7),
 // so that the 16 rows a lane group reads touch all 64 banks.
 __device__ __forceinline__ int gswz(int r) { return (r >> 1) & 7; }
 
 // Stages rows [0, 128) x K [k0, k0 + 64) of a row-major bf16 matrix; each of
-// the NW waves loads 128 / NW rows, eight whole ones per instruction.  Rows past the
+// the 8 waves loads 16 rows, eight whole ones per instruction.  Rows past the
 // last one repeat it (their results are not stored); K past H is zero.
-template <int NW>
 __device__ __forceinline__ void gate_stage(const uint16_t* __restrict__ src, int row0, int rows, int H, int k0,
                                            uint8_t* lds, int wave, int lane) {
 #pragma unroll
-  for (int i = 0; i < 16 / NW; ++i) {
-    const int r = 128 / NW * wave + 8 * i + (lane >> 3);
+  for (int i = 0; i < 16 / kGWaves; ++i) {
+    const int r = kTile / kGWaves * wave + 8 * i + (lane >> 3);
     const int seg = (lane & 7) ^ gswz(r);
     const int k = k0 + 8 * seg;
     const int row = min(row0 + r, rows - 1);
-    uint8_t* base = lds + (128 / NW * wave + 8 * i) * 128;
+    uint8_t* base = lds + (kTile / kGWaves * wave + 8 * i) * 128;
     if (k < H)
       __builtin_amdgcn_global_load_lds(src + (size_t)row * H + k, base, 16, 0, 0);
     else
@@ -78,12 +78,11 @@ __device__ __forceinline__ void gate_stage(const uint16_t* __restrict__ src, int
 }
 
 // One 128 x 128 tile over K stages [blockIdx.z * per, + per): part z of the
-// logits.  NW waves of 64 (4 of them) or 32 (8) experts x 64 tokens; WP planes of
-// W.
-template <int WP, int NW>
-__global__ __launch_bounds__(64 * NW) void gate_gemm_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ x,
-                                                        int T, int E, int ld, int H, int per,
-                                                        float* __restrict__ part) {
+// logits.  A wave has 32 experts x 64 tokens; WP planes of W.
+template <int WP>
+__global__ __launch_bounds__(64 * kGWaves) void gate_gemm_kernel(const uint16_t* __restrict__ w,
+                                                                 const uint16_t* __restrict__ x, int T, int E, int ld,
+                                                                 int H, int per, float* __restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint8_t s[2][(WP + 1) * kTile * 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -91,13 +90,13 @@ __global__ __launch_bounds__(64 * NW) void gate_gemm_kernel(const uint16_t* __re
   const int t0 = blockIdx.x * kTile, e0 = blockIdx.y * kTile;
   const int nst = (H + kGK - 1) / kGK;
   const int s0 = blockIdx.z * per, s1 = min(nst, s0 + per);
-  constexpr int NI = 16 / NW;  // 16-expert tiles of a wave
-  const int we = (wave % (NW / 2)) * 16 * NI, wt = wave / (NW / 2) * 64;
+  constexpr int NI = 16 / kGWaves;  // 16-expert tiles of a wave
+  const int we = (wave % (kGWaves / 2)) * 16 * NI, wt = wave / (kGWaves / 2) * 64;
   auto stage = [&](int c, uint8_t* b) __attribute__((always_inline)) {
-    gate_stage<NW>(x, t0, T, H, c * kGK, b, wave, lane);
+    gate_stage(x, t0, T, H, c * kGK, b, wave, lane);
 #pragma unroll
     for (int p = 0; p < WP; ++p)
-      gate_stage<NW>(w + (size_t)p * E * H, e0, E, H, c * kGK, b + (p + 1) * kTile * 128, wave, lane);
+      gate_stage(w + (size_t)p * E * H, e0, E, H, c * kGK, b + (p + 1) * kTile * 128, wave, lane);
   };
   v4f acc[NI][4];
 #pragma unroll
@@ -251,10 +250,10 @@ hipError_t launch_gate(const GatePlan& p, const GateSel& g, const void* w, bool 
                          static_cast<const float*>(w), n, planes);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;
-      hipLaunchKernelGGL((gate_gemm_kernel<3, 8>), grid, dim3(512), 0, s, planes, x, T, E, p.ld, H, p.per, part);
+      hipLaunchKernelGGL(gate_gemm_kernel<3>, grid, dim3(64 * kGWaves), 0, s, planes, x, T, E, p.ld, H, p.per, part);
     } else {
-      hipLaunchKernelGGL((gate_gemm_kernel<1, 8>), grid, dim3(512), 0, s, static_cast<const uint16_t*>(w), x, T, E, p.ld,
-                         H, p.per, part);
+      hipLaunchKernelGGL(gate_gemm_kernel<1>, grid, dim3(64 * kGWaves), 0, s, static_cast<const uint16_t*>(w), x,
+                         T, E, p.ld, H, p.per, part);
     }
   }
   const hipError_t err = hipGetLastError();
