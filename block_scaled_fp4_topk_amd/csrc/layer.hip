@@ -285,7 +285,7 @@ template <int MODE, int NC, int NI>
 __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   __shared__ float4 s_red[2][kWaves][2][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[kWaves][4096];
-  __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][(MODE == 0 ? 4 : 8) * kHRow];
+  __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][4 * kHRow];
   __shared__ int s_ids[kActive];
   __shared__ float s_tw[kActive];
   // per active expert: its id and tokens, and per token
@@ -569,7 +569,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const int begin = works ? (int)(wg * total / G) : 0, end = works ? (int)((wg + 1) * total / G) : 0;
   const uint32_t rowb2 = (uint32_t)(I >> 1), rows2 = (uint32_t)(MODE == 0 ? I >> 4 : I >> 5);
   constexpr int NB = MODE == 0 ? 1 : 2;  // parts of h
-  constexpr int kHalf = 4;               // tokens of an expert taken at a time
+  // tokens of an expert taken at a time (group32: all of them)
+  constexpr int kHalf = MODE == 0 ? 4 : kFewTokensG32;
+  static_assert(kHalf <= 4 && kFewTokens <= 2 * 4, "h rows are looked up four at a time, at most twice");
   constexpr int NS = 3;                  // steps in flight
   WPair w2[NS];
   uint64_t hb[NS][NB][kHalf];
@@ -795,11 +797,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         // kHalf tokens at a time (more of one expert: once again, their h
         // fetched on the spot)
 #pragma unroll 1
-        for (int n0 = 0; n0 < ne; n0 += kHalf) {
-          if (n0 > 0) {
-            h_rows(act, c, n0, hb[k]);
-            arrived(hb[k]);
-          }
+        for (int n0 = 0;;) {
 #pragma unroll
           for (int p = 0; p < NB; ++p)
 #pragma unroll
@@ -821,6 +819,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
               oacc[4 + i] = __builtin_fmaf(acc[1][i], cs, oacc[4 + i]);
             }
           }
+          n0 += kHalf;
+          if (MODE == 1 || n0 >= ne) break;
+          h_rows(act, c, n0, hb[k]);
+          arrived(hb[k]);
         }
       }
       load_w2(nxt.rb, nu, w2[k]);
