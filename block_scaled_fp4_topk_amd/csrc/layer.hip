@@ -1,6 +1,7 @@
-// A whole mixture-of-experts layer for at most 8 tokens, in two launches:
-// router logits, then one persistent kernel that selects the experts, runs
-// FC1 + SwiGLU and FC2 over their FP4 weights and writes the weighted sum.
+// A whole mixture-of-experts layer for at most 8 tokens (2 with group32
+// weights), in two launches: router logits, then one persistent kernel that
+// selects the experts, runs FC1 + SwiGLU and FC2 over their FP4 weights and
+// writes the weighted sum.
 //
 // With so few tokens the layer is a stream of weights (an expert's FP4 codes
 // and scales, read once) and what costs beside it are the dependences: token
@@ -9,19 +10,23 @@
 // * Every activation a wavefront needs for FC1 stays in its registers.  A
 //   wave owns a fixed slice of H (1/8 of it: at most 3 chunks of 256), whose
 //   MFMA operands for all token columns are loaded once (32 registers per
-//   chunk) and serve every expert; the weights come straight from HBM into
-//   registers, are decoded there and multiplied.  No operand passes through
-//   LDS; it only sums the 8 waves' partial tiles.  Columns of tokens that did
-//   not choose the expert are computed and dropped (the matrix instruction
-//   has 16 columns anyway).
+//   chunk) and serve every expert.  The weights come from HBM into registers
+//   as whole 128-byte lines, are turned into operand order through the wave's
+//   own 4 KB of LDS (no barrier) and decoded on the way into the matrix
+//   instruction.  Columns of tokens that did not choose the expert are computed
+//   and dropped (the matrix instruction has 16 columns anyway).  The 8 waves'
+//   partial tiles meet in LDS.
 // * Each chunk's registers are refilled with the same chunk of the next item
 //   as soon as it is consumed, so that 8 waves keep a whole item (up to 110 KB
 //   per CU) in flight.
-// * FC1 items (an expert's 16 gate rows and the 16 matching up rows) are
-//   claimed from one counter; no workgroup waits before every item has been
-//   claimed by a workgroup that is running and finishes it without waiting:
-//   however few workgroups are resident, every wait ends.  (The wait is
-//   bounded all the same, as the single-launch forward's.)
+// * FC1 items (an expert's 16 gate rows and the 16 matching up rows) lie in
+//   one queue per XCD; a workgroup claims from its own XCD's and, when that is
+//   empty, from one that is not.  Whoever claims an item is running and
+//   finishes it without waiting, and a claim that succeeds is followed by
+//   another look at all queues: after the last one that succeeds there is
+//   nothing left.  So every item is finished however few workgroups are
+//   resident, and the wait for them ends.  (It is bounded all the same, as the
+//   single-launch forward's; a workgroup that gives it up adds NaN.)
 // * FC2's work is split evenly by workgroup number: row blocks of 32 outputs
 //   x steps of 8 (expert, chunk) units, one per wave, laid end to end and cut
 //   into equal runs.  A workgroup's first weights are requested before it
@@ -29,13 +34,18 @@
 //   accumulators hold the output itself; where a run's border cuts a row
 //   block, its parts are summed in run order by whichever workgroup ends last
 //   (no atomics on values: the result does not depend on timing).
-// * What passes between workgroups of one launch (h, parts, counters) goes
-//   through agent-scope accesses, which do not stay in an XCD's L2.
+// * h, parts and counters are written past the caches of an XCD (agent-scope
+//   stores, complete before the counter that reports them is raised).  Parts
+//   and counters are read so too; h, which every workgroup reads, comes through
+//   the caches, behind one acquire per workgroup: it drops what the CU's L1
+//   and the XCD's L2 held of h before, and the barrier behind it holds the
+//   other waves' reads back.
 //
 // h keeps more than bfloat16: group16 weights multiply in fp16, h as fp16 with
-// one power of two per 16 values (11 significant bits); group32 weights
-// multiply in bfloat16, h as a high and a low part (16 bits), two
-// instructions per product.  The output's own rounding (8 bits) dominates.
+// one power of two per 16 values (11 significant bits, less below 2**-28 of the
+// largest of 256 values); group32 weights multiply in bfloat16, h as a high and
+// a low part (16 bits), two instructions per product.  The output's own
+// rounding (8 bits) dominates.
 #include "gate_core.h"
 
 namespace moefp4 {

@@ -161,7 +161,10 @@ moefp4_status moe_fp4_route(const moefp4_problem* p, const int32_t* topk_ids,
  * Renormalised weights are the quotients of the scores also where the scores
  * themselves are too small for FP32 (very negative logits, or a softmax whose
  * mass lies with masked experts).
- * With a bias the scores are formed and compared in 64 bits. */
+ * Scores and weights are formed in FP32 (a score below 2^-126 may be rounded
+ * to 0).  With a bias, scores + bias that FP32 does not tell apart for certain
+ * (closer than 2^-20 of the larger of 1 and their size) are formed again and
+ * compared in 64 bits. */
 typedef enum moefp4_score { MOEFP4_SCORE_SOFTMAX = 0, MOEFP4_SCORE_SIGMOID = 1 } moefp4_score;
 typedef enum moefp4_gate_fmt { MOEFP4_GATE_W_BF16 = 0, MOEFP4_GATE_W_F32 = 1 } moefp4_gate_fmt;
 typedef struct moefp4_gate {
@@ -261,11 +264,12 @@ moefp4_status moe_fp4_forward_static(const moefp4_problem* p,
  * Up to 8 tokens (2 with group32 weights) of BF16 activations (and H <= 6144,
  * top_k <= 16) run in two launches: router logits, then one persistent kernel
  * for selection, FC1, FC2 and the weighted sum.  That form keeps h to at least
- * 11 significant bits between FC1 and FC2 (moe_fp4_forward rounds it to
- * bfloat16); all its waits are bounded, and if one ever exceeded its bound
- * (0.3 s of its own running time), the outputs it was for are NaN and the
- * workspace's second word is nonzero.  Other sizes and formats run moe_fp4_gate and
- * moe_fp4_forward one after the other.
+ * 11 significant bits between FC1 and FC2, values below 2^-28 of the largest of
+ * 256 to fewer (moe_fp4_forward rounds it to bfloat16); all its waits are
+ * bounded, and if one ever exceeded its bound (0.3 s of its own running time),
+ * the outputs it was for are NaN and the workspace's second word is nonzero.
+ * Other sizes and formats run moe_fp4_gate and moe_fp4_forward one after the
+ * other.
  * act_fmt BF16, BF16_QUANT_FP8_K32 or BF16_QUANT_FP4_K32 (EINVAL otherwise:
  * the router takes bfloat16 x).  gate_w, bias as for moe_fp4_gate (E - shared
  * rows); topk_ids / topk_w [T, top_k] receive the selection, NULL if it is

@@ -103,3 +103,24 @@ def test_512_experts(gran):
     L = Layer(512, 256, 256, gran, 44, gs=gran == 16, T=8)
     for T in (1, 2, 8):
         L.check(T, 8, 2, renormalize=True)
+
+
+@pytest.mark.parametrize("gran,T", [(16, 1), (16, 8), (32, 2), (16, 12)])
+@pytest.mark.parametrize("E", [20, 300])
+def test_renormalised_weights_of_scores_below_fp32(E, gran, T):
+    """The layer's selection gives the router's weights, also where their scores are beyond FP32's range."""
+    require_gpu()
+    from test_gpu_gate_edges import check, planted
+    rng = np.random.default_rng(45)
+    H = I = 256
+    z = -95 - (rng.permutation(E) + 16) / 64
+    x, gw = (torch.from_numpy(v).bfloat16().cuda() for v in planted(T, z, H))
+    d = [torch.from_numpy(v).cuda() for v in (*mp.fp4_tensor(rng, E, 2 * I, H, gran), *mp.fp4_tensor(rng, E, H, I, gran))]
+    ids = torch.empty((T, 5), dtype=torch.int32, device="cuda")
+    wts = torch.empty((T, 5), device="cuda")
+    out = moe.layer(x, gw, 5, d[0], d[1], None, d[2], d[3], None, gran, scoring="sigmoid", renormalize=True, scale=2.5,
+                    topk_ids=ids, topk_w=wts, out_dtype=torch.float32)
+    rids, rwts = moe.gate(x, gw, 5, scoring="sigmoid", renormalize=True, scale=2.5)
+    assert torch.equal(ids, rids) and torch.equal(wts, rwts) and abs(float(wts[0].sum()) - 2.5) < 1e-5
+    check(T, z, False, 5, None, "sigmoid", 2.5)
+    assert bool(out.isfinite().all()) and bool((out != 0).any())
