@@ -105,15 +105,16 @@ hipError_t launch_rows_to_f16(const uint16_t* x, int T, int H, uint16_t* x16, fl
 // Up to 8 tokens with group16, 2 with group32 weights.  Both forms, captured
 // in a graph, two launches / gate + forward, us:
 //                                     T = 1      2        4          8        16
-//   256 experts, H 6144, I 2048, g16: 61/65    89/87    132/139   241/251   412/399
-//                                g32: 58/64    84/77    135/136   231/223   379/343
-//   128 experts, H 4096, I 1536, g16: 39/50    54/56     78/95    124/140   188/194
-//                                g32: 38/45    52/54     78/72    117/108   171/151
-//    64 experts, H 2048, I 768,  g16: 30/31    34/37     38/40     48/45     61/58
-//                                g32: 27/31    31/33     35/35     45/39     56/45
-// (FC2 takes a few instructions more per weight than the decode tiles, two
-// products with group32; without a graph gate + forward has five launches
-// more to enqueue.)
+//   256 experts, H 6144, I 2048, g16: 58/65    86/89    132/143   238/259   412/399
+//                                g32: 54/63    79/77    135/136   231/223   379/343
+//   128 experts, H 4096, I 1536, g16: 39/50    55/57     80/97    126/146   188/194
+//                                g32: 35/45    48/53     78/72    117/108   171/151
+//    64 experts, H 2048, I 768,  g16: 31/34    34/36     42/42     52/46     61/58
+//                                g32: 27/32    31/34     35/35     45/39     56/45
+// (Beyond the limits: measured in a form that took 16 tokens of either.  FC2
+// takes a few instructions more per weight than the decode tiles, two products
+// with group32; without a graph gate + forward has five launches more to
+// enqueue.)
 constexpr int kFewTokens = 8, kFewTokensG32 = 2;
 constexpr int kFewMaxH = 6144;
 constexpr int kFewMaxK = 16;
