@@ -752,6 +752,17 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
     return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", P.total,
                 workspace ? ws_bytes : (size_t)0);
   if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  // (workgroups store while others still read)
+  const size_t N = p->N, K = p->K, LR = (size_t)p->adapters * p->rank;
+  const struct { const void* p; size_t n; } in[] = {{x, p->T * K * 2}, {w, N * K / 2}, {w_sf, N * (K / p->gran_k)}, {w_gs, 4},
+                                                    {lora_a, LR * K * 2}, {lora_b, LR * N * 2}, {id, (size_t)p->T * 4},
+                                                    {scale, (size_t)p->adapters * 4}};
+  const char* o = static_cast<const char*>(out);
+  const size_t on = p->T * N * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2);
+  for (const auto& b : in) {
+    const char* q = static_cast<const char*>(b.p);
+    if (q && q < o + on && o < q + b.n) return fail(MOEFP4_EINVAL, "out overlaps an input");
+  }
   moefp4::ProjectArgs a;
   memset(&a, 0, sizeof a);
   a.T = (int)p->T;

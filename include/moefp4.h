@@ -307,7 +307,7 @@ moefp4_status moe_fp4_project_workspace_bytes(const moefp4_linear* p, size_t* by
  * multiple of 32 and rank a positive multiple of 8 (EINVAL otherwise); K a
  * multiple of 256 and N of 16, rank up to 128, up to 511 adapters, T below
  * 2^24, N*K and adapters*N*rank below 2^32 and T*N below 2^38 (EUNSUPPORTED
- * otherwise).  out overlaps no input.  Enqueued on `stream`. */
+ * otherwise).  out overlaps no input (EINVAL).  Enqueued on `stream`. */
 moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8_t* w, const uint8_t* w_sf,
                               const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
                               const float* scale, void* out, void* workspace, size_t ws_bytes, hipStream_t stream);

@@ -69,3 +69,24 @@ def test_layer_workspace_serves_smaller_batches(E, k, shared, H, I, gran, act):
             assert m.lib().moe_fp4_layer_workspace_bytes(ctypes.byref(p), ctypes.byref(g), ctypes.byref(n)) == m.OK
             return n.value
         grows(need)
+
+
+@pytest.mark.parametrize("T", [40, 1000])
+def test_project_refuses_an_output_over_its_inputs(T):
+    """In place, or with one byte in common: the tiled form reads x while other workgroups store.  (Addresses that
+    are never dereferenced.)"""
+    L = m.lib()
+    N = K = 512
+    p = m.Linear(T, N, K, 16, m.OUT_BF16, 2, 8)
+    size = dict(x=T * K * 2, w=N * K // 2, w_sf=N * K // 16, w_gs=4, a=2 * 8 * K * 2, b=2 * N * 8 * 2, id=T * 4, scale=8)
+    base = {n: (1 << 30) + (i << 28) for i, n in enumerate(size)}
+    out = T * N * 2
+
+    def call(at):
+        ptr = [ctypes.c_void_p(base[n]) for n in size]
+        return L.moe_fp4_project(ctypes.byref(p), *ptr, ctypes.c_void_p(at), ctypes.c_void_p(1 << 40), 1 << 40, None)
+    for n in size:
+        first = max(0, base[n] - out + 16)
+        last = base[n] + (size[n] - 1) // 16 * 16
+        for at in (base[n], first, last):
+            assert call(at) == m.EINVAL and b"overlaps" in L.moefp4_last_error(), n
