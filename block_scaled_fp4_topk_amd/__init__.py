@@ -15,6 +15,11 @@ Functions mirror the C entry points:
   layer(x, gate_w, top_k, w13, ...)   -> moe_fp4_layer (router and forward)
   forward_static(x, topk_ids, ...)    -> moe_fp4_forward_static (no workspace)
   project(x, w, w_sf, w_gs, ...)      -> moe_fp4_project (FP4 projection with low-rank adapters)
+  grouped(x, w, offsets, ...)         -> moe_fp4_grouped (products grouped by expert, bfloat16 or FP4 weights)
+  grouped_dx(dy, w, offsets, ...)     -> moe_fp4_grouped_dx (their gradient towards the rows)
+  grouped_dw(dy, x, offsets, ...)     -> moe_fp4_grouped_dw (and towards the weights)
+  block_norm(h, y, ...)               -> moe_fp4_block_norm (norms around a layer, gate and residual scale)
+  block_norm_grad(dh, dn, h, y, ...)  -> moe_fp4_block_norm_grad (their gradient)
   requant_gran_k(src, src_sf, ...)    -> fp4_requant_gran_k
   prepare_gemm_weights(src, src_sf, ...) -> moe_fp4_prepare_gemm_weights
   prepare_gemm_weights_g16(src, src_sf, src_gs, ...) -> moe_fp4_prepare_gemm_weights_g16
@@ -29,7 +34,8 @@ import functools
 import os
 
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
-           "forward_problem", "forward_static", "layer", "project",
+           "forward_problem", "forward_static", "layer", "project", "grouped", "grouped_dx", "grouped_dw",
+           "block_norm", "block_norm_grad",
            "requant_gran_k", "prepare_gemm_weights", "prepare_gemm_weights_g16", "quantize_act", "quantize_act_fp4",
            "dropped_assignments", "abandoned_waits", "LIB_PATH"]
 
@@ -62,6 +68,17 @@ class Gate(ctypes.Structure):
 class Linear(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("T", "N", "K")] + \
         [(n, ctypes.c_int32) for n in ("gran_k", "out_fmt", "adapters", "rank")]
+
+
+class Grouped(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("M", "N", "K")] + \
+        [(n, ctypes.c_int32) for n in ("E", "gran_k", "out_fmt")]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "H")] + \
+        [(n, ctypes.c_int32) for n in ("h_fmt", "post_fmt", "pre_fmt", "gate_fmt", "gate_kind", "gate_sigmoid")] + \
+        [(n, ctypes.c_float) for n in ("scale", "h_scale", "eps")]
 
 
 class MoeFp4Error(RuntimeError):
@@ -105,6 +122,20 @@ def lib():
         L.moe_fp4_project_workspace_bytes.restype = st
         L.moe_fp4_project.argtypes = [lp] + [_P] * 10 + [ctypes.c_size_t, _P]
         L.moe_fp4_project.restype = st
+        rp = ctypes.POINTER(Grouped)
+        L.moe_fp4_grouped.argtypes = [rp] + [_P] * 7
+        L.moe_fp4_grouped.restype = st
+        L.moe_fp4_grouped_dx.argtypes = [rp] + [_P] * 7
+        L.moe_fp4_grouped_dx.restype = st
+        L.moe_fp4_grouped_dw.argtypes = [rp] + [_P] * 4 + [ctypes.c_int32, _P]
+        L.moe_fp4_grouped_dw.restype = st
+        np_ = ctypes.POINTER(Norm)
+        L.moe_fp4_block_norm.argtypes = [np_] + [_P] * 8
+        L.moe_fp4_block_norm.restype = st
+        L.moe_fp4_block_norm_grad_workspace_bytes.argtypes = [np_, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fp4_block_norm_grad_workspace_bytes.restype = st
+        L.moe_fp4_block_norm_grad.argtypes = [np_] + [_P] * 13 + [ctypes.c_size_t, _P]
+        L.moe_fp4_block_norm_grad.restype = st
         L.moe_fp4_forward.argtypes = [ctypes.POINTER(Problem), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, _P]
         L.moe_fp4_forward.restype = st
@@ -251,6 +282,11 @@ def _gate_need(top_k, shared, scoring, w_fmt, T, E, H):
 def _layer_need(device, top_k, shared, scoring, w_fmt, *problem):
     g = make_gate(top_k, scoring, False, 1.0, shared, w_fmt)
     return _need(lib().moe_fp4_layer_workspace_bytes, ctypes.byref(Problem(*problem)), ctypes.byref(g))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_grad_need(T, H):
+    return _need(lib().moe_fp4_block_norm_grad_workspace_bytes, ctypes.byref(Norm(T, H)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -534,6 +570,172 @@ def project(x, w, w_sf, w_gs, gran_k, lora_a=None, lora_b=None, lora_id=None, lo
     _check(_lib.moe_fp4_project(ctypes.byref(Linear(*linear)), *at, *lora, _arg(out, "out", (out_dtype,), (T, N), dev),
                                 ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return out
+
+
+def _out_dtype(out, out_dtype):
+    import torch
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    return out_dtype, OUT_F32 if out_dtype is torch.float32 else OUT_BF16
+
+
+def _grouped_product(fn, name, along_k, x, w, offsets, w_sf, w_gs, gran_k, out, stream, out_dtype):
+    import torch
+    u8, bf = (torch.uint8,), (torch.bfloat16,)
+    M, cols = _dims(x, name, bf, 2)
+    dev = _current(x, stream)
+    if gran_k not in (None, 0, 16, 32):
+        raise ValueError(f"gran_k must be None (bfloat16 weights), 16 or 32, got {gran_k}")
+    E, N, K = _dims(w, "w", u8 if gran_k else bf, 3)
+    if gran_k:
+        K *= 2
+        if w_sf is None:
+            raise ValueError("FP4 weights need w_sf")
+    elif w_sf is not None or w_gs is not None:
+        raise ValueError("w_sf and w_gs go with FP4 weights (gran_k)")
+    _arg(w, "w", u8 if gran_k else bf, (E, N, K // 2 if gran_k else K), dev)
+    _arg(x, name, bf, (M, K if along_k else N), dev)
+    outs = N if along_k else K
+    out_dtype, fmt = _out_dtype(out, out_dtype)
+    sf = _arg(w_sf, "w_sf", u8, (E, N, K // gran_k), dev) if gran_k else None
+    gs = _arg(w_gs, "w_gs", (torch.float32,), (E,), dev)
+    off = _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    if out is None:
+        out = _empty(x, (M, outs), out_dtype, stream)
+    _check(fn(ctypes.byref(Grouped(M, N, K, E, gran_k or 0, fmt)), x.data_ptr(), w.data_ptr(), sf, gs, off,
+              _arg(out, "out", (out_dtype,), (M, outs), dev), _raw_stream(stream, dev)))
+    return out
+
+
+def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, stream=None, out_dtype=None):
+    """Products grouped by expert: out[r] = W_e x[r] for the rows r in
+    [offsets[e], offsets[e + 1]).  x [M, K] bfloat16; offsets [E + 1] int32,
+    ascending (as route() gives them); w [E, N, K] bfloat16, or [E, N, K/2] uint8
+    FP4 codes with w_sf [E, N, K/gran_k] uint8 (and w_gs [E] float32) and gran_k 16
+    or 32.  Returns out [M, N] bfloat16 (default) or float32; rows outside
+    [offsets[0], offsets[E]) are left as they are."""
+    return _grouped_product(lib().moe_fp4_grouped, "x", True, x, w, offsets, w_sf, w_gs, gran_k, out, stream, out_dtype)
+
+
+def grouped_dx(dy, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, stream=None, out_dtype=None):
+    """The gradient of grouped() towards its rows: out[r] = W_e^T dy[r], dy [M, N]
+    bfloat16, the weights and offsets as grouped() takes them.  Returns out
+    [M, K]."""
+    return _grouped_product(lib().moe_fp4_grouped_dx, "dy", False, dy, w, offsets, w_sf, w_gs, gran_k, out, stream,
+                            out_dtype)
+
+
+def grouped_dw(dy, x, offsets, out=None, accumulate=False, stream=None, out_dtype=None):
+    """The gradient of grouped() towards its weights: out[e] = the sum over
+    expert e's rows of dy[r] x[r]^T, zeros for an expert without rows.  dy [M, N]
+    and x [M, K] bfloat16, offsets [E + 1] int32.  accumulate adds the sums to
+    what out holds.  Returns out [E, N, K] bfloat16 (default) or float32."""
+    import torch
+    bf = (torch.bfloat16,)
+    (M, N), (_, K) = _dims(dy, "dy", bf, 2), _dims(x, "x", bf, 2)
+    dev = _current(dy, stream)
+    E = _dims(offsets, "offsets", (torch.int32,), 1)[0] - 1
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out_dtype, fmt = _out_dtype(out, out_dtype)
+    at = dy.data_ptr(), _arg(x, "x", bf, (M, K), dev), _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    if out is None:
+        out = _empty(dy, (max(E, 0), N, K), out_dtype, stream)
+    _check(lib().moe_fp4_grouped_dw(ctypes.byref(Grouped(M, N, K, E, 0, fmt)), *at,
+                                    _arg(out, "out", (out_dtype,), (E, N, K), dev), 1 if accumulate else 0,
+                                    _raw_stream(stream, dev)))
+    return out
+
+
+def _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream):
+    """(problem, device, addresses of y, post_w, gate and pre_w) of a block norm whose residual stream's type and
+    sizes are those of ``first``."""
+    import torch
+    bf, some = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+    T, H = _dims(first, name, some, 2)
+    dev = _current(first, stream)
+    if y is None and (post_w is not None or gate is not None):
+        raise ValueError("post_w and gate go with y")
+    if y is None and pre_w is None:
+        raise ValueError("y or pre_w is needed")
+    if gate_act not in (None, "sigmoid"):
+        raise ValueError(f"gate_act must be None or 'sigmoid', got {gate_act!r}")
+    kind, gate_at = 0, None
+    if gate is not None:
+        _dev(gate, "gate", some)
+        # (a gate of T = H elements is one per channel; [T, 1] says per token)
+        shapes = ((H,), (T,), (T, 1), (T, H)) if H != 1 else ((H,),)
+        if tuple(gate.shape) not in shapes:
+            raise ValueError(f"gate must have shape {(H,)}, {(T,)}, {(T, 1)} or {(T, H)}, got {tuple(gate.shape)}")
+        kind = (1, 2, 2, 3)[shapes.index(tuple(gate.shape))]
+        gate_at = _arg(gate, "gate", some, gate.shape, dev)
+    f32 = lambda t: OUT_F32 if t is not None and t.dtype is torch.float32 else OUT_BF16
+    at = (_arg(y, "y", bf, (T, H), dev), _arg(post_w, "post_w", some, (H,), dev), gate_at,
+          _arg(pre_w, "pre_w", some, (H,), dev))
+    return Norm(T, H, f32(first), f32(post_w), f32(pre_w), f32(gate), kind, 1 if gate_act else 0, scale, h_scale, eps), dev, at
+
+
+def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_scale=1.0, pre_w=None, eps=1e-6,
+               h_out=None, n=None, stream=None):
+    """The norms before and after a layer with its gate and residual scale:
+    h' = h_scale h + scale act(gate) a, a = rms(y) post_w (or y without post_w), and
+    n = rms(h') pre_w; rms(v) = v / sqrt(mean(v^2) + eps).  h [T, H] bfloat16 or
+    float32 (the residual stream), y [T, H] bfloat16 (the layer's output); gate [H]
+    (per channel; also where T = H), [T] or [T, 1] (per token) or [T, H]; gate_act
+    None or "sigmoid"; weights and gate bfloat16 or float32.  h_out may be h (in
+    place).  Returns (h', n): h' of h's type, n [T, H] bfloat16.  Without y h' is h
+    itself; without pre_w n is None."""
+    import torch
+    p, dev, (y_at, post_at, gate_at, pre_at) = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps,
+                                                          stream)
+    shape = (p.T, p.H)
+    if y is None and h_out is not None:
+        raise ValueError("h_out goes with y")
+    if pre_w is None and n is not None:
+        raise ValueError("n goes with pre_w")
+    if y is not None and h_out is None:
+        h_out = _empty(h, shape, h.dtype, stream)
+    if pre_w is not None and n is None:
+        n = _empty(h, shape, torch.bfloat16, stream)
+    _check(lib().moe_fp4_block_norm(ctypes.byref(p), h.data_ptr(), y_at, post_at, gate_at, pre_at,
+                                    _arg(h_out, "h_out", (h.dtype,), shape, dev),
+                                    _arg(n, "n", (torch.bfloat16,), shape, dev), _raw_stream(stream, dev)))
+    return (h if y is None else h_out), n
+
+
+def block_norm_grad(dh, dn, h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_scale=1.0, pre_w=None,
+                    eps=1e-6, d_h=None, workspace=None, stream=None):
+    """The gradient of block_norm(): dh and dn are those of h' and n (dh None: zero;
+    dn None without pre_w), h is the h' that block_norm() returned (None without
+    pre_w), the rest as block_norm() had it.  d_h may be dh (in place).  Returns
+    (d_h, d_y, d_post_w, d_gate, d_pre_w), None for what block_norm() did not have:
+    d_h of h's type, d_y bfloat16, the weights' and the gate's float32 (a gate [T, H]:
+    of its type)."""
+    import torch
+    f32 = (torch.float32,)
+    if (pre_w is None) != (dn is None) or (pre_w is None) != (h is None):
+        raise ValueError("dn and h go with pre_w")
+    first, name = (h, "h") if h is not None else (dh, "dh")
+    p, dev, at = _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
+    T, H = shape = (p.T, p.H)
+    need = _norm_grad_need(T, H)
+    own = (first.dtype,)
+    dh_at, dn_at, h_at = _arg(dh, "dh", own, shape, dev), _arg(dn, "dn", (torch.bfloat16,), shape, dev), None
+    if h is not None:
+        h_at = _arg(h, "h", own, shape, dev)
+    if d_h is None:
+        d_h = _empty(first, shape, first.dtype, stream)
+    new = lambda like, size, dtype: None if like is None else _empty(first, size, dtype, stream)
+    d_y, d_post, d_pre = new(y, shape, torch.bfloat16), new(post_w, (H,), torch.float32), new(pre_w, (H,), torch.float32)
+    d_gate = None if gate is None else new(gate, tuple(gate.shape), gate.dtype if p.gate_kind == 3 else torch.float32)
+    ws = _scratch(workspace, need, first, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib().moe_fp4_block_norm_grad(ctypes.byref(p), dh_at, dn_at, h_at, *at, _arg(d_h, "d_h", own, shape, dev),
+                                         ptr(d_y), ptr(d_post), ptr(d_gate), ptr(d_pre), ws.data_ptr(), ws.numel(),
+                                         _raw_stream(stream, dev)))
+    return d_h, d_y, d_post, d_gate, d_pre
 
 
 def requant_gran_k(src, src_sf, src_gs=None, src_gran=16, dst_gran=32, dst=None, dst_sf=None,

@@ -3,6 +3,7 @@
 // synchronisation; every check runs before the first launch.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -801,6 +802,258 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
     if (p->T > moefp4::kProjectFew) a.order = a.route.sorted_assign;
   }
   st = hip_status(moefp4::launch_project(a, stream), "project");
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+static moefp4_status grouped_check(const moefp4_grouped* p, bool weights) {
+  if (!p) return fail(MOEFP4_EINVAL, "problem is NULL");
+  if (p->M < 0 || p->E < 1 || p->N < 1 || p->K < 1)
+    return fail(MOEFP4_EINVAL, "M must be >= 0, E, N and K positive; got M=%lld E=%d N=%lld K=%lld", (long long)p->M, p->E,
+                (long long)p->N, (long long)p->K);
+  if (p->N % 8 || p->K % 8)
+    return fail(MOEFP4_EINVAL, "N and K must be multiples of 8, got N=%lld K=%lld", (long long)p->N, (long long)p->K);
+  if (p->gran_k != 0 && p->gran_k != 16 && p->gran_k != 32)
+    return fail(MOEFP4_EINVAL, "gran_k must be 0 (bfloat16 weights), 16 or 32, got %d", p->gran_k);
+  if (!weights && p->gran_k != 0) return fail(MOEFP4_EINVAL, "weight gradients have gran_k 0, got %d", p->gran_k);
+  if (p->gran_k != 0 && p->K % 32) return fail(MOEFP4_EINVAL, "FP4 weights need K a multiple of 32, got %lld", (long long)p->K);
+  if (p->out_fmt != MOEFP4_OUT_BF16 && p->out_fmt != MOEFP4_OUT_F32) return fail(MOEFP4_EINVAL, "unknown out_fmt %d", p->out_fmt);
+  const long long lim = 1LL << 40;
+  if (p->E > moefp4::kMaxExperts || p->M > (1LL << 24) || p->N > (1LL << 20) || p->K > (1LL << 20) || p->M * p->N >= lim ||
+      p->M * p->K >= lim || p->N * p->K >= lim / p->E)
+    return fail(MOEFP4_EUNSUPPORTED, "E up to %d, M up to 2^24, N and K up to 2^20, M*N, M*K and E*N*K below 2^40", moefp4::kMaxExperts);
+  return MOEFP4_OK;
+}
+
+struct Span { const void* p; size_t n; };
+
+static bool overlaps(const void* out, size_t bytes, const Span* in, int n) {
+  const char* o = static_cast<const char*>(out);
+  for (int i = 0; i < n; ++i) {
+    const char* q = static_cast<const char*>(in[i].p);
+    if (q && o < q + in[i].n && q < o + bytes) return true;
+  }
+  return false;
+}
+
+// form 0: the product, 1: towards the rows
+static moefp4_status grouped_product(const moefp4_grouped* p, int form, const void* x, const void* w, const uint8_t* w_sf,
+                                     const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
+  moefp4_status st = grouped_check(p, true);
+  if (st != MOEFP4_OK) return st;
+  if (p->M == 0) return ok();
+  if (!x || !w || !offsets || !out) return fail(MOEFP4_EINVAL, "%s, w, offsets and out must be non-NULL", form ? "dy" : "x");
+  if (p->gran_k ? !w_sf : (w_sf || w_gs)) return fail(MOEFP4_EINVAL, "w_sf goes with FP4 weights, and w_gs with them only");
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(w_sf, 16) || misaligned(out, 16) || misaligned(w_gs, 4) ||
+      misaligned(offsets, 4))
+    return fail(MOEFP4_EINVAL, "%s, w, w_sf and out must be 16-byte aligned, w_gs and offsets 4-byte", form ? "dy" : "x");
+  const size_t M = p->M, N = p->N, K = p->K, E = p->E, g = p->gran_k;
+  const Span in[] = {{x, 2 * M * (form ? N : K)}, {w, g ? E * N * (K / 2) : 2 * E * N * K}, {w_sf, g ? E * N * (K / g) : 0},
+                     {w_gs, 4 * E}, {offsets, 4 * (E + 1)}};
+  if (overlaps(out, M * (form ? K : N) * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2), in, 5))
+    return fail(MOEFP4_EINVAL, "out overlaps an input");
+  moefp4::GroupedArgs a;
+  memset(&a, 0, sizeof a);
+  a.M = (int)M;
+  a.E = (int)E;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.gran = p->gran_k;
+  a.out_f32 = p->out_fmt == MOEFP4_OUT_F32;
+  a.p = static_cast<const uint16_t*>(x);
+  if (g) a.w = static_cast<const uint8_t*>(w);
+  else a.q = static_cast<const uint16_t*>(w);
+  a.w_sf = w_sf;
+  a.w_gs = w_gs;
+  a.offsets = offsets;
+  a.out = out;
+  st = hip_status(moefp4::launch_grouped(a, form, stream), form ? "grouped_dx" : "grouped");
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+moefp4_status moe_fp4_grouped(const moefp4_grouped* p, const void* x, const void* w, const uint8_t* w_sf,
+                              const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
+  return grouped_product(p, 0, x, w, w_sf, w_gs, offsets, out, stream);
+}
+
+moefp4_status moe_fp4_grouped_dx(const moefp4_grouped* p, const void* dy, const void* w, const uint8_t* w_sf,
+                                 const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
+  return grouped_product(p, 1, dy, w, w_sf, w_gs, offsets, out, stream);
+}
+
+moefp4_status moe_fp4_grouped_dw(const moefp4_grouped* p, const void* dy, const void* x, const int32_t* offsets,
+                                 void* out, int32_t accumulate, hipStream_t stream) {
+  moefp4_status st = grouped_check(p, false);
+  if (st != MOEFP4_OK) return st;
+  if (!offsets || !out || (p->M > 0 && (!dy || !x))) return fail(MOEFP4_EINVAL, "dy, x, offsets and out must be non-NULL");
+  if (misaligned(dy, 16) || misaligned(x, 16) || misaligned(out, 16) || misaligned(offsets, 4))
+    return fail(MOEFP4_EINVAL, "dy, x and out must be 16-byte aligned, offsets 4-byte");
+  const size_t M = p->M, N = p->N, K = p->K, E = p->E;
+  const Span in[] = {{dy, 2 * M * N}, {x, 2 * M * K}, {offsets, 4 * (E + 1)}};
+  if (overlaps(out, E * N * K * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2), in, 3))
+    return fail(MOEFP4_EINVAL, "out overlaps an input");
+  moefp4::GroupedArgs a;
+  memset(&a, 0, sizeof a);
+  a.M = (int)M;
+  a.E = (int)E;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out_f32 = p->out_fmt == MOEFP4_OUT_F32;
+  a.accumulate = accumulate != 0;
+  a.p = static_cast<const uint16_t*>(dy);
+  a.q = static_cast<const uint16_t*>(x);
+  a.offsets = offsets;
+  a.out = out;
+  st = hip_status(moefp4::launch_grouped(a, 2, stream), "grouped_dw");
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+static moefp4_status norm_check(const moefp4_norm* p) {
+  if (!p) return fail(MOEFP4_EINVAL, "problem is NULL");
+  if (p->T < 0 || p->H < 8 || p->H % 8)
+    return fail(MOEFP4_EINVAL, "T must be >= 0 and H a positive multiple of 8, got T=%lld H=%lld", (long long)p->T, (long long)p->H);
+  for (int32_t f : {p->h_fmt, p->post_fmt, p->pre_fmt, p->gate_fmt})
+    if (f != MOEFP4_OUT_BF16 && f != MOEFP4_OUT_F32) return fail(MOEFP4_EINVAL, "unknown format %d", f);
+  if (p->gate_kind < MOEFP4_GATE_NONE || p->gate_kind > MOEFP4_GATE_ELEMENT)
+    return fail(MOEFP4_EINVAL, "unknown gate_kind %d", p->gate_kind);
+  if (p->gate_sigmoid != 0 && p->gate_sigmoid != 1) return fail(MOEFP4_EINVAL, "gate_sigmoid must be 0 or 1, got %d", p->gate_sigmoid);
+  if (!isfinite(p->scale) || !isfinite(p->h_scale) || !isfinite(p->eps) || p->eps < 0)
+    return fail(MOEFP4_EINVAL, "scale, h_scale and eps must be finite, eps >= 0");
+  if (p->H > moefp4::kNormMostH || p->T > (1LL << 24) || p->T * p->H >= (1LL << 40))
+    return fail(MOEFP4_EUNSUPPORTED, "H up to %d, T up to 2^24, T*H below 2^40", moefp4::kNormMostH);
+  return MOEFP4_OK;
+}
+
+static size_t gate_elements(const moefp4_norm* p) {
+  return p->gate_kind == MOEFP4_GATE_CHANNEL ? p->H : p->gate_kind == MOEFP4_GATE_TOKEN ? p->T :
+         p->gate_kind == MOEFP4_GATE_ELEMENT ? (size_t)p->T * p->H : 0;
+}
+
+// What both directions take: y, the gate and the weights go together as the problem says.
+static moefp4_status norm_operands(const moefp4_norm* p, const void* y, const void* post_w, const void* gate, const void* pre_w) {
+  if (!y && (post_w || gate || p->gate_kind != MOEFP4_GATE_NONE)) return fail(MOEFP4_EINVAL, "post_w and a gate need y");
+  if ((gate != nullptr) != (p->gate_kind != MOEFP4_GATE_NONE)) return fail(MOEFP4_EINVAL, "the gate goes with a gate_kind");
+  if (!y && !pre_w) return fail(MOEFP4_EINVAL, "y or pre_w must be non-NULL");
+  if (misaligned(y, 16) || misaligned(post_w, 16) || misaligned(pre_w, 16) ||
+      misaligned(gate, p->gate_kind == MOEFP4_GATE_TOKEN ? 4 : 16))
+    return fail(MOEFP4_EINVAL, "y, the weights and the gate must be 16-byte aligned (a gate per token 4-byte)");
+  return MOEFP4_OK;
+}
+
+static moefp4::NormArgs norm_args(const moefp4_norm* p) {
+  moefp4::NormArgs a;
+  memset(&a, 0, sizeof a);
+  a.T = p->T;
+  a.H = (int)p->H;
+  a.h_f32 = p->h_fmt == MOEFP4_OUT_F32;
+  a.post_f32 = p->post_fmt == MOEFP4_OUT_F32;
+  a.pre_f32 = p->pre_fmt == MOEFP4_OUT_F32;
+  a.gate_f32 = p->gate_fmt == MOEFP4_OUT_F32;
+  a.gate_kind = p->gate_kind;
+  a.gate_act = p->gate_sigmoid;
+  a.scale = p->scale;
+  a.h_scale = p->h_scale;
+  a.eps = p->eps;
+  return a;
+}
+
+moefp4_status moe_fp4_block_norm(const moefp4_norm* p, const void* h, const void* y, const void* post_w,
+                                 const void* gate, const void* pre_w, void* h_out, void* n, hipStream_t stream) {
+  moefp4_status st = norm_check(p);
+  if (st != MOEFP4_OK) return st;
+  if (p->T == 0) return ok();
+  st = norm_operands(p, y, post_w, gate, pre_w);
+  if (st != MOEFP4_OK) return st;
+  if (!h || (y != nullptr) != (h_out != nullptr) || (pre_w != nullptr) != (n != nullptr))
+    return fail(MOEFP4_EINVAL, "h must be non-NULL, h_out go with y and n with pre_w");
+  if (misaligned(h, 16) || misaligned(h_out, 16) || misaligned(n, 16))
+    return fail(MOEFP4_EINVAL, "h, h_out and n must be 16-byte aligned");
+  const size_t TH = (size_t)p->T * p->H, hb = p->h_fmt == MOEFP4_OUT_F32 ? 4 : 2;
+  const size_t wb[2] = {(size_t)p->H * (p->post_fmt == MOEFP4_OUT_F32 ? 4 : 2), (size_t)p->H * (p->pre_fmt == MOEFP4_OUT_F32 ? 4 : 2)};
+  const Span in[] = {{y, 2 * TH}, {post_w, wb[0]}, {gate, gate_elements(p) * (p->gate_fmt == MOEFP4_OUT_F32 ? 4 : 2)},
+                     {pre_w, wb[1]}, {h, h == h_out ? 0 : hb * TH}};
+  const Span out_h = {h_out, hb * TH}, in_h = {h, hb * TH};
+  if ((h_out && overlaps(h_out, hb * TH, in, 5)) || (n && (overlaps(n, 2 * TH, in, 4) || overlaps(n, 2 * TH, &in_h, 1) ||
+                                                           overlaps(n, 2 * TH, &out_h, 1))))
+    return fail(MOEFP4_EINVAL, "an output overlaps an input or the other output (h_out may be h itself)");
+  moefp4::NormArgs a = norm_args(p);
+  a.h = h;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.pre_w = pre_w;
+  a.h_out = h_out;
+  a.n = n;
+  st = hip_status(moefp4::launch_block_norm(a, stream), "block_norm");
+  return st == MOEFP4_OK ? ok() : st;
+}
+
+static size_t norm_grad_bytes(const moefp4_norm* p) {
+  // (rows of a smaller T take no more parts)
+  const size_t n = (size_t)moefp4::norm_grad_parts(p->T, (int)p->H) * p->H * 3 * 4;
+  return n > 256 ? align_up(n) : 256;
+}
+
+moefp4_status moe_fp4_block_norm_grad_workspace_bytes(const moefp4_norm* p, size_t* bytes) {
+  const moefp4_status st = norm_check(p);
+  if (st != MOEFP4_OK) return st;
+  if (!bytes) return fail(MOEFP4_EINVAL, "bytes is NULL");
+  *bytes = norm_grad_bytes(p);
+  return ok();
+}
+
+moefp4_status moe_fp4_block_norm_grad(const moefp4_norm* p, const void* dh, const void* dn, const void* h, const void* y,
+                                      const void* post_w, const void* gate, const void* pre_w, void* d_h, void* d_y,
+                                      float* d_post_w, void* d_gate, float* d_pre_w, void* workspace, size_t ws_bytes,
+                                      hipStream_t stream) {
+  moefp4_status st = norm_check(p);
+  if (st != MOEFP4_OK) return st;
+  const bool rows = p->T > 0;  // (tensors without elements may have no address)
+  if (rows) {
+    st = norm_operands(p, y, post_w, gate, pre_w);
+    if (st != MOEFP4_OK) return st;
+    if (!d_h || (y != nullptr) != (d_y != nullptr) || (gate != nullptr) != (d_gate != nullptr))
+      return fail(MOEFP4_EINVAL, "d_h must be non-NULL, d_y go with y and d_gate with the gate");
+    if ((pre_w != nullptr) != (dn != nullptr) || (pre_w != nullptr) != (h != nullptr))
+      return fail(MOEFP4_EINVAL, "dn and h go with pre_w");
+    if (!pre_w && !dh) return fail(MOEFP4_EINVAL, "dh or pre_w (and dn) must be non-NULL");
+  }
+  if ((post_w != nullptr) != (d_post_w != nullptr) || (pre_w != nullptr) != (d_pre_w != nullptr))
+    return fail(MOEFP4_EINVAL, "d_post_w goes with post_w and d_pre_w with pre_w");
+  if (p->gate_kind == MOEFP4_GATE_CHANNEL && !d_gate) return fail(MOEFP4_EINVAL, "d_gate must be non-NULL with a gate");
+  if (misaligned(dh, 16) || misaligned(dn, 16) || misaligned(h, 16) || misaligned(d_h, 16) || misaligned(d_y, 16) ||
+      misaligned(d_post_w, 16) || misaligned(d_pre_w, 16) || misaligned(d_gate, p->gate_kind == MOEFP4_GATE_TOKEN ? 4 : 16))
+    return fail(MOEFP4_EINVAL, "dh, dn, h, d_h, d_y, d_post_w, d_pre_w and d_gate must be 16-byte aligned (a gate per token 4-byte)");
+  const size_t need = norm_grad_bytes(p);
+  if (!workspace || ws_bytes < need)
+    return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  if (misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  const size_t T = p->T, H = p->H, TH = T * H, hb = p->h_fmt == MOEFP4_OUT_F32 ? 4 : 2, gb = p->gate_fmt == MOEFP4_OUT_F32 ? 4 : 2;
+  const size_t ge = gate_elements(p);
+  const Span in[] = {{dn, 2 * TH}, {h, hb * TH}, {y, 2 * TH}, {post_w, H * (p->post_fmt == MOEFP4_OUT_F32 ? 4 : 2)}, {gate, ge * gb},
+                     {pre_w, H * (p->pre_fmt == MOEFP4_OUT_F32 ? 4 : 2)}, {dh, hb * TH}};
+  const Span out[] = {{d_h, hb * TH}, {d_y, 2 * TH}, {d_post_w, 4 * H}, {d_gate, ge * (p->gate_kind == MOEFP4_GATE_ELEMENT ? gb : 4)},
+                      {d_pre_w, 4 * H}, {workspace, need}};
+  for (int i = 0; i < 6; ++i) {
+    if (!out[i].p) continue;
+    // (d_h may be dh, the last input)
+    if (overlaps(out[i].p, out[i].n, in, i == 0 && d_h == dh ? 6 : 7) || overlaps(out[i].p, out[i].n, out + i + 1, 5 - i))
+      return fail(MOEFP4_EINVAL, "an output or the workspace overlaps an input or another output (d_h may be dh itself)");
+  }
+  moefp4::NormArgs a = norm_args(p);
+  a.h = h;
+  a.y = y;
+  a.post_w = post_w;
+  a.gate = gate;
+  a.pre_w = pre_w;
+  a.dh = dh;
+  a.dn = dn;
+  a.d_h = d_h;
+  a.d_y = d_y;
+  a.d_gate = d_gate;
+  a.d_post_w = d_post_w;
+  a.d_pre_w = d_pre_w;
+  a.part = static_cast<float*>(workspace);
+  st = hip_status(moefp4::launch_block_norm_grad(a, stream), "block_norm_grad");
   return st == MOEFP4_OK ? ok() : st;
 }
 

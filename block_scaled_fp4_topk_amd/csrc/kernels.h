@@ -205,6 +205,39 @@ long long project_u_rows(long long T, long long K, long long R);
 long long project_part_rows(long long T, long long N, long long K);
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
 
+// Products grouped by expert (moe_fp4_grouped, _dx, _dw).  form 0: p = x [M, K],
+// q = W [E, N, K], out [M, N]; 1: p = dy [M, N], q = W, out [M, K]; 2: p = dy,
+// q = x, out [E, N, K].
+struct GroupedArgs {
+  int M, E, N, K;
+  int gran;           // 0: bfloat16 weights; 16, 32: FP4 (w, w_sf, w_gs in place of q)
+  int out_f32, accumulate;
+  const uint16_t *p, *q;
+  const uint8_t *w, *w_sf;
+  const float* w_gs;
+  const int32_t* offsets;
+  void* out;
+};
+hipError_t launch_grouped(const GroupedArgs& a, int form, hipStream_t s);
+
+// Block norms (moe_fp4_block_norm, _grad).  gate_kind 0: none, 1: [H], 2: [T],
+// 3: [T, H]; gate_act 1: sigmoid.
+struct NormArgs {
+  long long T;
+  int H, h_f32, post_f32, pre_f32, gate_f32, gate_kind, gate_act;
+  float scale, h_scale, eps;
+  const void *h, *y, *post_w, *gate, *pre_w;
+  void *h_out, *n;
+  const void *dh, *dn;
+  void *d_h, *d_y, *d_gate;
+  float *d_post_w, *d_pre_w;
+  float* part;  // [3][norm_grad_parts][H]
+};
+constexpr int kNormMostH = 16384;
+int norm_grad_parts(long long T, int H);
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_block_norm_grad(const NormArgs& a, hipStream_t s);
+
 struct FcArgs {
   const uint8_t* w;          // [E, N, K/2]
   const uint8_t* wsf;        // [E, N, K/gran]

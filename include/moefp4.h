@@ -312,6 +312,82 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
                               const float* w_gs, const void* lora_a, const void* lora_b, const int32_t* id,
                               const float* scale, void* out, void* workspace, size_t ws_bytes, hipStream_t stream);
 
+/* Matrix products grouped by expert with ragged sizes, and their gradients.
+ * The M rows of x, y, dy and dx lie in expert order: expert e's are
+ * [offsets[e], offsets[e + 1]), offsets [E + 1] int32 device memory, ascending
+ * (as moe_fp4_route gives them); an expert may have no rows, and rows outside
+ * [offsets[0], offsets[E]) are not read and their outputs are left as they are.
+ * (Offsets are taken within [0, M], so that no value of them reaches memory
+ * outside the tensors; where they descend, rows may be computed with any of the
+ * experts whose range holds them, or not at all.)
+ *   moe_fp4_grouped     y[r]  = W_e x[r]                 [M, N]
+ *   moe_fp4_grouped_dx  dx[r] = W_e^T dy[r]              [M, K]
+ *   moe_fp4_grouped_dw  dW_e  = sum over e's rows of dy[r] x[r]^T   [E, N, K]
+ * W_e [N, K]: bfloat16 (gran_k 0; w [E, N, K], w_sf and w_gs NULL), or FP4 in
+ * the RAW layout above with group16 or group32 scales (and w_gs [E] or NULL):
+ * the gradient through frozen experts.  x and dy bfloat16, FP32 accumulation,
+ * outputs bfloat16 or float32 (out_fmt, moefp4_out_fmt).  dw is written whole,
+ * zeros for an expert without rows; with accumulate != 0 the sums are added to
+ * what it holds (an expert without rows is left as it is). */
+typedef struct moefp4_grouped {
+  int64_t M, N, K;
+  int32_t E, gran_k, out_fmt;
+} moefp4_grouped;
+
+/* x, dy, w, w_sf and out 16-byte aligned, all device memory; N and K multiples
+ * of 8, K of 32 with FP4 weights (EINVAL otherwise); E up to 512, M up to 2^24, N
+ * and K up to 2^20, M*N, M*K and E*N*K below 2^40 (EUNSUPPORTED otherwise).  out
+ * overlaps no input (EINVAL).  No workspace.  Enqueued on `stream`. */
+moefp4_status moe_fp4_grouped(const moefp4_grouped* p, const void* x, const void* w, const uint8_t* w_sf,
+                              const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream);
+moefp4_status moe_fp4_grouped_dx(const moefp4_grouped* p, const void* dy, const void* w, const uint8_t* w_sf,
+                                 const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream);
+moefp4_status moe_fp4_grouped_dw(const moefp4_grouped* p, const void* dy, const void* x, const int32_t* offsets,
+                                 void* out, int32_t accumulate, hipStream_t stream);
+
+/* The norms before and after a layer, fused with the layer's gate and residual
+ * scale (a row of h is a token's residual stream, y the layer's output):
+ *   a  = rms(y) * post_w  (a = y without post_w),  rms(v) = v / sqrt(mean(v^2) + eps)
+ *   h' = h_scale * h + scale * act(gate) * a
+ *   n  = rms(h') * pre_w
+ * in FP32 throughout; n is formed from h' before its rounding to h's type.
+ * Without y (NULL; then post_w, gate and h_out are NULL too): n = rms(h) * pre_w,
+ * the norm before the first layer.  Without pre_w (NULL; then n too): h' alone.
+ * gate: none, one per channel [H], per token [T], or per element [T, H]; act the
+ * identity or the sigmoid.  h and h' [T, H] bfloat16 or float32 (h_fmt,
+ * moefp4_out_fmt), y and n [T, H] bfloat16, post_w and pre_w [H] and the gate
+ * bfloat16 or float32 (post_fmt, pre_fmt, gate_fmt). */
+typedef enum moefp4_gate_kind {
+  MOEFP4_GATE_NONE = 0, MOEFP4_GATE_CHANNEL = 1, MOEFP4_GATE_TOKEN = 2, MOEFP4_GATE_ELEMENT = 3
+} moefp4_gate_kind;
+typedef struct moefp4_norm {
+  int64_t T, H;
+  int32_t h_fmt, post_fmt, pre_fmt, gate_fmt, gate_kind, gate_sigmoid;
+  float scale, h_scale, eps;
+} moefp4_norm;
+
+/* All device memory, 16-byte aligned (a gate per token 4-byte); H a positive
+ * multiple of 8, eps >= 0, scale, h_scale and eps finite (EINVAL otherwise); H up
+ * to 16384, T up to 2^24, T*H below 2^40 (EUNSUPPORTED otherwise).  h_out may be
+ * h itself (in place); no other output overlaps an input or the other one
+ * (EINVAL).  No workspace.  Enqueued on `stream`. */
+moefp4_status moe_fp4_block_norm(const moefp4_norm* p, const void* h, const void* y, const void* post_w,
+                                 const void* gate, const void* pre_w, void* h_out, void* n, hipStream_t stream);
+
+/* Its gradient: from dh and dn, those of h' and n (dh [T, H] of h's type or NULL:
+ * zero; dn [T, H] bfloat16), and h here the h' that the call before gave, d_h
+ * [T, H] of h's type, d_y [T, H] bfloat16, and float32 d_post_w [H], d_pre_w [H]
+ * and d_gate [H] or [T] (a gate per element: [T, H] of the gate's type).  What the
+ * call before did not have is NULL here too: without y also d_y, without pre_w
+ * also h, dn and d_pre_w (then dh is needed).  Sums over rows are formed in a
+ * fixed order.  d_h may be dh itself; no other output overlaps anything
+ * (EINVAL). */
+moefp4_status moe_fp4_block_norm_grad_workspace_bytes(const moefp4_norm* p, size_t* bytes);
+moefp4_status moe_fp4_block_norm_grad(const moefp4_norm* p, const void* dh, const void* dn, const void* h, const void* y,
+                                      const void* post_w, const void* gate, const void* pre_w, void* d_h, void* d_y,
+                                      float* d_post_w, void* d_gate, float* d_pre_w, void* workspace, size_t ws_bytes,
+                                      hipStream_t stream);
+
 /* Reorder group32 weights (RAW layout, UE8M0 scales) into the GEMM layout
  * of the prefill kernels.  which = 0: w13 (N = 2I rows in w13_order, K =
  * H); which = 1: w2 (N = H, K = I).  The GEMM's weight rows are taken in
