@@ -22,16 +22,22 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-// 16 bytes per lane from base + off to consecutive places in LDS.  As an
-// instruction of its own (it writes no register): the compiler takes a builtin
-// direct load to alias every transposing LDS read, and waits for it there.
-// What ends it is wait_all.
-__device__ __forceinline__ void direct_load(const uint8_t* base, uint32_t off, const uint8_t* lds) {
+// 16 bytes per lane from `off` of a buffer to consecutive places in LDS; zeros
+// for what lies behind the buffer's end.  As an instruction of its own (it writes
+// no register): the compiler takes a builtin direct load to alias every
+// transposing LDS read, and waits for it there.  What ends it is wait_all.
+__device__ __forceinline__ void direct_load(const v4i& buffer, uint32_t off, uint32_t uniform_off, const uint8_t* lds) {
   typedef const __attribute__((address_space(3))) uint8_t* lds1;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"((uint32_t)(uintptr_t)(lds1)lds), "v"(off), "s"(base)
+               : "s"((uint32_t)(uintptr_t)(lds1)lds), "v"(off), "s"(buffer), "s"(uniform_off)
                : "memory");
+}
+
+// A buffer descriptor: `bytes` from p on.
+__device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uintptr_t>(p);
+  return v4i{(int)at, (int)(at >> 32) & 0xFFFF, (int)bytes, 0x00020000};
 }
 
 // ---------------------------------------------------------------------------
@@ -99,49 +105,56 @@ __device__ __forceinline__ int tswz(int r) { return (r & 3) | ((r >> 1) & 4); }
 // NTH threads load it, 16 bytes per lane straight to LDS.
 template <bool TR, int SIZE, int NTH>
 struct Operand {
+  static_assert(!TR || SIZE >= 128, "tswz swaps the chunks of 256 bytes");
   static constexpr int kPieces = SIZE * 8 / NTH;
   static constexpr int kBytes = SIZE * kS * 2;
   const uint8_t* base;  // uniform
   uint32_t ld;          // bytes per row
+  int valid;            // rows (TR: elements across) that exist
   uint32_t off[kPieces];
 
-  // valid: rows (TR: elements across) that exist
-  __device__ __forceinline__ void init(const void* p, uint32_t ld_bytes, int valid) {
-    base = static_cast<const uint8_t*>(p);
-    ld = ld_bytes;
+  // Where load i's lane is in a stage: row, and element of the row, as their LDS
+  // places (lane order) say.
+  __device__ __forceinline__ static int row(int i) {
+    constexpr int per = TR ? SIZE / 8 : 8;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if constexpr (TR) {
-        constexpr int per = SIZE / 8;  // pieces per row
-        const int r = (wave * kPieces + i) * (64 / per) + lane / per, piece = lane % per;
-        const int c = (((piece >> 1) ^ tswz(r)) << 4) + ((piece & 1) << 3);
-        off[i] = 2 * min(c, valid - 8);
-      } else {
-        const int r = (wave * kPieces + i) * 8 + (lane >> 3);
-        off[i] = min(r, valid - 1) * ld;
-      }
-    }
+    return (wave * kPieces + i) * (64 / per) + lane / per;
+  }
+  __device__ __forceinline__ static int col(int i) {
+    const int lane = threadIdx.x & 63, r = row(i);
+    if constexpr (TR) return (((lane % (SIZE / 8) >> 1) ^ tswz(r)) << 4) + ((lane & 1) << 3);
+    else return ((lane & 7) ^ pswz(r)) << 3;
   }
 
-  // stage s of a sum of n elements (past the last one: the last one again)
-  __device__ __forceinline__ void load(int s, int n, uint8_t* lds) const {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint8_t* at = TR ? base + (size_t)s * kS * ld : base;
+  // (what lies outside the tile is fetched from the last row or column inside)
+  __device__ __forceinline__ void init(const void* p, uint32_t ld_bytes, int exist) {
+    base = static_cast<const uint8_t*>(p);
+    ld = ld_bytes;
+    valid = exist;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      uint32_t o;
-      if constexpr (TR) {
-        constexpr int per = SIZE / 8;
-        const int r = (wave * kPieces + i) * (64 / per) + lane / per;
-        o = off[i] + (uint32_t)min(r, n - 1 - s * kS) * ld;
-      } else {
-        const int r = (wave * kPieces + i) * 8 + (lane >> 3);
-        o = off[i] + min(s * kS * 2 + (((lane & 7) ^ pswz(r)) << 4), 2 * (n - 8));
-      }
-      direct_load(at, o, lds + (wave * kPieces + i) * 1024);
+    for (int i = 0; i < kPieces; ++i)
+      off[i] = TR ? __umul24(row(i), ld) + 2 * min(col(i), valid - 8) : __umul24(min(row(i), valid - 1), ld) + 2 * col(i);
+  }
+
+  // Stage s of a sum of n elements, by kPieces loads.  (Behind the sum's end: the
+  // next row's elements, or zeros behind the last row; a stage behind the last one
+  // is zeros, without any access to memory.)
+  struct Stage { v4i buffer; uint32_t at; };
+  __device__ __forceinline__ Stage stage(int s, int n) const {
+    if constexpr (TR) {
+      const int rows = min(n - s * kS, kS);
+      return {buffer_of(base + (size_t)s * kS * ld, rows > 0 ? (rows - 1) * ld + 2 * min(valid, SIZE) : 0), 0u};
+    } else {
+      return {buffer_of(base, s * kS < n ? (min(valid, SIZE) - 1) * ld + 2 * n : 0), (uint32_t)s * kS * 2};
     }
+  }
+  __device__ __forceinline__ void piece(const Stage& s, int i, uint8_t* lds) const {
+    direct_load(s.buffer, off[i], s.at, lds + (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kPieces + i) * 1024);
+  }
+  __device__ __forceinline__ void load(int s, int n, uint8_t* lds) const {
+    const Stage st = stage(s, n);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) piece(st, i, lds);
   }
 
   // zeros behind the sum's last element in its last stage, of which `left` exist
@@ -165,21 +178,29 @@ struct Operand {
   }
 
   // The 16 rows from w0 + 16 t on, elements 32 ks .. + 31 of the stage, as a
-  // matrix operand (lane: row lane % 16, elements 8 (lane / 16) .. + 7).
-  __device__ __forceinline__ static u32x4 frag(const uint8_t* lds, uint32_t lane_at, int t, int ks) {
+  // matrix operand (lane: row lane % 16, elements 8 (lane / 16) .. + 7).  at:
+  // lane_at + the stage's place in LDS, which is a multiple of 4096.
+  __device__ __forceinline__ static u32x4 frag(uint32_t at, int t, int ks) {
     if constexpr (TR) {
-      const uint8_t* p = lds + (lane_at ^ (t << 5)) + ks * 32 * (SIZE * 2);
       typedef __attribute__((address_space(3))) v4s* lds4;
-      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
-      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * SIZE * 2));
+      const uint32_t p = at ^ (t << 5);
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)p + ks * 4 * SIZE * 2);
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(uintptr_t)p + ks * 4 * SIZE * 2 + SIZE);
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
       return u32x4{x[0], x[1], y[0], y[1]};
     } else {
-      return *reinterpret_cast<const u32x4*>(lds + (lane_at ^ (ks << 6)) + t * 2048);
+      typedef const __attribute__((address_space(3))) u32x4* lds16;
+      return ((lds16)(uintptr_t)(at ^ (ks << 6)))[t * 128];
     }
   }
 };
+
+// LDS as the instructions address it.
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  typedef const __attribute__((address_space(3))) uint8_t* lds1;
+  return (uint32_t)(uintptr_t)(lds1)p;
+}
 
 // Eight E2M1 codes times an E4M3 scale -> bfloat16, exact (6 significant bits):
 // multiplied as floats, whose upper halves are the result.
@@ -237,20 +258,27 @@ struct Fp4Operand : Operand<TR, SIZE, NTH> {
     else s = ps[os];
   }
 
-  // what was fetched into stage buffer lds, and the next stage asked for
-  __device__ __forceinline__ void load(int st, int n, uint8_t* lds) {
+  // What was fetched into stage buffer lds, eight codes at a time, and then the
+  // next stage asked for (behind the last one: the last one again).
+  static constexpr int kPieces = 5;
+  struct Stage { int st, n; };
+  __device__ __forceinline__ Stage stage(int st, int n) const { return {st, n}; }
+  __device__ __forceinline__ void piece(const Stage& of, int j, uint8_t* lds) {
+    if (j == 4) {
+      fetch(min(of.st + 1, (of.n - 1) / kS), of.n);
+      return;
+    }
     const int row = threadIdx.x / kPer, piece = threadIdx.x % kPer;
     uint32_t at = TR ? row * (SIZE * 2) + ((2 * piece ^ tswz(row)) << 5) : row * 128 + ((4 * piece ^ pswz(row)) << 4);
     asm volatile("" : "+v"(at));
+    u32x4 v;
+    if (GRAN == 16) v = dq8_scaled_bf16(c[j], e4m3_to_f32((s >> (8 * (j >> 1))) & 0xFFu));
+    else v = __builtin_bit_cast(u32x4, dq8_bf16(c[j], ue8m0_to_f32(s)));
+    *reinterpret_cast<u32x4*>(lds + (TR ? (at ^ ((j >> 1) << 5)) + 16 * (j & 1) : at ^ (j << 4))) = v;
+  }
+  __device__ __forceinline__ void load(int st, int n, uint8_t* lds) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 v;
-      if (GRAN == 16) v = dq8_scaled_bf16(c[j], e4m3_to_f32((s >> (8 * (j >> 1))) & 0xFFu));
-      else v = __builtin_bit_cast(u32x4, dq8_bf16(c[j], ue8m0_to_f32(s)));
-      *reinterpret_cast<u32x4*>(lds + (TR ? (at ^ ((j >> 1) << 5)) + 16 * (j & 1) : at ^ (j << 4))) = v;
-      __builtin_amdgcn_sched_barrier(0);  // (one after the other: registers are short)
-    }
-    fetch(min(st + 1, (n - 1) / kS), n);  // (behind the last stage: the last one again)
+    for (int j = 0; j < kPieces; ++j) piece(stage(st, n), j, lds);
   }
 };
 
@@ -259,10 +287,12 @@ struct WeightOperand { typedef Fp4Operand<TR, SIZE, NTH, GRAN> type; };
 template <bool TR, int SIZE, int NTH>
 struct WeightOperand<TR, SIZE, NTH, 0> { typedef Operand<TR, SIZE, NTH> type; };
 
-// Every wave's loads and LDS accesses done, and a barrier.
+// Every wave's LDS accesses done, and its loads but the LEFT newest (LEFT < 16),
+// and a barrier.
+template <int LEFT>
 __device__ __forceinline__ void wait_all() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070 | LEFT);  // vmcnt(LEFT) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -271,14 +301,17 @@ __device__ __forceinline__ void wait_all() {
 // the tiled product
 
 // P x Q outputs per workgroup: P along the rows (TN: along N), Q along the
-// output's contiguous side; WP x WQ waves.  GRAN: 0, or FP4 weights' group.
-template <int FORM, int GRAN, int P, int Q, int WP, int WQ>
-__global__ __launch_bounds__(WP * WQ * 64, 2) void grouped_tile_kernel(GroupedArgs a) {
+// output's contiguous side; WP x WQ waves.  GRAN: 0, or FP4 weights' group.  NB:
+// stages of the Q side in LDS (of the P side 2): where the weights come from HBM,
+// two stages of them in flight.
+template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
+__global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) void grouped_tile_kernel(GroupedArgs a) {
   constexpr int NTH = WP * WQ * 64;
   constexpr int NP = P / WP / 16, NQ = Q / WQ / 16;  // a wave's 16-row tiles
   typedef Operand<FORM == TN, P, NTH> OpP;
   typedef typename WeightOperand<FORM != NT, Q, NTH, GRAN>::type OpQ;
-  __shared__ __attribute__((aligned(16))) uint8_t s_p0[OpP::kBytes], s_p1[OpP::kBytes], s_q0[OpQ::kBytes], s_q1[OpQ::kBytes];
+  constexpr bool kFar = GRAN == 0 && NB == 3;  // the Q side's loads run two stages ahead, else one
+  __shared__ __attribute__((aligned(4096))) uint8_t s_p[2 * OpP::kBytes], s_q[NB * OpQ::kBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -332,88 +365,120 @@ __global__ __launch_bounds__(WP * WQ * 64, 2) void grouped_tile_kernel(GroupedAr
   // Half of the row tiles at a time (a phase): 16 products per wave at 128 x 64.
   constexpr int NH = NP / 2;
   u32x4 fq[2][NQ], fp[2][NH];
-  uint32_t at_q = OpQ::lane_at(wq), at_p = OpP::lane_at(wp);
-  auto read_q = [&](int buf, int ks) __attribute__((always_inline)) {
-    asm volatile("" : "+v"(at_q));  // (the tiles' addresses are formed anew: registers are short)
+  const uint32_t at_q = OpQ::lane_at(wq) + lds_address(s_q), at_p = OpP::lane_at(wp) + lds_address(s_p);
+  auto read_q = [&](uint32_t buf, int ks) __attribute__((always_inline)) {
+    uint32_t at = at_q + buf;
+    asm volatile("" : "+v"(at));  // (the tiles' addresses are formed anew: registers are short)
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) fq[ks][i] = OpQ::frag(buf ? s_q1 : s_q0, at_q, i, ks);
+    for (int i = 0; i < NQ; ++i) fq[ks][i] = OpQ::frag(at, i, ks);
   };
-  auto read_p = [&](int buf, int ks, int h) __attribute__((always_inline)) {
-    asm volatile("" : "+v"(at_p));
+  auto read_p = [&](uint32_t buf, int ks, int h) __attribute__((always_inline)) {
+    uint32_t at = at_p + buf;
+    asm volatile("" : "+v"(at));
 #pragma unroll
-    for (int j = 0; j < NH; ++j) fp[h][j] = OpP::frag(buf ? s_p1 : s_p0, at_p, NH * h + j, ks);
+    for (int j = 0; j < NH; ++j) fp[h][j] = OpP::frag(at, NH * h + j, ks);
+  };
+  auto multiply_one = [&](int ks, int h, int j, int i) __attribute__((always_inline)) {
+    v4f& c = acc[i][NH * h + j];
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fq[ks][i]), __builtin_bit_cast(v8bf, fp[h][j]), c, 0,
+                                                0, 0);
   };
   auto multiply = [&](int ks, int h) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < NH; ++j)
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        v4f& c = acc[i][NH * h + j];
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fq[ks][i]), __builtin_bit_cast(v8bf, fp[h][j]),
-                                                    c, 0, 0, 0);
-      }
+      for (int i = 0; i < NQ; ++i) multiply_one(ks, h, j, i);
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto load = [&](int s, int buf) __attribute__((always_inline)) {
-    op.load(s, sum, buf ? s_p1 : s_p0);
-    oq.load(s, sum, buf ? s_q1 : s_q0);
-  };
-  // A stage's loads have landed, and every wave has read the one before.
-  auto handover = [&](bool last, int buf) __attribute__((always_inline)) {
+  // A stage's loads have landed, and every wave has read the one before; what lies
+  // behind the sum in its last stage is cleared.
+  auto handover = [&](bool last, uint32_t pb, uint32_t qb) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    wait_all();
-    if (last && tail) {
-      OpP::clear(tail, buf ? s_p1 : s_p0);
-      OpQ::clear(tail, buf ? s_q1 : s_q0);
-      wait_all();
+    wait_all<kFar ? OpQ::kPieces : 0>();  // (the stage after it is still on its way)
+    if (tail && last) {
+      OpP::clear(tail, s_p + pb);
+      OpQ::clear(tail, s_q + qb);
+      wait_all<kFar ? OpQ::kPieces : 0>();
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage s in buffer buf, in four phases: the operands of a phase come while the
-  // one before multiplies.  The one barrier lies before the last phase, whose
-  // operands are in registers: behind it the next stage's first operands are read.
-  // NEXT: stages behind this one (2: or more).
-  auto stage = [&](auto NEXT, int s, int buf) __attribute__((always_inline)) {
-    read_p(buf, 0, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(0, 0);
-    read_q(buf, 1);
-    read_p(buf, 1, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(0, 1);
-    read_p(buf, 1, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(1, 0);
-    if constexpr (NEXT.value > 0) {
-      handover(NEXT.value == 1, buf ^ 1);
-      if constexpr (NEXT.value > 1) load(s + 2, buf);
-      read_q(buf ^ 1, 0);
-      read_p(buf ^ 1, 0, 0);
+  uint32_t pb = 0, qb = 0;  // where the stage at hand lies
+  auto next_q = [](uint32_t b) __attribute__((always_inline)) { return b + OpQ::kBytes == NB * OpQ::kBytes ? 0 : b + OpQ::kBytes; };
+  // HALVES: of a wave's row tiles, those that exist.  Others are neither read nor
+  // multiplied, so that an expert's short last tile takes as much less time.
+  auto stages = [&](auto HALVES) __attribute__((always_inline)) {
+    constexpr bool some = HALVES.value > 0, both = HALVES.value > 1;
+    // A stage in four phases: the operands of a phase come while the one before
+    // multiplies.  The one barrier lies before the last phase, whose operands are
+    // in registers: behind it the next stage's first operands are read, and the
+    // loads of a later stage go between the products.
+    auto three = [&]() __attribute__((always_inline)) {
+      if constexpr (both) read_p(pb, 0, 1);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    multiply(1, 1);
-  };
-  typedef std::integral_constant<int, 0> Last;
-  typedef std::integral_constant<int, 1> One;
-  typedef std::integral_constant<int, 2> More;
-  // (the last stage is always in buffer 1: no branch inside the loop)
-  if (FORM != TN || nst > 0) {
-    const int first = nst & 1;
-    load(0, first);
-    handover(nst == 1, first);
-    read_q(first, 0);
-    read_p(first, 0, 0);
-    if (nst > 1) {
-      load(1, first ^ 1);
-      if (first) stage(More{}, 0, 1);
-      int s = first;
-      for (; s < nst - 2; s += 2) {
-        stage(More{}, s, 0);
-        stage(More{}, s + 1, 1);
+      if constexpr (some) {
+        multiply(0, 0);
+        read_q(qb, 1);
+        read_p(pb, 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      stage(One{}, s, 0);
+      if constexpr (both) {
+        multiply(0, 1);
+        read_p(pb, 1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (some) multiply(1, 0);
+    };
+    if constexpr (some) {
+      read_q(0, 0);
+      read_p(0, 0, 0);
     }
-    stage(Last{}, nst - 1, 1);
+    for (int s = 0; s < nst - 1; ++s) {
+      three();
+      const uint32_t old_p = pb, old_q = qb;
+      pb ^= OpP::kBytes;
+      qb = next_q(qb);
+      handover(s + 2 == nst, pb, qb);
+      if constexpr (some) {
+        read_q(qb, 0);
+        read_p(pb, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      constexpr int pieces = OpP::kPieces + OpQ::kPieces, n = both ? NH * NQ : 1;
+      uint8_t* lds_q = s_q + (kFar ? old_q : next_q(qb));
+      const typename OpP::Stage sp = op.stage(s + 2, sum);
+      const typename OpQ::Stage sq = oq.stage(s + (kFar ? 3 : 2), sum);
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        if constexpr (both) multiply_one(1, 1, i / NQ, i % NQ);
+#pragma unroll
+        for (int k = i * pieces / n; k < (i + 1) * pieces / n; ++k) {
+          if (k < OpP::kPieces) op.piece(sp, k, s_p + old_p);
+          else oq.piece(sq, k - OpP::kPieces, lds_q);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    three();
+    if constexpr (both) multiply(1, 1);
+  };
+  if (FORM != TN || nst > 0) {
+    // (the newest loads are the Q side's farthest stage)
+    if constexpr (!kFar) op.load(0, sum, s_p);
+    oq.load(0, sum, s_q);
+    if constexpr (kFar) {
+      op.load(0, sum, s_p);
+      oq.load(1, sum, s_q + OpQ::kBytes);
+    }
+    handover(nst == 1, 0, 0);
+    op.load(1, sum, s_p + OpP::kBytes);
+    if constexpr (kFar) oq.load(2, sum, s_q + 2 * OpQ::kBytes);
+    else oq.load(1, sum, s_q + OpQ::kBytes);
+    if (FORM == TN || pn > wp + 16 * NH) stages(std::integral_constant<int, 2>{});
+    else if (pn > wp) stages(std::integral_constant<int, 1>{});
+    else stages(std::integral_constant<int, 0>{});
+    // (no load into LDS is left behind when the wave ends)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);
   }
 
   if (GRAN == 16 || GRAN == 32) {
@@ -450,20 +515,226 @@ __global__ __launch_bounds__(WP * WQ * 64, 2) void grouped_tile_kernel(GroupedAr
   }
 }
 
-template <int FORM, int GRAN, int P, int Q, int WP, int WQ>
+// ---------------------------------------------------------------------------
+// few rows per expert: the stream of the weights
+
+// A wave's chunk of 16 weight rows: whole 128-byte lines (load j: rows 8 j + lane
+// / 8, bytes 16 (lane & 7)) of 64 bfloat16 or 256 FP4 elements, and the scales of
+// row lane % 16.
+template <int GRAN>
+struct FewChunk {
+  u32x4 c[2];
+  u32x4 s;  // GRAN 16: 16 scales; 32: 8
+};
+
+// Sixteen (GRAN 32: eight) scales of a row from element k on; byte by byte where
+// the row may end before.
+template <int GRAN, bool WHOLE>
+__device__ __forceinline__ u32x4 few_scales(const uint8_t* base, uint32_t row, int k, int K) {
+  constexpr int n = 256 / GRAN;
+  u32x4 v = {0, 0, 0, 0};
+  if (WHOLE || k + 256 <= K) {
+    __builtin_memcpy(&v, base + (row + k / GRAN), n);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i >> 2] |= (uint32_t)base[row + min(k / GRAN + i, K / GRAN - 1)] << (8 * (i & 3));
+  }
+  return v;
+}
+
+// 16 NR weight rows x 16 NG rows of x per workgroup, the sum split over its 8
+// waves, chunk by chunk in turn; NC chunks of weights in flight per wave.  WHOLE:
+// the sum is whole chunks.
+template <int GRAN, bool WHOLE, int NR, int NG, int NC>
+__global__ __launch_bounds__(512, WHOLE && NG <= (GRAN ? 1 : 2) ? 4 : 2) void grouped_few_kernel(GroupedArgs a) {
+  constexpr int CK = GRAN ? 256 : 64;  // elements per chunk
+  constexpr int NJ = CK / 32;          // products of 32 elements
+  constexpr int ROWS = 16 * NR, XR = 16 * NG;
+  __shared__ v4f s_red[8][NR][NG][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, q = lane >> 4, K = a.K, N = a.N;
+  const int nq = (N + ROWS - 1) / ROWS;
+  Rows r = rows_of(a.offsets, a.E, a.M, XR, nq, blockIdx.x);
+  if (r.e < 0) return;
+  const int e = __builtin_amdgcn_readfirstlane(r.e), i0 = __builtin_amdgcn_readfirstlane(r.i);
+  const int m0 = i0 / nq * XR, n0 = i0 % nq * ROWS;
+  const int rows = __builtin_amdgcn_readfirstlane(r.n) - m0;  // of x, from here on
+  const size_t first = (size_t)__builtin_amdgcn_readfirstlane(r.r0) + m0;
+
+  // weights: lane's row of each load, and its 16 bytes of a line
+  const uint32_t ldw = GRAN ? K / 2 : 2 * K, line = 16 * (lane & 7), last = ldw - 16;
+  const size_t wrow = (size_t)e * N + n0;
+  const uint8_t* wbase = (GRAN ? a.w : reinterpret_cast<const uint8_t*>(a.q)) + wrow * ldw;
+  const uint8_t* sbase = GRAN ? a.w_sf + wrow * (K / (GRAN ? GRAN : 1)) : nullptr;
+  const int left = N - n0 - 1;
+  const int nch = (K + CK - 1) / CK;
+  typedef FewChunk<GRAN> Chunk;
+  auto load = [&](int c, Chunk (&w)[NR]) __attribute__((always_inline)) {
+    c = min(c, nch - 1);  // (behind the last: the last again, not used)
+#pragma unroll
+    for (int t = 0; t < NR; ++t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t row = min(16 * t + 8 * j + (lane >> 3), left);
+        w[t].c[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wbase + row * ldw + (WHOLE ? c * 128 + line : min(c * 128 + line, last))));
+      }
+      if constexpr (GRAN != 0)
+        w[t].s = few_scales<GRAN, WHOLE>(sbase, __umul24(min(16 * t + r16, left), K / GRAN), c * CK, K);
+    }
+  };
+  Chunk w[NC][NR];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) load(wave + 8 * i, w[i]);
+
+  // x: row r16 of each 16, elements 32 j + 8 q .. + 7 of a chunk (rows behind the
+  // last repeat it: their results are not stored)
+  const uint16_t* xbase = a.p + first * K;
+  uint32_t xr[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) xr[g] = (uint32_t)min(16 * g + r16, rows - 1) * K + 8 * q;
+  u32x4 x[NG][NJ];
+  auto load_x = [&](int g, int c, int j) __attribute__((always_inline)) {
+    const int k = min(c, nch - 1) * CK + 32 * j;
+    x[g][j] = *reinterpret_cast<const u32x4*>(xbase + (xr[g] + (WHOLE ? k : min(k, K - 8 - 8 * q))));
+  };
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_x(g, wave, j);
+
+  v4f acc[NR][NG];
+#pragma unroll
+  for (int t = 0; t < NR; ++t)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[t][g] = v4f{0.f, 0.f, 0.f, 0.f};
+  // the lines turned into operand order through the wave's own LDS: 16 rows of
+  // 128 bytes, 16-byte piece p of row r at p ^ pswz(r)
+  uint8_t* turn = reinterpret_cast<uint8_t*>(&s_red[wave][0][0][0]);
+  const int wr = lane >> 3;
+  const uint32_t tw0 = wr * 128 + 16 * ((lane & 7) ^ pswz(wr)), tw1 = (wr + 8) * 128 + 16 * ((lane & 7) ^ pswz(wr + 8));
+  for (int c0 = 0; c0 < nch; c0 += 8 * NC) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = c0 + wave + 8 * i;
+      typedef typename std::conditional<GRAN == 0, u32x4, uint32_t>::type Raw;
+      Raw raw[NR][NJ];
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        *reinterpret_cast<u32x4*>(turn + tw0) = w[i][t].c[0];
+        *reinterpret_cast<u32x4*>(turn + tw1) = w[i][t].c[1];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint8_t* p = turn + r16 * 128 + (GRAN == 0 ? 16 * ((4 * j + q) ^ pswz(r16)) : 16 * (j ^ pswz(r16)) + 4 * q);
+          raw[t][j] = *reinterpret_cast<const Raw*>(p);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+      u32x4 s[NR];
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        s[t] = w[i][t].s;
+        if (GRAN == 16) {  // (the lane's elements lie in every other group)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[t][j] >>= 8 * (q >> 1);
+        }
+      }
+      if (WHOLE && c >= nch) break;  // (the wave's last)
+      // (the next chunk into these registers is asked for before this one multiplies)
+      if (c0 + 8 * NC < nch) load(c + 8 * NC, w[i]);
+      auto operand = [&](int t, int j) __attribute__((always_inline)) {
+        u32x4 v;
+        if constexpr (GRAN == 0) v = raw[t][j];
+        else if constexpr (GRAN == 16) v = dq8_scaled_bf16(raw[t][j], __builtin_amdgcn_cvt_f32_fp8((int)(s[t][j >> 1] >> (16 * (j & 1))), 0));
+        else v = __builtin_bit_cast(u32x4, dq8_bf16(raw[t][j], ue8m0_to_f32((s[t][j >> 2] >> (8 * (j & 3))) & 0xFFu)));
+        return !WHOLE && c * CK + 32 * j + 8 * q >= K ? u32x4{0, 0, 0, 0} : v;
+      };
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        u32x4 A[NR];
+#pragma unroll
+        for (int t = 0; t < NR; ++t) A[t] = operand(t, j);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          // (zeros on both sides behind the sum's last element)
+          const u32x4 b = !WHOLE && c * CK + 32 * j + 8 * q >= K ? u32x4{0, 0, 0, 0} : x[g][j];
+#pragma unroll
+          for (int t = 0; t < NR; ++t)
+            acc[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, A[t]), __builtin_bit_cast(v8bf, b),
+                                                                acc[t][g], 0, 0, 0);
+          load_x(g, c + 8, j);  // (into the registers just used)
+        }
+        if (GRAN) __builtin_amdgcn_sched_barrier(0);  // (one decoding after the other: registers are short)
+      }
+    }
+  }
+  const float gs = GRAN && a.w_gs ? a.w_gs[e] : 1.0f;
+  __syncthreads();  // (every wave is done with its turning place)
+#pragma unroll
+  for (int t = 0; t < NR; ++t)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s_red[wave][t][g][lane] = acc[t][g];
+  __syncthreads();
+  // thread: output column n0 + rn of rows rt, rt + 512 / ROWS, ..
+  const int rn = tid & (ROWS - 1);
+  if (n0 + rn >= N) return;
+  for (int t = tid / ROWS; t < min(rows, XR); t += 512 / ROWS) {
+    float v = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      v += reinterpret_cast<const float*>(&s_red[p][rn >> 4][t >> 4][(t & 15) + 16 * ((rn & 15) >> 2)])[rn & 3];
+    if (GRAN) v *= gs;
+    const size_t at = (first + t) * N + n0 + rn;
+    if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+    else static_cast<uint16_t*>(a.out)[at] = (uint16_t)bf16_bits(v);
+  }
+}
+
+template <int GRAN, int NR, int NG, int NC>
+hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
+  const long long nq = (a.N + 16 * NR - 1) / (16 * NR), most = a.E < a.M ? a.E : a.M;
+  const dim3 grid((unsigned)((a.M / (16 * NG) + most) * nq)), block(512);
+  if (a.K % (GRAN ? 256 : 64) == 0) hipLaunchKernelGGL((grouped_few_kernel<GRAN, true, NR, NG, NC>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((grouped_few_kernel<GRAN, false, NR, NG, NC>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
 hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
   const long long nq = ((FORM == NT ? a.N : a.K) + Q - 1) / Q;
   const long long most = a.E < a.M ? a.E : a.M;  // experts with rows
   const long long tiles = FORM == TN ? (long long)a.E * ((a.N + P - 1) / P) * nq : (a.M / P + most) * nq;
   // whole rounds of 8 XCDs of 32 tiles (tile_of)
   const long long grid = (tiles + 255) / 256 * 256;
-  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ>), dim3((unsigned)grid), dim3(WP * WQ * 64), 0, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB>), dim3((unsigned)grid), dim3(WP * WQ * 64), 0, s, a);
   return hipGetLastError();
+}
+
+// Row tiles of `size` rows over `most` experts with rows: about half of each
+// expert's last one is empty.
+long long row_tiles(long long M, long long most, int size) {
+  const long long n = (M + size / 2 * most) / size;
+  return n > most ? n : most;
 }
 
 template <int FORM, int GRAN>
 hipError_t launch_form(const GroupedArgs& a, hipStream_t s) {
-  return launch_tile<FORM, GRAN, 256, 256, 2, 4>(a, s);
+  const long long M = a.M, most = a.E < M ? a.E : M, outs = FORM == NT ? a.N : a.K;
+  auto tiles = [&](int P, int Q) { return (FORM == TN ? (long long)a.E * ((a.N + P - 1) / P) : row_tiles(M, most, P)) * ((outs + Q - 1) / Q); };
+  if constexpr (FORM == TN) {
+    // 256 x 256 where it fills the chip
+    if (a.N > 128 && a.K > 128 && tiles(256, 256) >= 256) return launch_tile<FORM, 0, 256, 256, 2, 4, 3>(a, s);
+    return launch_tile<FORM, 0, 128, 128, 2, 2, 2>(a, s);
+  } else {
+    if constexpr (FORM == NT) {
+      if (M <= (GRAN ? 16 : 6) * most) return launch_few<GRAN, 2, 1, GRAN ? 1 : 3>(a, s);
+      if (M <= 12 * most || (M <= 100 * most && tiles(64, 128) < 256)) return launch_few<GRAN, 2, 2, GRAN ? 1 : 3>(a, s);
+    }
+    if (tiles(256, 256) >= 256 && outs > 128 && (GRAN == 0 || M >= 192 * most)) return launch_tile<FORM, GRAN, 256, 256, 2, 4, GRAN ? 2 : 3>(a, s);
+    if (tiles(128, 128) >= 256 && (GRAN == 0 || M >= 96 * most)) return launch_tile<FORM, GRAN, 128, 128, 2, 2, GRAN ? 2 : 3>(a, s);
+    return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
+  }
 }
 
 }  // namespace
