@@ -269,12 +269,16 @@ struct Fp4Operand : Operand<TR, SIZE, NTH> {
       return;
     }
     const int row = threadIdx.x / kPer, piece = threadIdx.x % kPer;
-    uint32_t at = TR ? row * (SIZE * 2) + ((2 * piece ^ tswz(row)) << 5) : row * 128 + ((4 * piece ^ pswz(row)) << 4);
+    // (TR: pieces 256 bytes apart write the two halves of a chunk in turn, so that
+    // 16 lanes write to all 64 banks)
+    const bool swap = TR && (piece & 4);
+    uint32_t at = TR ? row * (SIZE * 2) + ((2 * piece ^ tswz(row)) << 5) + (swap ? 16 : 0) : row * 128 + ((4 * piece ^ pswz(row)) << 4);
     asm volatile("" : "+v"(at));
     u32x4 v;
-    if (GRAN == 16) v = dq8_scaled_bf16(c[j], e4m3_to_f32((s >> (8 * (j >> 1))) & 0xFFu));
-    else v = __builtin_bit_cast(u32x4, dq8_bf16(c[j], ue8m0_to_f32(s)));
-    *reinterpret_cast<u32x4*>(lds + (TR ? (at ^ ((j >> 1) << 5)) + 16 * (j & 1) : at ^ (j << 4))) = v;
+    const uint32_t codes = swap ? c[j ^ 1] : c[j];
+    if (GRAN == 16) v = dq8_scaled_bf16(codes, e4m3_to_f32((s >> (8 * (j >> 1))) & 0xFFu));
+    else v = __builtin_bit_cast(u32x4, dq8_bf16(codes, ue8m0_to_f32(s)));
+    *reinterpret_cast<u32x4*>(lds + (TR ? at ^ ((j >> 1) << 5) ^ ((j & 1) << 4) : at ^ (j << 4))) = v;
   }
   __device__ __forceinline__ void load(int st, int n, uint8_t* lds) {
 #pragma unroll
@@ -286,6 +290,19 @@ template <bool TR, int SIZE, int NTH, int GRAN>
 struct WeightOperand { typedef Fp4Operand<TR, SIZE, NTH, GRAN> type; };
 template <bool TR, int SIZE, int NTH>
 struct WeightOperand<TR, SIZE, NTH, 0> { typedef Operand<TR, SIZE, NTH> type; };
+
+// A store, past the caches if asked for.  (The empty asm keeps the compiler from
+// making one ordinary store of the two.)
+template <class V>
+__device__ __forceinline__ void store(const V& v, V* to, bool past) {
+  if (past) {
+    asm volatile("" ::: "memory");
+    __builtin_nontemporal_store(v, to);
+    asm volatile("" ::: "memory");
+  } else {
+    *to = v;
+  }
+}
 
 // Every wave's LDS accesses done, and its loads but the LEFT newest (LEFT < 16),
 // and a barrier.
@@ -476,9 +493,6 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
     if (FORM == TN || pn > wp + 16 * NH) stages(std::integral_constant<int, 2>{});
     else if (pn > wp) stages(std::integral_constant<int, 1>{});
     else stages(std::integral_constant<int, 0>{});
-    // (no load into LDS is left behind when the wave ends)
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70);
   }
 
   if (GRAN == 16 || GRAN == 32) {
@@ -488,30 +502,49 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
 #pragma unroll
       for (int j = 0; j < NP; ++j) acc[i][j] *= gs;
   }
+  // Out through LDS, 16 rows of a wave's 64 columns at a time, so that whole lines
+  // are written (E = 16, N = 4096, K = 6144, float32: 8192 rows' dW 731 -> 704 us);
+  // past the caches where the output is larger than the last one (687 us; 64
+  // experts of 2048 x 2048, 16384 rows 367 -> 286 us).
+  static_assert(Q / WQ == 64 && WP * WQ * 4096 <= 2 * OpP::kBytes, "4 KB per wave");
+  wait_all<0>();  // (every wave is done with the stages)
+  v4f* turn = reinterpret_cast<v4f*>(s_p) + wave * 256;  // [16][16], piece c of row r at c ^ r
   const size_t row0 = FORM == TN ? (size_t)r.e * a.N + p0 : (size_t)(r.r0 + p0);
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const int p = wp + 16 * j + r16;
-    if (p >= pn) continue;
+    const int p16 = wp + 16 * j;
+    if (p16 >= pn) break;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = wq + 16 * i + 4 * q4;
-      if (q >= qn) continue;  // (a multiple of 8 exist)
-      const size_t at = (row0 + p) * outs + q0 + q;
-      v4f v = acc[i][j];
-      if (a.out_f32) {
-        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(a.out) + at);
+    for (int i = 0; i < NQ; ++i) turn[r16 * 16 + ((4 * i + q4) ^ r16)] = acc[i][j];
+    __builtin_amdgcn_wave_barrier();
+    if (a.out_f32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = 4 * k + q4, q = wq + 4 * r16;
+        v4f v = turn[row * 16 + (r16 ^ row)];
+        if (p16 + row >= pn || q >= qn) continue;
+        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(a.out) + (row0 + p16 + row) * outs + q0 + q);
         if (FORM == TN && a.accumulate) v += *o;
-        *o = v;
-      } else {
-        uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at);
+        store(v, o, a.stream);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = 8 * k + (lane >> 3), c = 2 * (lane & 7), q = wq + 4 * c;
+        v4f v = turn[row * 16 + (c ^ row)], w = turn[row * 16 + ((c + 1) ^ row)];
+        if (p16 + row >= pn || q >= qn) continue;  // (a multiple of 8 columns exist)
+        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + (row0 + p16 + row) * outs + q0 + q);
         if (FORM == TN && a.accumulate) {
-          const uint2 b = *o;
-          v += v4f{u2f(b.x << 16), u2f(b.x & 0xFFFF0000u), u2f(b.y << 16), u2f(b.y & 0xFFFF0000u)};
+          const u32x4 b = *o;
+          v += v4f{u2f(b[0] << 16), u2f(b[0] & 0xFFFF0000u), u2f(b[1] << 16), u2f(b[1] & 0xFFFF0000u)};
+          w += v4f{u2f(b[2] << 16), u2f(b[2] & 0xFFFF0000u), u2f(b[3] << 16), u2f(b[3] & 0xFFFF0000u)};
         }
-        *o = uint2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+        const u32x4 x = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16),
+                         bf16_bits(w[0]) | (bf16_bits(w[1]) << 16), bf16_bits(w[2]) | (bf16_bits(w[3]) << 16)};
+        store(x, o, a.stream);
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -739,7 +772,10 @@ hipError_t launch_form(const GroupedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_grouped(const GroupedArgs& a, int form, hipStream_t s) {
+hipError_t launch_grouped(const GroupedArgs& args, int form, hipStream_t s) {
+  GroupedArgs a = args;
+  const long long outs = form == TN ? (long long)a.E * a.N * a.K : (long long)a.M * (form == NT ? a.N : a.K);
+  a.stream = outs * (a.out_f32 ? 4 : 2) > (256LL << 20);
   if (form == TN) return launch_form<TN, 0>(a, s);
   if (a.gran == 16) return form == NT ? launch_form<NT, 16>(a, s) : launch_form<NN, 16>(a, s);
   if (a.gran == 32) return form == NT ? launch_form<NT, 32>(a, s) : launch_form<NN, 32>(a, s);

@@ -212,6 +212,7 @@ struct GroupedArgs {
   int M, E, N, K;
   int gran;           // 0: bfloat16 weights; 16, 32: FP4 (w, w_sf, w_gs in place of q)
   int out_f32, accumulate;
+  int stream;         // the output is larger than the caches (set by launch_grouped)
   const uint16_t *p, *q;
   const uint8_t *w, *w_sf;
   const float* w_gs;
