@@ -123,11 +123,13 @@ def lib():
         L.moe_fp4_project.argtypes = [lp] + [_P] * 10 + [ctypes.c_size_t, _P]
         L.moe_fp4_project.restype = st
         rp = ctypes.POINTER(Grouped)
-        L.moe_fp4_grouped.argtypes = [rp] + [_P] * 7
+        L.moe_fp4_grouped_workspace_bytes.argtypes = [rp, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_fp4_grouped_workspace_bytes.restype = st
+        L.moe_fp4_grouped.argtypes = [rp] + [_P] * 7 + [ctypes.c_size_t, _P]
         L.moe_fp4_grouped.restype = st
-        L.moe_fp4_grouped_dx.argtypes = [rp] + [_P] * 7
+        L.moe_fp4_grouped_dx.argtypes = L.moe_fp4_grouped.argtypes
         L.moe_fp4_grouped_dx.restype = st
-        L.moe_fp4_grouped_dw.argtypes = [rp] + [_P] * 4 + [ctypes.c_int32, _P]
+        L.moe_fp4_grouped_dw.argtypes = [rp] + [_P] * 4 + [ctypes.c_int32, _P, ctypes.c_size_t, _P]
         L.moe_fp4_grouped_dw.restype = st
         np_ = ctypes.POINTER(Norm)
         L.moe_fp4_block_norm.argtypes = [np_] + [_P] * 8
@@ -282,6 +284,11 @@ def _gate_need(top_k, shared, scoring, w_fmt, T, E, H):
 def _layer_need(device, top_k, shared, scoring, w_fmt, *problem):
     g = make_gate(top_k, scoring, False, 1.0, shared, w_fmt)
     return _need(lib().moe_fp4_layer_workspace_bytes, ctypes.byref(Problem(*problem)), ctypes.byref(g))
+
+
+@functools.lru_cache(maxsize=1024)
+def _grouped_need(direction, *problem):
+    return _need(lib().moe_fp4_grouped_workspace_bytes, ctypes.byref(Grouped(*problem)), direction)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -581,8 +588,18 @@ def _out_dtype(out, out_dtype):
     return out_dtype, OUT_F32 if out_dtype is torch.float32 else OUT_BF16
 
 
-def _grouped_product(fn, name, along_k, x, w, offsets, w_sf, w_gs, gran_k, out, stream, out_dtype):
+def _grouped_scratch(direction, problem, workspace, like, stream):
+    """(the workspace, held until the call is enqueued; its address; its size), None and 0 where none is needed."""
+    need = _grouped_need(direction, *problem)
+    if need == 0 and workspace is None:
+        return None, None, 0
+    ws = _scratch(workspace, need, like, stream)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _grouped_product(fn, direction, name, x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream, out_dtype):
     import torch
+    along_k = direction == 0
     u8, bf = (torch.uint8,), (torch.bfloat16,)
     M, cols = _dims(x, name, bf, 2)
     dev = _current(x, stream)
@@ -604,30 +621,34 @@ def _grouped_product(fn, name, along_k, x, w, offsets, w_sf, w_gs, gran_k, out, 
     off = _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
     if out is None:
         out = _empty(x, (M, outs), out_dtype, stream)
-    _check(fn(ctypes.byref(Grouped(M, N, K, E, gran_k or 0, fmt)), x.data_ptr(), w.data_ptr(), sf, gs, off,
-              _arg(out, "out", (out_dtype,), (M, outs), dev), _raw_stream(stream, dev)))
+    problem = (M, N, K, E, gran_k or 0, fmt)
+    ws, *room = _grouped_scratch(direction, problem, workspace, x, stream)
+    _check(fn(ctypes.byref(Grouped(*problem)), x.data_ptr(), w.data_ptr(), sf, gs, off,
+              _arg(out, "out", (out_dtype,), (M, outs), dev), *room, _raw_stream(stream, dev)))
     return out
 
 
-def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, stream=None, out_dtype=None):
+def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, workspace=None, stream=None, out_dtype=None):
     """Products grouped by expert: out[r] = W_e x[r] for the rows r in
     [offsets[e], offsets[e + 1]).  x [M, K] bfloat16; offsets [E + 1] int32,
     ascending (as route() gives them); w [E, N, K] bfloat16, or [E, N, K/2] uint8
     FP4 codes with w_sf [E, N, K/gran_k] uint8 (and w_gs [E] float32) and gran_k 16
     or 32.  Returns out [M, N] bfloat16 (default) or float32; rows outside
     [offsets[0], offsets[E]) are left as they are."""
-    return _grouped_product(lib().moe_fp4_grouped, "x", True, x, w, offsets, w_sf, w_gs, gran_k, out, stream, out_dtype)
-
-
-def grouped_dx(dy, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, stream=None, out_dtype=None):
-    """The gradient of grouped() towards its rows: out[r] = W_e^T dy[r], dy [M, N]
-    bfloat16, the weights and offsets as grouped() takes them.  Returns out
-    [M, K]."""
-    return _grouped_product(lib().moe_fp4_grouped_dx, "dy", False, dy, w, offsets, w_sf, w_gs, gran_k, out, stream,
+    return _grouped_product(lib().moe_fp4_grouped, 0, "x", x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)
 
 
-def grouped_dw(dy, x, offsets, out=None, accumulate=False, stream=None, out_dtype=None):
+def grouped_dx(dy, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, workspace=None, stream=None,
+               out_dtype=None):
+    """The gradient of grouped() towards its rows: out[r] = W_e^T dy[r], dy [M, N]
+    bfloat16, the weights and offsets as grouped() takes them.  Returns out
+    [M, K]."""
+    return _grouped_product(lib().moe_fp4_grouped_dx, 1, "dy", dy, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
+                            out_dtype)
+
+
+def grouped_dw(dy, x, offsets, out=None, accumulate=False, workspace=None, stream=None, out_dtype=None):
     """The gradient of grouped() towards its weights: out[e] = the sum over
     expert e's rows of dy[r] x[r]^T, zeros for an expert without rows.  dy [M, N]
     and x [M, K] bfloat16, offsets [E + 1] int32.  accumulate adds the sums to
@@ -643,9 +664,10 @@ def grouped_dw(dy, x, offsets, out=None, accumulate=False, stream=None, out_dtyp
     at = dy.data_ptr(), _arg(x, "x", bf, (M, K), dev), _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
     if out is None:
         out = _empty(dy, (max(E, 0), N, K), out_dtype, stream)
-    _check(lib().moe_fp4_grouped_dw(ctypes.byref(Grouped(M, N, K, E, 0, fmt)), *at,
-                                    _arg(out, "out", (out_dtype,), (E, N, K), dev), 1 if accumulate else 0,
-                                    _raw_stream(stream, dev)))
+    problem = (M, N, K, E, 0, fmt)
+    ws, *room = _grouped_scratch(2, problem, workspace, dy, stream)
+    _check(_lib.moe_fp4_grouped_dw(ctypes.byref(Grouped(*problem)), *at, _arg(out, "out", (out_dtype,), (E, N, K), dev),
+                                   1 if accumulate else 0, *room, _raw_stream(stream, dev)))
     return out
 
 

@@ -835,9 +835,39 @@ static bool overlaps(const void* out, size_t bytes, const Span* in, int n) {
   return false;
 }
 
+static size_t grouped_floats(const moefp4_grouped* p, int form) {
+  return (size_t)moefp4::grouped_part_floats(form, p->M, p->E, p->N, p->K);
+}
+
+moefp4_status moe_fp4_grouped_workspace_bytes(const moefp4_grouped* p, int32_t direction, size_t* bytes) {
+  if (direction < MOEFP4_GROUPED || direction > MOEFP4_GROUPED_DW) return fail(MOEFP4_EINVAL, "unknown direction %d", direction);
+  const moefp4_status st = grouped_check(p, direction != MOEFP4_GROUPED_DW);
+  if (st != MOEFP4_OK) return st;
+  if (!bytes) return fail(MOEFP4_EINVAL, "bytes is NULL");
+  *bytes = align_up(4 * grouped_floats(p, direction));
+  return ok();
+}
+
+// out and the workspace (what this call itself takes of it) against each other and the inputs.
+static moefp4_status grouped_room(const moefp4_grouped* p, int form, const Span* in, int n, void* out, size_t outputs, void* workspace,
+                                  size_t ws_bytes, moefp4::GroupedArgs* a) {
+  const moefp4::GroupedPlan plan = moefp4::grouped_plan(form, p->M, p->E, p->N, p->K, p->gran_k);
+  const size_t need = plan.parts > 1 ? 4 * outputs * plan.parts : 0;
+  const Span to = {out, outputs * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2)};
+  if (need && (!workspace || ws_bytes < need))
+    return fail(MOEFP4_EWORKSPACE, "workspace of %zu bytes needed, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  if (need && misaligned(workspace, 256)) return fail(MOEFP4_EINVAL, "workspace must be 256-byte aligned");
+  if (overlaps(out, to.n, in, n)) return fail(MOEFP4_EINVAL, "out overlaps an input");
+  if (need && (overlaps(workspace, need, in, n) || overlaps(workspace, need, &to, 1)))
+    return fail(MOEFP4_EINVAL, "the workspace overlaps an input or out");
+  a->part = need ? static_cast<float*>(workspace) : nullptr;
+  return MOEFP4_OK;
+}
+
 // form 0: the product, 1: towards the rows
 static moefp4_status grouped_product(const moefp4_grouped* p, int form, const void* x, const void* w, const uint8_t* w_sf,
-                                     const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
+                                     const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
+                                     hipStream_t stream) {
   moefp4_status st = grouped_check(p, true);
   if (st != MOEFP4_OK) return st;
   if (p->M == 0) return ok();
@@ -849,10 +879,10 @@ static moefp4_status grouped_product(const moefp4_grouped* p, int form, const vo
   const size_t M = p->M, N = p->N, K = p->K, E = p->E, g = p->gran_k;
   const Span in[] = {{x, 2 * M * (form ? N : K)}, {w, g ? E * N * (K / 2) : 2 * E * N * K}, {w_sf, g ? E * N * (K / g) : 0},
                      {w_gs, 4 * E}, {offsets, 4 * (E + 1)}};
-  if (overlaps(out, M * (form ? K : N) * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2), in, 5))
-    return fail(MOEFP4_EINVAL, "out overlaps an input");
   moefp4::GroupedArgs a;
   memset(&a, 0, sizeof a);
+  st = grouped_room(p, form, in, 5, out, M * (form ? K : N), workspace, ws_bytes, &a);
+  if (st != MOEFP4_OK) return st;
   a.M = (int)M;
   a.E = (int)E;
   a.N = (int)N;
@@ -871,17 +901,19 @@ static moefp4_status grouped_product(const moefp4_grouped* p, int form, const vo
 }
 
 moefp4_status moe_fp4_grouped(const moefp4_grouped* p, const void* x, const void* w, const uint8_t* w_sf,
-                              const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
-  return grouped_product(p, 0, x, w, w_sf, w_gs, offsets, out, stream);
+                              const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
+                              hipStream_t stream) {
+  return grouped_product(p, 0, x, w, w_sf, w_gs, offsets, out, workspace, ws_bytes, stream);
 }
 
 moefp4_status moe_fp4_grouped_dx(const moefp4_grouped* p, const void* dy, const void* w, const uint8_t* w_sf,
-                                 const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream) {
-  return grouped_product(p, 1, dy, w, w_sf, w_gs, offsets, out, stream);
+                                 const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream) {
+  return grouped_product(p, 1, dy, w, w_sf, w_gs, offsets, out, workspace, ws_bytes, stream);
 }
 
 moefp4_status moe_fp4_grouped_dw(const moefp4_grouped* p, const void* dy, const void* x, const int32_t* offsets,
-                                 void* out, int32_t accumulate, hipStream_t stream) {
+                                 void* out, int32_t accumulate, void* workspace, size_t ws_bytes, hipStream_t stream) {
   moefp4_status st = grouped_check(p, false);
   if (st != MOEFP4_OK) return st;
   if (!offsets || !out || (p->M > 0 && (!dy || !x))) return fail(MOEFP4_EINVAL, "dy, x, offsets and out must be non-NULL");
@@ -889,10 +921,10 @@ moefp4_status moe_fp4_grouped_dw(const moefp4_grouped* p, const void* dy, const 
     return fail(MOEFP4_EINVAL, "dy, x and out must be 16-byte aligned, offsets 4-byte");
   const size_t M = p->M, N = p->N, K = p->K, E = p->E;
   const Span in[] = {{dy, 2 * M * N}, {x, 2 * M * K}, {offsets, 4 * (E + 1)}};
-  if (overlaps(out, E * N * K * (p->out_fmt == MOEFP4_OUT_F32 ? 4 : 2), in, 3))
-    return fail(MOEFP4_EINVAL, "out overlaps an input");
   moefp4::GroupedArgs a;
   memset(&a, 0, sizeof a);
+  st = grouped_room(p, 2, in, 3, out, E * N * K, workspace, ws_bytes, &a);
+  if (st != MOEFP4_OK) return st;
   a.M = (int)M;
   a.E = (int)E;
   a.N = (int)N;

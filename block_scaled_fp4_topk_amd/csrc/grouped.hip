@@ -43,11 +43,11 @@ __device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
 // ---------------------------------------------------------------------------
 // tiles
 
-// The place of workgroup b among the tiles: groups of 32 consecutive tiles per
-// XCD in turn (an XCD's 32 CUs share an L2).
-__device__ __forceinline__ int tile_of(int b) {
-  const int i = b >> 3;
-  return (((i >> 5) * 8 + (b & 7)) << 5) + (i & 31);
+// The place of workgroup b among the tiles: groups of up to 32 consecutive tiles
+// per XCD in turn (an XCD's 32 CUs share an L2).
+__device__ __forceinline__ int tile_of(int b, int group) {
+  const int i = b >> 3, g = i / group;
+  return (g * 8 + (b & 7)) * group + i - g * group;
 }
 
 // Tile i of the np x nq tiles of one expert, four of np at a time, so that
@@ -318,7 +318,8 @@ __device__ __forceinline__ void wait_all() {
 // the tiled product
 
 // P x Q outputs per workgroup: P along the rows (TN: along N), Q along the
-// output's contiguous side; WP x WQ waves.  GRAN: 0, or FP4 weights' group.  NB:
+// output's contiguous side; WP x WQ waves.  blockIdx.y: the part of the sum (more
+// than one: to a.part as float32, which grouped_sum adds up).  GRAN: 0, or FP4 weights' group.  NB:
 // stages of the Q side in LDS (of the P side 2): where the weights come from HBM,
 // two stages of them in flight.
 template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   const int r16 = lane & 15, q4 = lane >> 4;
   const int outs = FORM == NT ? a.N : a.K;  // the output's contiguous side
   const int nq = (outs + Q - 1) / Q;
-  const int tile = tile_of(blockIdx.x);
+  const int tile = tile_of(blockIdx.x, a.group);
   Rows r;
   if constexpr (FORM == TN) {
     const int np = (a.N + P - 1) / P, e = tile / (np * nq);
@@ -352,8 +353,11 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   tile_at(__builtin_amdgcn_readfirstlane(r.i), __builtin_amdgcn_readfirstlane(r.np), nq, &tp, &tq);
   const int p0 = tp * P, q0 = tq * Q;
   const int pn = (FORM == TN ? a.N : r.n) - p0, qn = outs - q0;  // what exists of the tile
-  const int sum = FORM == NT ? a.K : FORM == NN ? a.N : r.n;
-  const int nst = (sum + kS - 1) / kS, tail = sum & (kS - 1);
+  // the stages [s0, s1) of the sum, which ends at element `sum` here
+  const int whole = FORM == NT ? a.K : FORM == NN ? a.N : r.n;
+  const int per = ((whole + kS - 1) / kS + a.parts - 1) / a.parts;
+  const int s0 = min((int)blockIdx.y * per, (whole + kS - 1) / kS), s1 = min(s0 + per, (whole + kS - 1) / kS);
+  const int sum = min(whole, s1 * kS), tail = sum & (kS - 1);
   const int wp = (wave / WQ) * (P / WP), wq = (wave % WQ) * (Q / WQ);
 
   OpP op;
@@ -362,13 +366,13 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
     op.init(a.p + (size_t)r.r0 * a.N + p0, 2 * a.N, pn);
     oq.init(a.q + (size_t)r.r0 * a.K + q0, 2 * a.K, qn);
   } else {
-    op.init(a.p + (size_t)(r.r0 + p0) * sum, 2 * sum, pn);
+    op.init(a.p + (size_t)(r.r0 + p0) * whole, 2 * whole, pn);
     // the weights' first row and column of the tile
     const size_t row = (size_t)r.e * a.N + (FORM == NT ? q0 : 0);
     const int col = FORM == NT ? 0 : q0;
     if constexpr (GRAN != 0) {
       oq.init(a.w + row * (a.K / 2) + col / 2, a.w_sf + row * (a.K / GRAN) + col / GRAN, a.K, qn);
-      oq.fetch(0, sum);
+      if (s1 > s0) oq.fetch(s0, sum);
     } else {
       oq.init(a.q + row * a.K + col, 2 * a.K, qn);
     }
@@ -449,12 +453,12 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       read_q(0, 0);
       read_p(0, 0, 0);
     }
-    for (int s = 0; s < nst - 1; ++s) {
+    for (int s = s0; s < s1 - 1; ++s) {
       three();
       const uint32_t old_p = pb, old_q = qb;
       pb ^= OpP::kBytes;
       qb = next_q(qb);
-      handover(s + 2 == nst, pb, qb);
+      handover(s + 2 == s1, pb, qb);
       if constexpr (some) {
         read_q(qb, 0);
         read_p(pb, 0, 0);
@@ -478,18 +482,18 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
     three();
     if constexpr (both) multiply(1, 1);
   };
-  if (FORM != TN || nst > 0) {
+  if (s1 > s0) {
     // (the newest loads are the Q side's farthest stage)
-    if constexpr (!kFar) op.load(0, sum, s_p);
-    oq.load(0, sum, s_q);
+    if constexpr (!kFar) op.load(s0, sum, s_p);
+    oq.load(s0, sum, s_q);
     if constexpr (kFar) {
-      op.load(0, sum, s_p);
-      oq.load(1, sum, s_q + OpQ::kBytes);
+      op.load(s0, sum, s_p);
+      oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
     }
-    handover(nst == 1, 0, 0);
-    op.load(1, sum, s_p + OpP::kBytes);
-    if constexpr (kFar) oq.load(2, sum, s_q + 2 * OpQ::kBytes);
-    else oq.load(1, sum, s_q + OpQ::kBytes);
+    handover(s1 - s0 == 1, 0, 0);
+    op.load(s0 + 1, sum, s_p + OpP::kBytes);
+    if constexpr (kFar) oq.load(s0 + 2, sum, s_q + 2 * OpQ::kBytes);
+    else oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
     if (FORM == TN || pn > wp + 16 * NH) stages(std::integral_constant<int, 2>{});
     else if (pn > wp) stages(std::integral_constant<int, 1>{});
     else stages(std::integral_constant<int, 0>{});
@@ -510,6 +514,8 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   wait_all<0>();  // (every wave is done with the stages)
   v4f* turn = reinterpret_cast<v4f*>(s_p) + wave * 256;  // [16][16], piece c of row r at c ^ r
   const size_t row0 = FORM == TN ? (size_t)r.e * a.N + p0 : (size_t)(r.r0 + p0);
+  const bool one = a.parts == 1, f32 = a.out_f32 || !one, add = FORM == TN && one && a.accumulate, past = one && a.stream;
+  void* out = one ? a.out : a.part + (size_t)blockIdx.y * (FORM == TN ? (size_t)a.E * a.N : (size_t)a.M) * outs;
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const int p16 = wp + 16 * j;
@@ -517,15 +523,15 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
 #pragma unroll
     for (int i = 0; i < NQ; ++i) turn[r16 * 16 + ((4 * i + q4) ^ r16)] = acc[i][j];
     __builtin_amdgcn_wave_barrier();
-    if (a.out_f32) {
+    if (f32) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int row = 4 * k + q4, q = wq + 4 * r16;
         v4f v = turn[row * 16 + (r16 ^ row)];
         if (p16 + row >= pn || q >= qn) continue;
-        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(a.out) + (row0 + p16 + row) * outs + q0 + q);
-        if (FORM == TN && a.accumulate) v += *o;
-        store(v, o, a.stream);
+        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(out) + (row0 + p16 + row) * outs + q0 + q);
+        if (add) v += *o;
+        store(v, o, past);
       }
     } else {
 #pragma unroll
@@ -533,18 +539,56 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
         const int row = 8 * k + (lane >> 3), c = 2 * (lane & 7), q = wq + 4 * c;
         v4f v = turn[row * 16 + (c ^ row)], w = turn[row * 16 + ((c + 1) ^ row)];
         if (p16 + row >= pn || q >= qn) continue;  // (a multiple of 8 columns exist)
-        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + (row0 + p16 + row) * outs + q0 + q);
-        if (FORM == TN && a.accumulate) {
+        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + (row0 + p16 + row) * outs + q0 + q);
+        if (add) {
           const u32x4 b = *o;
           v += v4f{u2f(b[0] << 16), u2f(b[0] & 0xFFFF0000u), u2f(b[1] << 16), u2f(b[1] & 0xFFFF0000u)};
           w += v4f{u2f(b[2] << 16), u2f(b[2] & 0xFFFF0000u), u2f(b[3] << 16), u2f(b[3] & 0xFFFF0000u)};
         }
         const u32x4 x = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16),
                          bf16_bits(w[0]) | (bf16_bits(w[1]) << 16), bf16_bits(w[2]) | (bf16_bits(w[3]) << 16)};
-        store(x, o, a.stream);
+        store(x, o, past);
       }
     }
     __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// The sum of the parts, in order: eight outputs per thread.  Rows of no expert
+// (TN: none) are left as they are.
+template <bool TN_>
+__global__ __launch_bounds__(256) void grouped_sum_kernel(GroupedArgs a, int outs) {
+  const long long rows = TN_ ? (long long)a.E * a.N : a.M, i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= rows * outs) return;
+  if (!TN_) {
+    const int r = (int)(i / outs);
+    if (r < min(max(a.offsets[0], 0), a.M) || r >= min(max(a.offsets[a.E], 0), a.M)) return;
+  }
+  if (TN_ && a.accumulate) {
+    const int e = (int)(i / outs / a.N);
+    if (a.offsets[e + 1] <= a.offsets[e]) return;  // (nothing to add)
+  }
+  v4f v = {0.f, 0.f, 0.f, 0.f}, w = v;
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    const v4f* q = reinterpret_cast<const v4f*>(a.part + p * rows * outs + i);
+    v += q[0];
+    w += q[1];
+  }
+  if (a.out_f32) {
+    v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(a.out) + i);
+    if (TN_ && a.accumulate) v += o[0], w += o[1];
+    o[0] = v;
+    o[1] = w;
+  } else {
+    u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + i);
+    if (TN_ && a.accumulate) {
+      const u32x4 b = *o;
+      v += v4f{u2f(b[0] << 16), u2f(b[0] & 0xFFFF0000u), u2f(b[1] << 16), u2f(b[1] & 0xFFFF0000u)};
+      w += v4f{u2f(b[2] << 16), u2f(b[2] & 0xFFFF0000u), u2f(b[3] << 16), u2f(b[3] & 0xFFFF0000u)};
+    }
+    *o = u32x4{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16),
+               bf16_bits(w[0]) | (bf16_bits(w[1]) << 16), bf16_bits(w[2]) | (bf16_bits(w[3]) << 16)};
   }
 }
 
@@ -734,52 +778,107 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
 }
 
 template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
-hipError_t launch_tile(const GroupedArgs& a, hipStream_t s) {
-  const long long nq = ((FORM == NT ? a.N : a.K) + Q - 1) / Q;
-  const long long most = a.E < a.M ? a.E : a.M;  // experts with rows
-  const long long tiles = FORM == TN ? (long long)a.E * ((a.N + P - 1) / P) * nq : (a.M / P + most) * nq;
-  // whole rounds of 8 XCDs of 32 tiles (tile_of)
-  const long long grid = (tiles + 255) / 256 * 256;
-  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB>), dim3((unsigned)grid), dim3(WP * WQ * 64), 0, s, a);
+hipError_t launch_tile(const GroupedArgs& args, hipStream_t s) {
+  const long long outs = FORM == NT ? args.N : args.K, nq = (outs + Q - 1) / Q;
+  const long long most = args.E < args.M ? args.E : args.M;  // experts with rows
+  const long long tiles = FORM == TN ? (long long)args.E * ((args.N + P - 1) / P) * nq : (args.M / P + most) * nq;
+  GroupedArgs a = args;
+  a.group = (int)(tiles >= 256 ? 32 : (tiles + 7) / 8);
+  const long long round = 8 * a.group;  // (tile_of)
+  const dim3 grid((unsigned)((tiles + round - 1) / round * round), a.parts);
+  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB>), grid, dim3(WP * WQ * 64), 0, s, a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || a.parts == 1) return err;
+  const long long n = (FORM == TN ? (long long)a.E * a.N : a.M) * outs / 8;
+  hipLaunchKernelGGL((grouped_sum_kernel<FORM == TN>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, (int)outs);
   return hipGetLastError();
 }
 
-// Row tiles of `size` rows over `most` experts with rows: about half of each
-// expert's last one is empty.
-long long row_tiles(long long M, long long most, int size) {
-  const long long n = (M + size / 2 * most) / size;
-  return n > most ? n : most;
-}
-
 template <int FORM, int GRAN>
-hipError_t launch_form(const GroupedArgs& a, hipStream_t s) {
-  const long long M = a.M, most = a.E < M ? a.E : M, outs = FORM == NT ? a.N : a.K;
-  auto tiles = [&](int P, int Q) { return (FORM == TN ? (long long)a.E * ((a.N + P - 1) / P) : row_tiles(M, most, P)) * ((outs + Q - 1) / Q); };
-  if constexpr (FORM == TN) {
-    // 256 x 256 where it fills the chip
-    if (a.N > 128 && a.K > 128 && tiles(256, 256) >= 256) return launch_tile<FORM, 0, 256, 256, 2, 4, 3>(a, s);
-    return launch_tile<FORM, 0, 128, 128, 2, 2, 2>(a, s);
-  } else {
-    if constexpr (FORM == NT) {
-      if (M <= (GRAN ? 16 : 6) * most) return launch_few<GRAN, 2, 1, GRAN ? 1 : 3>(a, s);
-      if (M <= 12 * most || (M <= 100 * most && tiles(64, 128) < 256)) return launch_few<GRAN, 2, 2, GRAN ? 1 : 3>(a, s);
-    }
-    if (tiles(256, 256) >= 256 && outs > 128 && (GRAN == 0 || M >= 192 * most)) return launch_tile<FORM, GRAN, 256, 256, 2, 4, GRAN ? 2 : 3>(a, s);
-    if (tiles(128, 128) >= 256 && (GRAN == 0 || M >= 96 * most)) return launch_tile<FORM, GRAN, 128, 128, 2, 2, GRAN ? 2 : 3>(a, s);
-    return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
+hipError_t launch_form(const GroupedArgs& a, const GroupedPlan& plan, hipStream_t s) {
+  if constexpr (FORM == NT) {
+    if (plan.few == 1) return launch_few<GRAN, 2, 1, GRAN ? 1 : 3>(a, s);
+    if (plan.few == 2) return launch_few<GRAN, 2, 2, GRAN ? 1 : 3>(a, s);
   }
+  if (plan.tile == 256) return launch_tile<FORM, GRAN, 256, 256, 2, 4, GRAN ? 2 : 3>(a, s);
+  if constexpr (FORM != TN) {
+    if (plan.tile == 64) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
+  }
+  return launch_tile<FORM, GRAN, 128, 128, 2, 2, GRAN || FORM == TN ? 2 : 3>(a, s);
 }
 
 }  // namespace
 
+// Stages of a sum (an average one's).
+static long long stages_of(int form, long long M, long long E, long long N, long long K) {
+  const long long most = E < M ? E : M;
+  return ((form == NT ? K : form == NN ? N : most ? M / most : 0) + kS - 1) / kS;
+}
+
+static long long most_parts(int form, long long M, long long E, long long N, long long K) {
+  const long long stages = stages_of(form, M, E, N, K);
+  return stages < 16 ? 1 : stages / 4 > 32 ? 32 : stages / 4;
+}
+
+// With fewer than 256 tiles the sums are split so that there are up to 512, four
+// stages of 64 elements at least to a part (a stage of a lone workgroup takes 0.5
+// us, its loads' latency), where that saves more than the 6 us of adding the parts:
+// 60 rows of one expert, N = K = 4096: dx 44 -> 20 us; dW of 8192 rows of one
+// expert, 64 x 4096: 94 -> 28 us.  (Up to 256 parts times tiles: 300 rows' dx 43 us,
+// with up to 512 27 us.)
+GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long long K, int gran) {
+  const long long most = E < M ? E : M, outs = form == NT ? N : K;
+  // Row tiles over `most` experts with rows: about half of each expert's last one is empty.
+  auto tiles = [&](int P, int Q) {
+    const long long n = (M + P / 2 * most) / P, rows = form == TN ? E * ((N + P - 1) / P) : n > most ? n : most;
+    return rows * ((outs + Q - 1) / Q);
+  };
+  GroupedPlan p{0, 128, 1};
+  if (form == TN) {
+    if (N > 128 && K > 128 && tiles(256, 256) >= 256) p.tile = 256;
+  } else {
+    if (form == NT && M <= (gran ? 16 : 6) * most) p.few = 1;
+    else if (form == NT && M <= 12 * most) p.few = 2;
+    if (p.few) return p;
+    if (tiles(256, 256) >= 256 && outs > 128 && (gran == 0 || M >= 192 * most)) p.tile = 256;
+    else if (tiles(128, 128) >= 256 && (gran == 0 || M >= 96 * most)) p.tile = 128;
+    else p.tile = 64;
+  }
+  const long long n = p.tile == 256 ? tiles(256, 256) : p.tile == 128 ? tiles(128, 128) : tiles(64, 128);
+  p.parts = (int)most_parts(form, M, E, N, K);  // (1 without rows)
+  if (p.parts > 512 / n) p.parts = (int)(512 / n);
+  const long long stages = stages_of(form, M, E, N, K);
+  if (n >= 256 || p.parts < 2 || stages * (p.parts - 1) < 18 * p.parts) p.parts = 1;
+  return p;
+}
+
+long long grouped_part_floats(int form, long long M, long long E, long long N, long long K) {
+  const long long outs = form == NT ? N : K, nq = (outs + 127) / 128;
+  const long long parts = most_parts(form, M, E, N, K);
+  if (parts < 2) return 0;
+  if (form == TN) {
+    const long long n = E * ((N + 127) / 128) * nq;
+    return n >= 256 ? 0 : (parts < 512 / n ? parts : 512 / n) * E * N * K;
+  }
+  // (fewer than 256 tiles have no more rows than this: one expert per tile at
+  // least, 64 rows and half a tile of each expert at most)
+  long long rows = E * nq < 256 ? M : 256 / nq;
+  if (rows > M || form == NT) rows = M;
+  if (form == NT && E * nq >= 256) return 0;  // (what is not `few` has rows for every expert)
+  const long long all = parts * rows * outs, cap = 512LL * 96 * 128;
+  return all < cap ? all : cap;
+}
+
 hipError_t launch_grouped(const GroupedArgs& args, int form, hipStream_t s) {
   GroupedArgs a = args;
+  const GroupedPlan plan = grouped_plan(form, a.M, a.E, a.N, a.K, a.gran);
   const long long outs = form == TN ? (long long)a.E * a.N * a.K : (long long)a.M * (form == NT ? a.N : a.K);
   a.stream = outs * (a.out_f32 ? 4 : 2) > (256LL << 20);
-  if (form == TN) return launch_form<TN, 0>(a, s);
-  if (a.gran == 16) return form == NT ? launch_form<NT, 16>(a, s) : launch_form<NN, 16>(a, s);
-  if (a.gran == 32) return form == NT ? launch_form<NT, 32>(a, s) : launch_form<NN, 32>(a, s);
-  return form == NT ? launch_form<NT, 0>(a, s) : launch_form<NN, 0>(a, s);
+  a.parts = plan.parts;
+  if (form == TN) return launch_form<TN, 0>(a, plan, s);
+  if (a.gran == 16) return form == NT ? launch_form<NT, 16>(a, plan, s) : launch_form<NN, 16>(a, plan, s);
+  if (a.gran == 32) return form == NT ? launch_form<NT, 32>(a, plan, s) : launch_form<NN, 32>(a, plan, s);
+  return form == NT ? launch_form<NT, 0>(a, plan, s) : launch_form<NN, 0>(a, plan, s);
 }
 
 }  // namespace moefp4

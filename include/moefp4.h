@@ -318,8 +318,8 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
  * (as moe_fp4_route gives them); an expert may have no rows, and rows outside
  * [offsets[0], offsets[E]) are not read and their outputs are left as they are.
  * (Offsets are taken within [0, M], so that no value of them reaches memory
- * outside the tensors; where they descend, rows may be computed with any of the
- * experts whose range holds them, or not at all.)
+ * outside the tensors; where they descend, what the outputs hold is not
+ * specified.)
  *   moe_fp4_grouped     y[r]  = W_e x[r]                 [M, N]
  *   moe_fp4_grouped_dx  dx[r] = W_e^T dy[r]              [M, K]
  *   moe_fp4_grouped_dw  dW_e  = sum over e's rows of dy[r] x[r]^T   [E, N, K]
@@ -334,16 +334,24 @@ typedef struct moefp4_grouped {
   int32_t E, gran_k, out_fmt;
 } moefp4_grouped;
 
-/* x, dy, w, w_sf and out 16-byte aligned, all device memory; N and K multiples
- * of 8, K of 32 with FP4 weights (EINVAL otherwise); E up to 512, M up to 2^24, N
- * and K up to 2^20, M*N, M*K and E*N*K below 2^40 (EUNSUPPORTED otherwise).  out
- * overlaps no input (EINVAL).  No workspace.  Enqueued on `stream`. */
+/* Workspace of one of the calls (direction) on p; it serves smaller M as well.
+ * 0 bytes: none is needed, and NULL is taken. */
+typedef enum moefp4_grouped_direction { MOEFP4_GROUPED = 0, MOEFP4_GROUPED_DX = 1, MOEFP4_GROUPED_DW = 2 } moefp4_grouped_direction;
+moefp4_status moe_fp4_grouped_workspace_bytes(const moefp4_grouped* p, int32_t direction, size_t* bytes);
+
+/* x, dy, w, w_sf and out 16-byte aligned, the workspace 256-byte aligned, all
+ * device memory; N and K multiples of 8, K of 32 with FP4 weights (EINVAL
+ * otherwise); E up to 512, M up to 2^24, N and K up to 2^20, M*N, M*K and E*N*K
+ * below 2^40 (EUNSUPPORTED otherwise).  out overlaps no input and not the
+ * workspace (EINVAL).  Enqueued on `stream`. */
 moefp4_status moe_fp4_grouped(const moefp4_grouped* p, const void* x, const void* w, const uint8_t* w_sf,
-                              const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream);
+                              const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
+                              hipStream_t stream);
 moefp4_status moe_fp4_grouped_dx(const moefp4_grouped* p, const void* dy, const void* w, const uint8_t* w_sf,
-                                 const float* w_gs, const int32_t* offsets, void* out, hipStream_t stream);
+                                 const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream);
 moefp4_status moe_fp4_grouped_dw(const moefp4_grouped* p, const void* dy, const void* x, const int32_t* offsets,
-                                 void* out, int32_t accumulate, hipStream_t stream);
+                                 void* out, int32_t accumulate, void* workspace, size_t ws_bytes, hipStream_t stream);
 
 /* The norms before and after a layer, fused with the layer's gate and residual
  * scale (a row of h is a token's residual stream, y the layer's output):

@@ -126,7 +126,9 @@ class Case:
 SHAPES = [([1], 8, 32), ([1], 4096, 2080), ([3, 0, 2], 24, 96), ((8, 64), 520, 288), ((40, 60), 72, 1056), ((90, 9), 264, 160),
           ([17, 0, 1, 33], 136, 320), ([0, 300, 0], 1000, 704), ((700, 3), 1096, 224), ([63, 64, 65, 1], 256, 128),
           ([127, 128, 129, 0], 384, 64), ([255, 256, 257], 648, 96), ((1500, 12), 2056, 512), ([2100, 2000], 4104, 96),
-          ((4000, 64), 32, 512), ((4000, 64), 512, 32), ([1000], 16, 2048), ([60], 2048, 4096)]
+          ((4000, 64), 32, 512), ((4000, 64), 512, 32), ([1000], 16, 2048), ([60], 2048, 4096),
+          # sums in parts: few tiles, long sums; fewer stages than parts in one expert
+          ([5000], 64, 256), ([1300, 0, 20], 1320, 1184), ([33], 1096, 2080)]
 
 
 def rows_of(shape, seed=0):
@@ -215,7 +217,7 @@ def test_special_values_in_a_group():
 
 def test_dw_accumulates():
     require_gpu()
-    for rows, N, K in (([5, 0, 70], 40, 72), ([300, 0, 65], 520, 136), ([2000, 0], 2056, 2056)):
+    for rows, N, K in (([5, 0, 70], 40, 72), ([300, 0, 65], 520, 136), ([2000, 0], 2056, 2056), ([4000, 0, 9000], 72, 136)):
         c = Case(rows, N, K)
         ref = moe.grouped_dw(c.dy, c.x, c.off, out_dtype=torch.float32)
         old = torch.randn((c.E, N, K), device="cuda")
@@ -255,6 +257,27 @@ def test_offsets_beyond_the_rows_are_taken_within():
                  (moe.grouped_dx(c.dy, c.w, off, **f32), moe.grouped_dx(c.dy, c.w, c.off, **f32)),
                  (moe.grouped_dw(c.dy, c.x, off, **f32), moe.grouped_dw(c.dy, c.x, c.off, **f32))):
         assert torch.equal(a, b)
+
+
+def test_workspace_guard_and_smaller_batches():
+    """Sums in parts stay within the workspace that is asked for, which serves smaller batches too."""
+    require_gpu()
+    for d, (N, K) in enumerate(((64, 2048), (2048, 64), (64, 264))):
+        big = Case([4000], N, K)
+        need = moe._grouped_need(d, 4000, N, K, 1, 0, 1)
+        assert need > 0
+        buf = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        at = (-buf.data_ptr()) % 256
+        ws = buf[at:at + need]
+        for rows in (4000, 700, 65, 33, 1):
+            c = Case([rows], N, K)
+            f = (lambda **k: moe.grouped(c.x, c.w, c.off, **k), lambda **k: moe.grouped_dx(c.dy, c.w, c.off, **k),
+                 lambda **k: moe.grouped_dw(c.dy, c.x, c.off, **k))[d]
+            assert torch.equal(f(), f(workspace=ws))
+        with pytest.raises(moe.MoeFp4Error, match="workspace"):
+            c = big
+            f(workspace=ws[:256])
+        assert bool((buf[:at] == 0x5A).all()) and bool((buf[at + need:] == 0x5A).all())
 
 
 def test_512_experts():

@@ -54,24 +54,24 @@ BAD_SIZES = [(dict(M=-1), m.EINVAL), (dict(E=0), m.EINVAL), (dict(N=0), m.EINVAL
 @pytest.mark.parametrize("kw,status", BAD_SIZES)
 def test_grouped_sizes(L, kw, status):
     p = problem(**kw)
-    calls = (lambda: L.moe_fp4_grouped(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z),
-             lambda: L.moe_fp4_grouped_dx(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z),
-             lambda: L.moe_fp4_grouped_dw(ctypes.byref(p), Z, Z, Z, Z, 0, Z))
+    calls = (lambda: L.moe_fp4_grouped(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z, 0, Z),
+             lambda: L.moe_fp4_grouped_dx(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z, 0, Z),
+             lambda: L.moe_fp4_grouped_dw(ctypes.byref(p), Z, Z, Z, Z, 0, Z, 0, Z))
     for call in calls:
         assert call() == status and len(L.moefp4_last_error()) > 0
 
 
 def test_grouped_refuses_before_launch(L):
     for fn in (L.moe_fp4_grouped, L.moe_fp4_grouped_dx):
-        assert fn(None, Z, Z, Z, Z, Z, Z, Z) == m.EINVAL
+        assert fn(None, Z, Z, Z, Z, Z, Z, Z, 0, Z) == m.EINVAL
         p = problem()
-        assert fn(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z) == m.OK  # no rows: nothing to do
+        assert fn(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z, 0, Z) == m.OK  # no rows: nothing to do
         p = problem(gran_k=16, K=48)
-        assert fn(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z) == m.EINVAL and b"32" in L.moefp4_last_error()
+        assert fn(ctypes.byref(p), Z, Z, Z, Z, Z, Z, Z, 0, Z) == m.EINVAL and b"32" in L.moefp4_last_error()
         for gran in (0, 32):
             p = problem(M=16, gran_k=gran)
             good = [far(0), far(1), far(2) if gran else Z, Z, far(4), far(5)]
-            call = lambda a: fn(ctypes.byref(p), *a, Z)
+            call = lambda a: fn(ctypes.byref(p), *a, far(9), BIG, Z)
             for k in (0, 1, 4, 5):
                 a = list(good)
                 a[k] = Z
@@ -95,12 +95,12 @@ def test_grouped_refuses_before_launch(L):
 
 def test_grouped_dw_refuses_before_launch(L):
     fn = L.moe_fp4_grouped_dw
-    assert fn(None, Z, Z, Z, Z, 0, Z) == m.EINVAL
+    assert fn(None, Z, Z, Z, Z, 0, Z, 0, Z) == m.EINVAL
     p = problem(gran_k=16)
-    assert fn(ctypes.byref(p), Z, Z, Z, Z, 0, Z) == m.EINVAL
+    assert fn(ctypes.byref(p), Z, Z, Z, Z, 0, Z, 0, Z) == m.EINVAL
     p = problem(M=16)
     good = [far(0), far(1), far(2), far(3)]
-    call = lambda a: fn(ctypes.byref(p), *a, 0, Z)
+    call = lambda a: fn(ctypes.byref(p), *a, 0, far(9), BIG, Z)
     for k in range(4):
         a = list(good)
         a[k] = Z
@@ -112,7 +112,53 @@ def test_grouped_dw_refuses_before_launch(L):
             a[3] = a[k]
             assert call(a) == m.EINVAL and b"overlaps" in L.moefp4_last_error()
     p = problem(M=0)
-    assert fn(ctypes.byref(p), Z, Z, far(2), Z, 0, Z) == m.EINVAL  # dw is written whole
+    assert fn(ctypes.byref(p), Z, Z, far(2), Z, 0, Z, 0, Z) == m.EINVAL  # dw is written whole
+    assert fn(ctypes.byref(p), Z, Z, far(2), far(2), 0, Z, 0, Z) == m.EINVAL and b"overlaps" in L.moefp4_last_error()
+
+
+def grouped_ws(L, direction, **kw):
+    n = ctypes.c_size_t(0)
+    return L.moe_fp4_grouped_workspace_bytes(ctypes.byref(problem(**kw)), direction, ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("kw,status", BAD_SIZES)
+def test_grouped_workspace_sizes(L, kw, status):
+    for d in range(3):
+        assert grouped_ws(L, d, **kw)[0] == status
+    assert grouped_ws(L, 3)[0] == m.EINVAL and grouped_ws(L, -1)[0] == m.EINVAL
+    assert L.moe_fp4_grouped_workspace_bytes(ctypes.byref(problem()), 0, None) == m.EINVAL
+
+
+def test_grouped_workspace_serves_smaller_batches(L):
+    """What a call asks for is never more than the workspace of a larger batch.  (The calls are refused in any case: their
+    out lies over an input.)"""
+    asked = 0
+    for N, K, E in ((4096, 4096, 1), (64, 4096, 1), (4096, 64, 3), (1024, 2048, 8), (2048, 1024, 60), (8, 6144, 64), (1 << 20, 64, 1),
+                    (3200, 1280, 17)):
+        for d in range(3):
+            have = 0
+            for M in (1, 2, 7, 13, 40, 64, 65, 96, 200, 700, 2000, 5000, 8191, 60000):
+                st, n = grouped_ws(L, d, M=M, N=N, K=K, E=E)
+                assert st == m.OK and have <= n <= 64 << 20 and n % 256 == 0, (d, M, N, K, E)
+                have = n
+                p = ctypes.byref(problem(M=M, N=N, K=K, E=E))
+                call = lambda ws, by: (L.moe_fp4_grouped, L.moe_fp4_grouped_dx)[d](p, far(0), far(1), Z, Z, far(4), far(0), ws, by, Z) \
+                    if d < 2 else L.moe_fp4_grouped_dw(p, far(0), far(1), far(4), far(0), 0, ws, by, Z)
+                st = call(Z, 0)
+                assert st in (m.EWORKSPACE, m.EINVAL)
+                if st == m.EWORKSPACE:
+                    asked += 1
+                    need = int(L.moefp4_last_error().split()[2])
+                    assert need <= n, (d, M, N, K, E)
+                    assert call(far(9), need - 1) == m.EWORKSPACE
+                    assert call(odd(9, 64), need) == m.EINVAL and b"256" in L.moefp4_last_error()
+                    assert call(far(9), need) == m.EINVAL and b"out overlaps" in L.moefp4_last_error()
+    assert asked > 20
+    # the workspace over an input or out
+    p = ctypes.byref(problem(M=60, N=4096, K=4096, E=1))
+    for k in (0, 1, 4, 5):
+        assert L.moe_fp4_grouped_dx(p, far(0), far(1), Z, Z, far(4), far(5), far(k), BIG, Z) == m.EINVAL
+        assert b"workspace overlaps" in L.moefp4_last_error()
 
 
 def norm(**kw):
