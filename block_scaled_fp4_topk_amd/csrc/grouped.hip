@@ -61,34 +61,39 @@ __device__ __forceinline__ void tile_at(int i, int np, int nq, int* p, int* q) {
 struct Rows { int e, r0, n, i, np; };  // expert, its first row, its rows, the tile among the expert's, row tiles
 
 // The expert that tile `tile` belongs to, where every row tile of `size` rows
-// has nq tiles; e = -1 behind the last tile.  Every wave finds it by itself: a
-// lane counts the tiles of E / 64 experts.
+// has nq tiles; e = -1 behind the last tile.  Every wave finds it by itself, a
+// lane counting the tiles of E / 64 experts, whose offsets it loads all at once.
 __device__ __forceinline__ Rows rows_of(const int32_t* offsets, int E, int M, int size, int nq, int tile) {
-  const int lane = threadIdx.x & 63, per = (E + 63) >> 6, e0 = min(lane * per, E), e1 = min(e0 + per, E);
-  int cnt = 0, a = min(max(offsets[e0], 0), M);
-  for (int e = e0; e < e1; ++e) {
-    const int b = min(max(offsets[e + 1], 0), M);
-    cnt += (max(b - a, 0) + size - 1) / size;
-    a = b;
-  }
+  constexpr int kPer = kMaxExperts / 64;
+  const int lane = threadIdx.x & 63, per = (E + 63) >> 6, e0 = lane * per;
+  int at[kPer + 1], cnt = 0;
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) at[i] = i <= per ? offsets[min(e0 + i, E)] : 0;
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) at[i] = min(max(at[i], 0), M);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) cnt += i < per ? (max(at[i + 1] - at[i], 0) + size - 1) / size : 0;
   int incl = cnt;
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(incl, d, 64);
     if (lane >= d) incl += v;
   }
   const int want = tile / nq;
   const uint64_t in = __ballot(want < incl);
-  Rows r{-1, 0, 0, 0, 0};
-  if (in == 0) return r;
-  const int src = __builtin_ctzll(in);
-  int before = __builtin_amdgcn_readlane(incl - cnt, src);
-  for (int e = src * per; e < E; ++e) {
-    const int s = min(max(offsets[e], 0), M), b = min(max(offsets[e + 1], 0), M);
-    const int n = max(b - s, 0), t = (n + size - 1) / size;
-    if (want < before + t) return Rows{e, s, n, tile - before * nq, t};
+  if (in == 0) return Rows{-1, 0, 0, 0, 0};
+  // (every lane among its own; what counts is the lane that holds the tile)
+  Rows r{0, 0, 0, 0, 0};
+  int before = incl - cnt;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int n = max(at[i + 1] - at[i], 0), t = i < per ? (n + size - 1) / size : 0;
+    if (want >= before && want < before + t) r = Rows{e0 + i, at[i], n, tile - before * nq, t};
     before += t;
   }
-  return r;
+  const int src = __builtin_ctzll(in);
+  return Rows{__builtin_amdgcn_readlane(r.e, src), __builtin_amdgcn_readlane(r.r0, src), __builtin_amdgcn_readlane(r.n, src),
+              __builtin_amdgcn_readlane(r.i, src), __builtin_amdgcn_readlane(r.np, src)};
 }
 
 // ---------------------------------------------------------------------------
@@ -157,11 +162,13 @@ struct Operand {
     for (int i = 0; i < kPieces; ++i) piece(st, i, lds);
   }
 
-  // zeros behind the sum's last element in its last stage, of which `left` exist
+  // Zeros behind the sum's last element in its last stage, of which `left` exist.
+  // (Across the sum what lies behind it lies behind the buffer's end, and is zeros
+  // already.)
+  static constexpr bool kClear = !TR;
   __device__ __forceinline__ static void clear(int left, uint8_t* lds) {
     for (int v = threadIdx.x; v < kBytes / 16; v += NTH) {
-      const bool out = TR ? v / (SIZE / 8) >= left : 8 * ((v & 7) ^ pswz(v >> 3)) >= left;
-      if (out) *reinterpret_cast<uint4*>(lds + 16 * v) = uint4{0, 0, 0, 0};
+      if (8 * ((v & 7) ^ pswz(v >> 3)) >= left) *reinterpret_cast<uint4*>(lds + 16 * v) = uint4{0, 0, 0, 0};
     }
   }
 
@@ -222,6 +229,13 @@ __device__ __forceinline__ u32x4 dq8_scaled_bf16(uint32_t codes, float scale) {
 template <bool TR, int SIZE, int NTH, int GRAN>
 struct Fp4Operand : Operand<TR, SIZE, NTH> {
   static_assert(SIZE * kS == 32 * NTH, "32 codes per thread and stage");
+  static constexpr bool kClear = true;
+  __device__ __forceinline__ static void clear(int left, uint8_t* lds) {
+    for (int v = threadIdx.x; v < SIZE * kS / 8; v += NTH) {
+      const bool out = TR ? v / (SIZE / 8) >= left : 8 * ((v & 7) ^ pswz(v >> 3)) >= left;
+      if (out) *reinterpret_cast<uint4*>(lds + 16 * v) = uint4{0, 0, 0, 0};
+    }
+  }
   static constexpr int kPer = TR ? SIZE / 32 : 2;  // pieces of a row
   const uint8_t *codes, *sf;  // uniform
   int K;
@@ -304,14 +318,22 @@ __device__ __forceinline__ void store(const V& v, V* to, bool past) {
   }
 }
 
-// Every wave's LDS accesses done, and its loads but the LEFT newest (LEFT < 16),
-// and a barrier.
+// Every wave's LDS accesses done, and its memory accesses but the LEFT newest
+// (LEFT <= 63), and a barrier.
 template <int LEFT>
 __device__ __forceinline__ void wait_all() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | LEFT);  // vmcnt(LEFT) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);  // vmcnt(LEFT) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Every wave's loads but the `left` (0, 4, 8 or 16) newest accesses done, and a barrier.
+__device__ __forceinline__ void wait_loads(int left) {
+  if (left == 0) wait_all<0>();
+  else if (left == 4) wait_all<4>();
+  else if (left == 8) wait_all<8>();
+  else wait_all<16>();
 }
 
 // ---------------------------------------------------------------------------
@@ -321,20 +343,24 @@ __device__ __forceinline__ void wait_all() {
 // output's contiguous side; WP x WQ waves.  blockIdx.y: the part of the sum (more
 // than one: to a.part as float32, which grouped_sum adds up).  GRAN: 0, or FP4 weights' group.  NB:
 // stages of the Q side in LDS (of the P side 2): where the weights come from HBM,
-// two stages of them in flight.
-template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
+// two stages of them in flight.  MANY: a workgroup takes a.many tiles next to each
+// other along Q, the first loads of one on their way while the one before is
+// stored: for short sums, where finding the expert and waiting for a lone stage is
+// most of a tile's time.  (2: sums of one stage, whose room is that of one.)
+template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB, int MANY>
 __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) void grouped_tile_kernel(GroupedArgs a) {
   constexpr int NTH = WP * WQ * 64;
   constexpr int NP = P / WP / 16, NQ = Q / WQ / 16;  // a wave's 16-row tiles
   typedef Operand<FORM == TN, P, NTH> OpP;
   typedef typename WeightOperand<FORM != NT, Q, NTH, GRAN>::type OpQ;
   constexpr bool kFar = GRAN == 0 && NB == 3;  // the Q side's loads run two stages ahead, else one
-  __shared__ __attribute__((aligned(4096))) uint8_t s_p[2 * OpP::kBytes], s_q[NB * OpQ::kBytes];
+  __shared__ __attribute__((aligned(4096))) uint8_t s_p[(MANY == 2 ? 1 : 2) * OpP::kBytes], s_q[NB * OpQ::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_turn[MANY ? WP * WQ * 4096 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
   const int outs = FORM == NT ? a.N : a.K;  // the output's contiguous side
-  const int nq = (outs + Q - 1) / Q;
+  const int nq = MANY ? ((outs + Q - 1) / Q + a.many - 1) / a.many : (outs + Q - 1) / Q;
   const int tile = tile_of(blockIdx.x, a.group);
   Rows r;
   if constexpr (FORM == TN) {
@@ -346,13 +372,16 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
     r = rows_of(a.offsets, a.E, a.M, P, nq, tile);
     if (r.e < 0) return;
   }
-  r.e = __builtin_amdgcn_readfirstlane(r.e);
-  r.r0 = __builtin_amdgcn_readfirstlane(r.r0);
-  r.n = __builtin_amdgcn_readfirstlane(r.n);
+  if constexpr (FORM == TN) {
+    r.r0 = __builtin_amdgcn_readfirstlane(r.r0);
+    r.n = __builtin_amdgcn_readfirstlane(r.n);
+  }
   int tp, tq;
-  tile_at(__builtin_amdgcn_readfirstlane(r.i), __builtin_amdgcn_readfirstlane(r.np), nq, &tp, &tq);
-  const int p0 = tp * P, q0 = tq * Q;
-  const int pn = (FORM == TN ? a.N : r.n) - p0, qn = outs - q0;  // what exists of the tile
+  tile_at(r.i, r.np, nq, &tp, &tq);
+  const int p0 = tp * P;
+  int q0 = tq * Q * (MANY ? a.many : 1);
+  const int q_end = MANY ? min(outs, q0 + Q * a.many) : outs;
+  const int pn = (FORM == TN ? a.N : r.n) - p0;  // what exists of the tile
   // the stages [s0, s1) of the sum, which ends at element `sum` here
   const int whole = FORM == NT ? a.K : FORM == NN ? a.N : r.n;
   const int per = ((whole + kS - 1) / kS + a.parts - 1) / a.parts;
@@ -362,27 +391,27 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
 
   OpP op;
   OpQ oq;
-  if constexpr (FORM == TN) {
-    op.init(a.p + (size_t)r.r0 * a.N + p0, 2 * a.N, pn);
-    oq.init(a.q + (size_t)r.r0 * a.K + q0, 2 * a.K, qn);
-  } else {
-    op.init(a.p + (size_t)(r.r0 + p0) * whole, 2 * whole, pn);
-    // the weights' first row and column of the tile
-    const size_t row = (size_t)r.e * a.N + (FORM == NT ? q0 : 0);
-    const int col = FORM == NT ? 0 : q0;
-    if constexpr (GRAN != 0) {
-      oq.init(a.w + row * (a.K / 2) + col / 2, a.w_sf + row * (a.K / GRAN) + col / GRAN, a.K, qn);
-      if (s1 > s0) oq.fetch(s0, sum);
+  auto aim = [&]() __attribute__((always_inline)) {  // the Q side at q0
+    const int qn = outs - q0;
+    if constexpr (FORM == TN) {
+      oq.init(a.q + (size_t)r.r0 * a.K + q0, 2 * a.K, qn);
     } else {
-      oq.init(a.q + row * a.K + col, 2 * a.K, qn);
+      // the weights' first row and column of the tile
+      const size_t row = (size_t)r.e * a.N + (FORM == NT ? q0 : 0);
+      const int col = FORM == NT ? 0 : q0;
+      if constexpr (GRAN != 0) {
+        oq.init(a.w + row * (a.K / 2) + col / 2, a.w_sf + row * (a.K / GRAN) + col / GRAN, a.K, qn);
+        if (s1 > s0) oq.fetch(s0, sum);
+      } else {
+        oq.init(a.q + row * a.K + col, 2 * a.K, qn);
+      }
     }
-  }
+  };
+  if constexpr (FORM == TN) op.init(a.p + (size_t)r.r0 * a.N + p0, 2 * a.N, pn);
+  else op.init(a.p + (size_t)(r.r0 + p0) * whole, 2 * whole, pn);
+  aim();
 
   v4f acc[NQ][NP];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i)
-#pragma unroll
-    for (int j = 0; j < NP; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   // Half of the row tiles at a time (a phase): 16 products per wave at 128 x 64.
   constexpr int NH = NP / 2;
   u32x4 fq[2][NQ], fp[2][NH];
@@ -413,13 +442,17 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   };
   // A stage's loads have landed, and every wave has read the one before; what lies
   // behind the sum in its last stage is cleared.
+  int stores = 0;  // newer than a tile's first loads
+  bool lone = false;  // (a lone stage's P side is cleared once)
   auto handover = [&](bool last, uint32_t pb, uint32_t qb) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    wait_all<kFar ? OpQ::kPieces : 0>();  // (the stage after it is still on its way)
-    if (tail && last) {
-      OpP::clear(tail, s_p + pb);
-      OpQ::clear(tail, s_q + qb);
-      wait_all<kFar ? OpQ::kPieces : 0>();
+    if constexpr (MANY) wait_loads(stores);
+    else wait_all<kFar ? OpQ::kPieces : 0>();  // (the stage after it is still on its way)
+    stores = 0;
+    if ((OpQ::kClear || (OpP::kClear && !lone)) && tail && last) {
+      if (OpP::kClear && !lone) OpP::clear(tail, s_p + pb);
+      if constexpr (OpQ::kClear) OpQ::clear(tail, s_q + qb);
+      wait_all<MANY ? 63 : kFar ? OpQ::kPieces : 0>();
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -453,7 +486,7 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       read_q(0, 0);
       read_p(0, 0, 0);
     }
-    for (int s = s0; s < s1 - 1; ++s) {
+    for (int s = s0; MANY < 2 && s < s1 - 1; ++s) {
       three();
       const uint32_t old_p = pb, old_q = qb;
       pb ^= OpP::kBytes;
@@ -482,25 +515,40 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
     three();
     if constexpr (both) multiply(1, 1);
   };
-  if (s1 > s0) {
-    // (the newest loads are the Q side's farthest stage)
-    if constexpr (!kFar) op.load(s0, sum, s_p);
+  // The first stage's loads (the newest are the Q side's farthest stage).
+  // (a lone stage's P side stays where it is)
+  auto start = [&](bool first) __attribute__((always_inline)) {
+    if (s1 <= s0) return;
+    if (!kFar && (first || s1 - s0 > 1)) op.load(s0, sum, s_p);
     oq.load(s0, sum, s_q);
     if constexpr (kFar) {
       op.load(s0, sum, s_p);
       oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
     }
+  };
+  start(true);
+  const float gs = GRAN && a.w_gs ? a.w_gs[r.e] : 1.0f;
+  const size_t row0 = FORM == TN ? (size_t)r.e * a.N + p0 : (size_t)(r.r0 + p0);
+  const bool one = a.parts == 1, f32 = a.out_f32 || !one, add = FORM == TN && one && a.accumulate, past = one && a.stream;
+  void* out = one ? a.out : a.part + (size_t)blockIdx.y * (FORM == TN ? (size_t)a.E * a.N : (size_t)a.M) * outs;
+  for (;;) {
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+#pragma unroll
+    for (int j = 0; j < NP; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (s1 > s0) {
+    pb = qb = 0;
     handover(s1 - s0 == 1, 0, 0);
-    op.load(s0 + 1, sum, s_p + OpP::kBytes);
-    if constexpr (kFar) oq.load(s0 + 2, sum, s_q + 2 * OpQ::kBytes);
-    else oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
+    if constexpr (MANY < 2) {
+      op.load(s0 + 1, sum, s_p + OpP::kBytes);
+      if constexpr (kFar) oq.load(s0 + 2, sum, s_q + 2 * OpQ::kBytes);
+      else oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
+    }
     if (FORM == TN || pn > wp + 16 * NH) stages(std::integral_constant<int, 2>{});
     else if (pn > wp) stages(std::integral_constant<int, 1>{});
     else stages(std::integral_constant<int, 0>{});
   }
-
-  if (GRAN == 16 || GRAN == 32) {
-    const float gs = a.w_gs ? a.w_gs[r.e] : 1.0f;
+  if constexpr (GRAN != 0) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -510,16 +558,31 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   // are written (E = 16, N = 4096, K = 6144, float32: 8192 rows' dW 731 -> 704 us);
   // past the caches where the output is larger than the last one (687 us; 64
   // experts of 2048 x 2048, 16384 rows 367 -> 286 us).
-  static_assert(Q / WQ == 64 && WP * WQ * 4096 <= 2 * OpP::kBytes, "4 KB per wave");
-  wait_all<0>();  // (every wave is done with the stages)
-  v4f* turn = reinterpret_cast<v4f*>(s_p) + wave * 256;  // [16][16], piece c of row r at c ^ r
-  const size_t row0 = FORM == TN ? (size_t)r.e * a.N + p0 : (size_t)(r.r0 + p0);
-  const bool one = a.parts == 1, f32 = a.out_f32 || !one, add = FORM == TN && one && a.accumulate, past = one && a.stream;
-  void* out = one ? a.out : a.part + (size_t)blockIdx.y * (FORM == TN ? (size_t)a.E * a.N : (size_t)a.M) * outs;
+  static_assert(Q / WQ == 64 && (MANY || WP * WQ * 4096 <= 2 * OpP::kBytes), "4 KB per wave");
+  if constexpr (MANY) wait_all<63>();  // (every wave is done with the stages; `turn` lies elsewhere)
+  else wait_all<0>();                  // (and no load is left that would write to it)
+  v4f* turn = reinterpret_cast<v4f*>(MANY ? s_turn : s_p) + wave * 256;  // [16][16], piece c of row r at c ^ r
+  const int q00 = q0, qn = outs - q0;
+  const bool again = MANY && q0 + Q < q_end;
+  if (again) {
+    q0 += Q;
+    aim();
+    start(false);
+    lone = s1 - s0 == 1;
+  }
+  // MANY: every store is issued, dropped where the tile has no such row or column,
+  // so that their number is known to the next wait for loads.
+  const int eb = f32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(out) + (row0 * outs + q00) * eb, 0,
+                                                                       min(pn, P) * outs * eb, 0x00020000);
+  auto drop = [&](const u32x4& x, int row, int q) __attribute__((always_inline)) {
+    const uint32_t at = q < qn ? (uint32_t)(row * outs + q) * eb : 0xFFFFFFFFu;
+    __builtin_amdgcn_raw_buffer_store_b128(x, to, at, 0, 0);
+  };
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     const int p16 = wp + 16 * j;
-    if (p16 >= pn) break;
+    if (!MANY && p16 >= pn) break;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) turn[r16 * 16 + ((4 * i + q4) ^ r16)] = acc[i][j];
     __builtin_amdgcn_wave_barrier();
@@ -528,8 +591,12 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       for (int k = 0; k < 4; ++k) {
         const int row = 4 * k + q4, q = wq + 4 * r16;
         v4f v = turn[row * 16 + (r16 ^ row)];
+        if constexpr (MANY) {
+          drop(__builtin_bit_cast(u32x4, v), p16 + row, q);
+          continue;
+        }
         if (p16 + row >= pn || q >= qn) continue;
-        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(out) + (row0 + p16 + row) * outs + q0 + q);
+        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(out) + (row0 + p16 + row) * outs + q00 + q);
         if (add) v += *o;
         store(v, o, past);
       }
@@ -538,20 +605,26 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       for (int k = 0; k < 2; ++k) {
         const int row = 8 * k + (lane >> 3), c = 2 * (lane & 7), q = wq + 4 * c;
         v4f v = turn[row * 16 + (c ^ row)], w = turn[row * 16 + ((c + 1) ^ row)];
-        if (p16 + row >= pn || q >= qn) continue;  // (a multiple of 8 columns exist)
-        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + (row0 + p16 + row) * outs + q0 + q);
-        if (add) {
+        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + (row0 + p16 + row) * outs + q00 + q);
+        const bool there = p16 + row < pn && q < qn;  // (a multiple of 8 columns exist)
+        if (add && there) {
           const u32x4 b = *o;
           v += v4f{u2f(b[0] << 16), u2f(b[0] & 0xFFFF0000u), u2f(b[1] << 16), u2f(b[1] & 0xFFFF0000u)};
           w += v4f{u2f(b[2] << 16), u2f(b[2] & 0xFFFF0000u), u2f(b[3] << 16), u2f(b[3] & 0xFFFF0000u)};
         }
         const u32x4 x = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16),
                          bf16_bits(w[0]) | (bf16_bits(w[1]) << 16), bf16_bits(w[2]) | (bf16_bits(w[3]) << 16)};
-        store(x, o, past);
+        if constexpr (MANY) drop(x, p16 + row, q);
+        else if (there) store(x, o, past);
       }
     }
     __builtin_amdgcn_wave_barrier();
   }
+  if constexpr (MANY) stores = f32 ? 4 * NP : 2 * NP;
+  if (!again) break;
+  }
+  // (no load into LDS is left behind when the wave ends)
+  if constexpr (MANY) wait_loads(stores);
 }
 
 // The sum of the parts, in order: eight outputs per thread.  Rows of no expert
@@ -777,16 +850,17 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB>
+template <int FORM, int GRAN, int P, int Q, int WP, int WQ, int NB, int MANY = 0>
 hipError_t launch_tile(const GroupedArgs& args, hipStream_t s) {
-  const long long outs = FORM == NT ? args.N : args.K, nq = (outs + Q - 1) / Q;
+  const long long outs = FORM == NT ? args.N : args.K;
+  const long long nq = MANY ? ((outs + Q - 1) / Q + args.many - 1) / args.many : (outs + Q - 1) / Q;
   const long long most = args.E < args.M ? args.E : args.M;  // experts with rows
   const long long tiles = FORM == TN ? (long long)args.E * ((args.N + P - 1) / P) * nq : (args.M / P + most) * nq;
   GroupedArgs a = args;
   a.group = (int)(tiles >= 256 ? 32 : (tiles + 7) / 8);
   const long long round = 8 * a.group;  // (tile_of)
   const dim3 grid((unsigned)((tiles + round - 1) / round * round), a.parts);
-  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB>), grid, dim3(WP * WQ * 64), 0, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB, MANY>), grid, dim3(WP * WQ * 64), 0, s, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.parts == 1) return err;
   const long long n = (FORM == TN ? (long long)a.E * a.N : a.M) * outs / 8;
@@ -799,6 +873,10 @@ hipError_t launch_form(const GroupedArgs& a, const GroupedPlan& plan, hipStream_
   if constexpr (FORM == NT) {
     if (plan.few == 1) return launch_few<GRAN, 2, 1, GRAN ? 1 : 3>(a, s);
     if (plan.few == 2) return launch_few<GRAN, 2, 2, GRAN ? 1 : 3>(a, s);
+  }
+  if constexpr (GRAN == 0 && FORM != TN) {
+    if (plan.many > 0 && (FORM == NT ? a.K : a.N) <= kS) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 1, 2>(a, s);
+    if (plan.many > 0) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2, 1>(a, s);
   }
   if (plan.tile == 256) return launch_tile<FORM, GRAN, 256, 256, 2, 4, GRAN ? 2 : 3>(a, s);
   if constexpr (FORM != TN) {
@@ -833,13 +911,26 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
     const long long n = (M + P / 2 * most) / P, rows = form == TN ? E * ((N + P - 1) / P) : n > most ? n : most;
     return rows * ((outs + Q - 1) / Q);
   };
-  GroupedPlan p{0, 128, 1};
+  GroupedPlan p{0, 128, 1, 0};
   if (form == TN) {
     if (N > 128 && K > 128 && tiles(256, 256) >= 256) p.tile = 256;
   } else {
     if (form == NT && M <= (gran ? 16 : 6) * most) p.few = 1;
     else if (form == NT && M <= 12 * most) p.few = 2;
     if (p.few) return p;
+  }
+  // Short sums: several tiles per workgroup, so that there are about 768 (three per
+  // CU), and for one stage this form in any case.  64 experts, bfloat16, N = 32, K =
+  // 6144, dx of 4000 rows 45 -> 21 us (512 workgroups 24 us, 1024 22 us); two stages,
+  // N = 128, K = 4096, float32: 37 -> 28 us.
+  const long long stages = stages_of(form, M, E, N, K);
+  if (form != TN && gran == 0 && stages <= 2) {
+    const long long n = tiles(64, 128) / 768;
+    p.many = n > 8 ? 8 : n > 1 || stages == 2 ? (int)n : 1;
+    if (p.many > 1 || stages == 1) return p;
+  }
+  p.many = 0;
+  if (form != TN) {
     if (tiles(256, 256) >= 256 && outs > 128 && (gran == 0 || M >= 192 * most)) p.tile = 256;
     else if (tiles(128, 128) >= 256 && (gran == 0 || M >= 96 * most)) p.tile = 128;
     else p.tile = 64;
@@ -847,7 +938,6 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
   const long long n = p.tile == 256 ? tiles(256, 256) : p.tile == 128 ? tiles(128, 128) : tiles(64, 128);
   p.parts = (int)most_parts(form, M, E, N, K);  // (1 without rows)
   if (p.parts > 512 / n) p.parts = (int)(512 / n);
-  const long long stages = stages_of(form, M, E, N, K);
   if (n >= 256 || p.parts < 2 || stages * (p.parts - 1) < 18 * p.parts) p.parts = 1;
   return p;
 }
@@ -875,6 +965,7 @@ hipError_t launch_grouped(const GroupedArgs& args, int form, hipStream_t s) {
   const long long outs = form == TN ? (long long)a.E * a.N * a.K : (long long)a.M * (form == NT ? a.N : a.K);
   a.stream = outs * (a.out_f32 ? 4 : 2) > (256LL << 20);
   a.parts = plan.parts;
+  a.many = plan.many;
   if (form == TN) return launch_form<TN, 0>(a, plan, s);
   if (a.gran == 16) return form == NT ? launch_form<NT, 16>(a, plan, s) : launch_form<NN, 16>(a, plan, s);
   if (a.gran == 32) return form == NT ? launch_form<NT, 32>(a, plan, s) : launch_form<NN, 32>(a, plan, s);

@@ -213,7 +213,7 @@ struct GroupedArgs {
   int gran;           // 0: bfloat16 weights; 16, 32: FP4 (w, w_sf, w_gs in place of q)
   int out_f32, accumulate;
   int stream;         // the output is larger than the caches (set by launch_grouped, as parts is)
-  int parts, group;   // of every sum; consecutive tiles per XCD
+  int parts, group, many;  // of every sum; consecutive tiles per XCD; tiles per workgroup
   float* part;        // [parts][outputs] where parts > 1
   const uint16_t *p, *q;
   const uint8_t *w, *w_sf;
@@ -222,9 +222,9 @@ struct GroupedArgs {
   void* out;
 };
 // The form of a product: few 1, 2: the stream of the weights with 16 or 32 rows
-// per workgroup; else tiles of tile x tile outputs (64: 64 x 128), the sums in
-// parts.
-struct GroupedPlan { int few, tile, parts; };
+// per workgroup; else many > 0: so many tiles of 64 x 128 per workgroup, or tiles
+// of tile x tile outputs (64: 64 x 128), the sums in parts.
+struct GroupedPlan { int few, tile, parts, many; };
 GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long long K, int gran);
 // The most floats that the parts of M or fewer rows take.
 long long grouped_part_floats(int form, long long M, long long E, long long N, long long K);

@@ -127,6 +127,8 @@ SHAPES = [([1], 8, 32), ([1], 4096, 2080), ([3, 0, 2], 24, 96), ((8, 64), 520, 2
           ([17, 0, 1, 33], 136, 320), ([0, 300, 0], 1000, 704), ((700, 3), 1096, 224), ([63, 64, 65, 1], 256, 128),
           ([127, 128, 129, 0], 384, 64), ([255, 256, 257], 648, 96), ((1500, 12), 2056, 512), ([2100, 2000], 4104, 96),
           ((4000, 64), 32, 512), ((4000, 64), 512, 32), ([1000], 16, 2048), ([60], 2048, 4096),
+          # short sums, many tiles per workgroup
+          ((4000, 64), 72, 2080), ((4000, 64), 2056, 96), ((2000, 130), 1096, 128),
           # sums in parts: few tiles, long sums; fewer stages than parts in one expert
           ([5000], 64, 256), ([1300, 0, 20], 1320, 1184), ([33], 1096, 2080)]
 
