@@ -671,32 +671,40 @@ def grouped_dw(dy, x, offsets, out=None, accumulate=False, workspace=None, strea
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_problem(*fields):
+    return ctypes.byref(Norm(*fields))
+
+
 def _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream):
-    """(problem, device, addresses of y, post_w, gate and pre_w) of a block norm whose residual stream's type and
-    sizes are those of ``first``."""
+    """((T, H), gate kind, problem, device, addresses of y, post_w, gate and pre_w) of a block norm whose residual
+    stream's type and sizes are those of ``first``."""
     import torch
-    bf, some = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    T, H = _dims(first, name, some, 2)
+    bf, f32, some = (torch.bfloat16,), torch.float32, (torch.bfloat16, torch.float32)
+    T, H = shape = _dims(first, name, some, 2)
     dev = _current(first, stream)
     if y is None and (post_w is not None or gate is not None):
         raise ValueError("post_w and gate go with y")
     if y is None and pre_w is None:
         raise ValueError("y or pre_w is needed")
-    if gate_act not in (None, "sigmoid"):
+    if gate_act is not None and gate_act != "sigmoid":
         raise ValueError(f"gate_act must be None or 'sigmoid', got {gate_act!r}")
-    kind, gate_at = 0, None
+    kind, gate_at, gate_fmt = 0, None, OUT_BF16
     if gate is not None:
         _dev(gate, "gate", some)
         # (a gate of T = H elements is one per channel; [T, 1] says per token)
-        shapes = ((H,), (T,), (T, 1), (T, H)) if H != 1 else ((H,),)
-        if tuple(gate.shape) not in shapes:
-            raise ValueError(f"gate must have shape {(H,)}, {(T,)}, {(T, 1)} or {(T, H)}, got {tuple(gate.shape)}")
-        kind = (1, 2, 2, 3)[shapes.index(tuple(gate.shape))]
-        gate_at = _arg(gate, "gate", some, gate.shape, dev)
-    f32 = lambda t: OUT_F32 if t is not None and t.dtype is torch.float32 else OUT_BF16
-    at = (_arg(y, "y", bf, (T, H), dev), _arg(post_w, "post_w", some, (H,), dev), gate_at,
+        size = tuple(gate.shape)
+        kind = 1 if size == (H,) else 2 if size == (T,) or size == (T, 1) else 3 if size == (T, H) else 0
+        if kind == 0:
+            raise ValueError(f"gate must have shape {(H,)}, {(T,)}, {(T, 1)} or {(T, H)}, got {size}")
+        gate_at, gate_fmt = _arg(gate, "gate", some, gate.shape, dev), OUT_F32 if gate.dtype is f32 else OUT_BF16
+    at = (_arg(y, "y", bf, shape, dev), _arg(post_w, "post_w", some, (H,), dev), gate_at,
           _arg(pre_w, "pre_w", some, (H,), dev))
-    return Norm(T, H, f32(first), f32(post_w), f32(pre_w), f32(gate), kind, 1 if gate_act else 0, scale, h_scale, eps), dev, at
+    problem = _norm_problem(T, H, OUT_F32 if first.dtype is f32 else OUT_BF16,
+                            OUT_F32 if post_w is not None and post_w.dtype is f32 else OUT_BF16,
+                            OUT_F32 if pre_w is not None and pre_w.dtype is f32 else OUT_BF16, gate_fmt, kind,
+                            0 if gate_act is None else 1, scale, h_scale, eps)
+    return shape, kind, problem, dev, at
 
 
 def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_scale=1.0, pre_w=None, eps=1e-6,
@@ -710,9 +718,7 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
     place).  Returns (h', n): h' of h's type, n [T, H] bfloat16.  Without y h' is h
     itself; without pre_w n is None."""
     import torch
-    p, dev, (y_at, post_at, gate_at, pre_at) = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps,
-                                                          stream)
-    shape = (p.T, p.H)
+    shape, _, problem, dev, at = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
     if y is None and h_out is not None:
         raise ValueError("h_out goes with y")
     if pre_w is None and n is not None:
@@ -721,8 +727,7 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
         h_out = _empty(h, shape, h.dtype, stream)
     if pre_w is not None and n is None:
         n = _empty(h, shape, torch.bfloat16, stream)
-    _check(lib().moe_fp4_block_norm(ctypes.byref(p), h.data_ptr(), y_at, post_at, gate_at, pre_at,
-                                    _arg(h_out, "h_out", (h.dtype,), shape, dev),
+    _check(lib().moe_fp4_block_norm(problem, h.data_ptr(), *at, _arg(h_out, "h_out", (h.dtype,), shape, dev),
                                     _arg(n, "n", (torch.bfloat16,), shape, dev), _raw_stream(stream, dev)))
     return (h if y is None else h_out), n
 
@@ -740,8 +745,8 @@ def block_norm_grad(dh, dn, h, y=None, post_w=None, gate=None, gate_act=None, sc
     if (pre_w is None) != (dn is None) or (pre_w is None) != (h is None):
         raise ValueError("dn and h go with pre_w")
     first, name = (h, "h") if h is not None else (dh, "dh")
-    p, dev, at = _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
-    T, H = shape = (p.T, p.H)
+    shape, kind, problem, dev, at = _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
+    T, H = shape
     need = _norm_grad_need(T, H)
     own = (first.dtype,)
     dh_at, dn_at, h_at = _arg(dh, "dh", own, shape, dev), _arg(dn, "dn", (torch.bfloat16,), shape, dev), None
@@ -751,10 +756,10 @@ def block_norm_grad(dh, dn, h, y=None, post_w=None, gate=None, gate_act=None, sc
         d_h = _empty(first, shape, first.dtype, stream)
     new = lambda like, size, dtype: None if like is None else _empty(first, size, dtype, stream)
     d_y, d_post, d_pre = new(y, shape, torch.bfloat16), new(post_w, (H,), torch.float32), new(pre_w, (H,), torch.float32)
-    d_gate = None if gate is None else new(gate, tuple(gate.shape), gate.dtype if p.gate_kind == 3 else torch.float32)
+    d_gate = None if gate is None else new(gate, tuple(gate.shape), gate.dtype if kind == 3 else torch.float32)
     ws = _scratch(workspace, need, first, stream)
     ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib().moe_fp4_block_norm_grad(ctypes.byref(p), dh_at, dn_at, h_at, *at, _arg(d_h, "d_h", own, shape, dev),
+    _check(lib().moe_fp4_block_norm_grad(problem, dh_at, dn_at, h_at, *at, _arg(d_h, "d_h", own, shape, dev),
                                          ptr(d_y), ptr(d_post), ptr(d_gate), ptr(d_pre), ws.data_ptr(), ws.numel(),
                                          _raw_stream(stream, dev)))
     return d_h, d_y, d_post, d_gate, d_pre

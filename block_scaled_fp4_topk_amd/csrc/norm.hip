@@ -251,27 +251,42 @@ __global__ __launch_bounds__(MOST) void block_norm_grad_kernel(NormArgs a) {
     p[0] += v4f{v[0], v[1], v[2], v[3]};
     p[MOST] += v4f{v[4], v[5], v[6], v[7]};
   };
-  for (long long t = first; t < a.T; t += step) {
-    const size_t row = (size_t)t * H;
+  // A row's values; the next row's are asked for before this one's sums.
+  struct Row {
     Eight<F32> h[C], d[C];
     Eight<false> y[C], dn[C];
-    float ss[3] = {0.0f, 0.0f, 0.0f};
+  } ahead;
+  auto load = [&](long long t) __attribute__((always_inline)) {
+    const size_t row = (size_t)t * H;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int at = (c * tpr + tid) * 8;
-      h[c].zero();
-      d[c].zero();
-      y[c].zero();
-      dn[c].zero();
+      ahead.h[c].zero();
+      ahead.d[c].zero();
+      ahead.y[c].zero();
+      ahead.dn[c].zero();
       if (at < H) {
         if (a.pre_w) {
-          h[c].load(a.h, row + at);
-          dn[c].load(a.dn, row + at);
+          ahead.h[c].load(a.h, row + at);
+          ahead.dn[c].load(a.dn, row + at);
         }
-        if (KIND >= 0) y[c].load(a.y, row + at);
-        if (a.dh) d[c].load(a.dh, row + at);
+        if (KIND >= 0) ahead.y[c].load(a.y, row + at);
+        if (a.dh) ahead.d[c].load(a.dh, row + at);
       }
     }
+  };
+  // (512 threads: two workgroups per CU without it take 133 us for 8192 rows of 4096,
+  // float32, one with it 157 us; 1024 threads have too few registers)
+  constexpr bool kAhead = MOST == 768 || MOST == 256;
+  if (kAhead && first < a.T) load(first);
+  for (long long t = first; t < a.T; t += step) {
+    const size_t row = (size_t)t * H;
+    if (!kAhead) load(t);
+    const Row now = ahead;
+    if (kAhead && t + step < a.T) load(t + step);
+    const Eight<F32>(&h)[C] = now.h, (&d)[C] = now.d;
+    const Eight<false>(&y)[C] = now.y, (&dn)[C] = now.dn;
+    float ss[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int at = (c * tpr + tid) * 8;
@@ -551,22 +566,27 @@ __global__ __launch_bounds__(1024) void block_norm_grad_wide_kernel(NormArgs a) 
 }
 
 // The sums over the parts, in order: 64 columns per workgroup, the parts split
-// over its 4 waves.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, int parts) {
-  __shared__ float s[4][64];
+// over its 16 waves.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int parts) {
+  __shared__ float s[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kind = blockIdx.y;
   float* out = kind == 0 ? a.d_pre_w : kind == 1 ? a.d_post_w : a.gate_kind == 1 ? static_cast<float*>(a.d_gate) : nullptr;
   if (!out) return;
-  const int c = blockIdx.x * 64 + lane, per = (parts + 3) / 4;
+  const int c = blockIdx.x * 64 + lane, per = (parts + 15) / 16;
   float v = 0.0f;
   if (c < a.H) {
     const float* p = a.part + (size_t)kind * parts * a.H + c;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = wave * per; i < min(parts, (wave + 1) * per); ++i) v += p[(size_t)i * a.H];
   }
   s[wave][lane] = v;
   __syncthreads();
-  if (wave == 0 && c < a.H) out[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+  if (wave == 0 && c < a.H) {
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v += s[w][lane];
+    out[c] = v;
+  }
 }
 
 // Rows of up to 512 elements: a wave each.  Beyond, a workgroup of as many waves
@@ -617,9 +637,12 @@ hipError_t launch(const NormArgs& a, int parts, hipStream_t s) {
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) { return launch(a, 0, s); }
 
+// As many workgroups as the chip holds at a time, so that the parts of the sums
+// over rows are few (8192 x 6144, float32: 256 of them 235 us, 512 242 us).
 int norm_grad_parts(long long T, int H) {
   if (H <= 512) return (int)(T < 4096 ? (T + 3) / 4 * 4 : 4096);
-  const long long most = 256 * (2048 / threads_of(H, H <= 8192 ? 1 : 2));
+  const int waves = threads_of(H, H <= 8192 ? 1 : 2) / 64;
+  const long long most = 256 * (waves > 8 ? 1 : waves > 4 ? 2 : 12 / waves);
   return (int)(T < most ? T : most);
 }
 
@@ -630,7 +653,7 @@ hipError_t launch_block_norm_grad(const NormArgs& a, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   if (a.pre_w || a.post_w || a.gate_kind == 1)
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((a.H + 63) / 64, 3), dim3(256), 0, s, a, parts);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((a.H + 63) / 64, 3), dim3(1024), 0, s, a, parts);
   return hipGetLastError();
 }
 
