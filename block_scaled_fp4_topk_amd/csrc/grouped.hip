@@ -101,16 +101,20 @@ __device__ __forceinline__ Rows rows_of(const int32_t* offsets, int E, int M, in
 
 // 16-byte segment s of LDS row r (128 bytes) sits at s ^ pswz(r).
 __device__ __forceinline__ int pswz(int r) { return (r >> 1) & 7; }
-// 32-byte chunk c of LDS row r (an element of the sum) sits at c ^ tswz(r): the
-// 8 rows that 32 lanes of a transposing read take lie in different banks.
-__device__ __forceinline__ int tswz(int r) { return (r & 3) | ((r >> 1) & 4); }
+// 32-byte chunk c of LDS row r (an element of the sum; BYTES long) sits at c ^
+// tswz(r): the 8 rows that 32 lanes of a transposing read take lie in different
+// banks.
+template <int BYTES>
+__device__ __forceinline__ int tswz(int r) {
+  static_assert(BYTES >= 128, "four chunks at least");
+  return BYTES >= 256 ? (r & 3) | ((r >> 1) & 4) : ((r >> 1) & 1) | ((r >> 2) & 2);
+}
 
 // One operand's stage: SIZE rows of kS elements along the sum (TR = false), or
 // kS rows of SIZE elements (TR: across it; read by the transposing LDS reads).
 // NTH threads load it, 16 bytes per lane straight to LDS.
 template <bool TR, int SIZE, int NTH>
 struct Operand {
-  static_assert(!TR || SIZE >= 128, "tswz swaps the chunks of 256 bytes");
   static constexpr int kPieces = SIZE * 8 / NTH;
   static constexpr int kBytes = SIZE * kS * 2;
   const uint8_t* base;  // uniform
@@ -127,7 +131,7 @@ struct Operand {
   }
   __device__ __forceinline__ static int col(int i) {
     const int lane = threadIdx.x & 63, r = row(i);
-    if constexpr (TR) return (((lane % (SIZE / 8) >> 1) ^ tswz(r)) << 4) + ((lane & 1) << 3);
+    if constexpr (TR) return (((lane % (SIZE / 8) >> 1) ^ tswz<SIZE * 2>(r)) << 4) + ((lane & 1) << 3);
     else return ((lane & 7) ^ pswz(r)) << 3;
   }
 
@@ -178,7 +182,7 @@ struct Operand {
     const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
     if constexpr (TR) {
       const int r = 8 * q + (r16 >> 2);
-      return r * (SIZE * 2) + ((tswz(r) ^ (w0 >> 4)) << 5) + ((r16 & 3) << 3);
+      return r * (SIZE * 2) + ((tswz<SIZE * 2>(r) ^ (w0 >> 4)) << 5) + ((r16 & 3) << 3);
     } else {
       return (w0 + r16) * 128 + ((q ^ pswz(r16)) << 4);
     }
@@ -286,7 +290,7 @@ struct Fp4Operand : Operand<TR, SIZE, NTH> {
     // (TR: pieces 256 bytes apart write the two halves of a chunk in turn, so that
     // 16 lanes write to all 64 banks)
     const bool swap = TR && (piece & 4);
-    uint32_t at = TR ? row * (SIZE * 2) + ((2 * piece ^ tswz(row)) << 5) + (swap ? 16 : 0) : row * 128 + ((4 * piece ^ pswz(row)) << 4);
+    uint32_t at = TR ? row * (SIZE * 2) + ((2 * piece ^ tswz<SIZE * 2>(row)) << 5) + (swap ? 16 : 0) : row * 128 + ((4 * piece ^ pswz(row)) << 4);
     asm volatile("" : "+v"(at));
     u32x4 v;
     const uint32_t codes = swap ? c[j ^ 1] : c[j];
@@ -879,9 +883,10 @@ hipError_t launch_form(const GroupedArgs& a, const GroupedPlan& plan, hipStream_
     if (plan.many > 0) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2, 1>(a, s);
   }
   if (plan.tile == 256) return launch_tile<FORM, GRAN, 256, 256, 2, 4, GRAN ? 2 : 3>(a, s);
-  if constexpr (FORM != TN) {
-    if (plan.tile == 64) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
+  if constexpr (FORM == TN) {
+    if (plan.tile == 64 && a.N > 64) return launch_tile<FORM, GRAN, 128, 64, 4, 1, 2>(a, s);
   }
+  if (plan.tile == 64) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
   return launch_tile<FORM, GRAN, 128, 128, 2, 2, GRAN || FORM == TN ? 2 : 3>(a, s);
 }
 
@@ -914,6 +919,7 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
   GroupedPlan p{0, 128, 1, 0};
   if (form == TN) {
     if (N > 128 && K > 128 && tiles(256, 256) >= 256) p.tile = 256;
+    else if (N <= 64 || K <= 64) p.tile = 64;  // (a low-rank factor's: 4000 rows, 64 experts, 32 x 6144 28 -> 21 us)
   } else {
     if (form == NT && M <= (gran ? 16 : 6) * most) p.few = 1;
     else if (form == NT && M <= 12 * most) p.few = 2;
@@ -935,7 +941,7 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
     else if (tiles(128, 128) >= 256 && (gran == 0 || M >= 96 * most)) p.tile = 128;
     else p.tile = 64;
   }
-  const long long n = p.tile == 256 ? tiles(256, 256) : p.tile == 128 ? tiles(128, 128) : tiles(64, 128);
+  const long long n = p.tile == 256 ? tiles(256, 256) : p.tile == 128 || form == TN ? tiles(128, 128) : tiles(64, 128);
   p.parts = (int)most_parts(form, M, E, N, K);  // (1 without rows)
   if (p.parts > 512 / n) p.parts = (int)(512 / n);
   if (n >= 256 || p.parts < 2 || stages * (p.parts - 1) < 18 * p.parts) p.parts = 1;
@@ -947,7 +953,7 @@ long long grouped_part_floats(int form, long long M, long long E, long long N, l
   const long long parts = most_parts(form, M, E, N, K);
   if (parts < 2) return 0;
   if (form == TN) {
-    const long long n = E * ((N + 127) / 128) * nq;
+    const long long n = E * ((N + 127) / 128) * nq;  // (N or K <= 64: tiles of 64 are as many)
     return n >= 256 ? 0 : (parts < 512 / n ? parts : 512 / n) * E * N * K;
   }
   // (fewer than 256 tiles have no more rows than this: one expert per tile at
