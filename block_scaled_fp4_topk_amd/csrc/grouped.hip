@@ -43,8 +43,8 @@ __device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
 // ---------------------------------------------------------------------------
 // tiles
 
-// The place of workgroup b among the tiles: groups of up to 32 consecutive tiles
-// per XCD in turn (an XCD's 32 CUs share an L2).
+// The place of workgroup b among the tiles: groups of consecutive tiles per XCD in
+// turn (an XCD's 32 CUs share an L2).
 __device__ __forceinline__ int tile_of(int b, int group) {
   const int i = b >> 3, g = i / group;
   return (g * 8 + (b & 7)) * group + i - g * group;
@@ -861,7 +861,11 @@ hipError_t launch_tile(const GroupedArgs& args, hipStream_t s) {
   const long long most = args.E < args.M ? args.E : args.M;  // experts with rows
   const long long tiles = FORM == TN ? (long long)args.E * ((args.N + P - 1) / P) * nq : (args.M / P + most) * nq;
   GroupedArgs a = args;
-  a.group = (int)(tiles >= 256 ? 32 : (tiles + 7) / 8);
+  // Consecutive tiles per XCD.  dW of 16 experts of 16384 rows, N = 4096, K = 6144: 32
+  // 926 us, 16 901, 4 898, 1 907 (64 experts of 8000 rows: 32 1082 us, 4 1063).  The
+  // other forms: 32 the best or within 1% of it (8 experts of 16384 rows: 718 us, 4 748).
+  const int most_group = FORM == TN ? 4 : 32;
+  a.group = (int)(tiles >= 8 * most_group ? most_group : (tiles + 7) / 8);
   const long long round = 8 * a.group;  // (tile_of)
   const dim3 grid((unsigned)((tiles + round - 1) / round * round), a.parts);
   hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB, MANY>), grid, dim3(WP * WQ * 64), 0, s, a);
