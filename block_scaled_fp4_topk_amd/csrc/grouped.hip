@@ -417,7 +417,7 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
 
   v4f acc[NQ][NP];
   // Half of the row tiles at a time (a phase): 16 products per wave at 128 x 64.
-  constexpr int NH = NP / 2;
+  constexpr int NH = NP / 2, kLess = NH > 2 ? NH / 2 : NH;
   u32x4 fq[2][NQ], fp[2][NH];
   const uint32_t at_q = OpQ::lane_at(wq) + lds_address(s_q), at_p = OpP::lane_at(wp) + lds_address(s_p);
   auto read_q = [&](uint32_t buf, int ks) __attribute__((always_inline)) {
@@ -426,20 +426,20 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
 #pragma unroll
     for (int i = 0; i < NQ; ++i) fq[ks][i] = OpQ::frag(at, i, ks);
   };
-  auto read_p = [&](uint32_t buf, int ks, int h) __attribute__((always_inline)) {
+  auto read_p = [&](uint32_t buf, int ks, int h, int n) __attribute__((always_inline)) {
     uint32_t at = at_p + buf;
     asm volatile("" : "+v"(at));
 #pragma unroll
-    for (int j = 0; j < NH; ++j) fp[h][j] = OpP::frag(at, NH * h + j, ks);
+    for (int j = 0; j < n; ++j) fp[h][j] = OpP::frag(at, NH * h + j, ks);
   };
   auto multiply_one = [&](int ks, int h, int j, int i) __attribute__((always_inline)) {
     v4f& c = acc[i][NH * h + j];
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fq[ks][i]), __builtin_bit_cast(v8bf, fp[h][j]), c, 0,
                                                 0, 0);
   };
-  auto multiply = [&](int ks, int h) __attribute__((always_inline)) {
+  auto multiply = [&](int ks, int h, int n) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NH; ++j)
+    for (int j = 0; j < n; ++j)
 #pragma unroll
       for (int i = 0; i < NQ; ++i) multiply_one(ks, h, j, i);
     __builtin_amdgcn_sched_barrier(0);
@@ -462,33 +462,36 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   };
   uint32_t pb = 0, qb = 0;  // where the stage at hand lies
   auto next_q = [](uint32_t b) __attribute__((always_inline)) { return b + OpQ::kBytes == NB * OpQ::kBytes ? 0 : b + OpQ::kBytes; };
-  // HALVES: of a wave's row tiles, those that exist.  Others are neither read nor
-  // multiplied, so that an expert's short last tile takes as much less time.
-  auto stages = [&](auto HALVES) __attribute__((always_inline)) {
-    constexpr bool some = HALVES.value > 0, both = HALVES.value > 1;
+  // TILES: of a wave's row tiles, those that exist (by halves; by quarters of 8).
+  // Others are neither read nor multiplied, so that an expert's short last tile takes
+  // as much less time (halves of 8 only, 16384 rows of 64 experts, N = 4096, K = 6144:
+  // 1050 us, quarters 1031; dx 1020 and 1000; of 4: quarters gain nothing).
+  auto stages = [&](auto TILES) __attribute__((always_inline)) {
+    constexpr int n0 = TILES.value < NH ? TILES.value : NH, n1 = TILES.value - n0;  // the phases' halves
+    constexpr bool some = n0 > 0, both = n1 > 0;
     // A stage in four phases: the operands of a phase come while the one before
     // multiplies.  The one barrier lies before the last phase, whose operands are
     // in registers: behind it the next stage's first operands are read, and the
     // loads of a later stage go between the products.
     auto three = [&]() __attribute__((always_inline)) {
-      if constexpr (both) read_p(pb, 0, 1);
+      if constexpr (both) read_p(pb, 0, 1, n1);
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (some) {
-        multiply(0, 0);
+        multiply(0, 0, n0);
         read_q(qb, 1);
-        read_p(pb, 1, 0);
+        read_p(pb, 1, 0, n0);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (both) {
-        multiply(0, 1);
-        read_p(pb, 1, 1);
+        multiply(0, 1, n1);
+        read_p(pb, 1, 1, n1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (some) multiply(1, 0);
+      if constexpr (some) multiply(1, 0, n0);
     };
     if constexpr (some) {
       read_q(0, 0);
-      read_p(0, 0, 0);
+      read_p(0, 0, 0, n0);
     }
     for (int s = s0; MANY < 2 && s < s1 - 1; ++s) {
       three();
@@ -498,10 +501,10 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       handover(s + 2 == s1, pb, qb);
       if constexpr (some) {
         read_q(qb, 0);
-        read_p(pb, 0, 0);
+        read_p(pb, 0, 0, n0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      constexpr int pieces = OpP::kPieces + OpQ::kPieces, n = both ? NH * NQ : 1;
+      constexpr int pieces = OpP::kPieces + OpQ::kPieces, n = both ? n1 * NQ : 1;
       uint8_t* lds_q = s_q + (kFar ? old_q : next_q(qb));
       const typename OpP::Stage sp = op.stage(s + 2, sum);
       const typename OpQ::Stage sq = oq.stage(s + (kFar ? 3 : 2), sum);
@@ -517,7 +520,7 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       }
     }
     three();
-    if constexpr (both) multiply(1, 1);
+    if constexpr (both) multiply(1, 1, n1);
   };
   // The first stage's loads (the newest are the Q side's farthest stage).
   // (a lone stage's P side stays where it is)
@@ -548,8 +551,10 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       if constexpr (kFar) oq.load(s0 + 2, sum, s_q + 2 * OpQ::kBytes);
       else oq.load(s0 + 1, sum, s_q + OpQ::kBytes);
     }
-    if (FORM == TN || pn > wp + 16 * NH) stages(std::integral_constant<int, 2>{});
-    else if (pn > wp) stages(std::integral_constant<int, 1>{});
+    if (FORM == TN || pn > wp + 16 * (NP - kLess)) stages(std::integral_constant<int, NP>{});
+    else if (kLess < NH && pn > wp + 16 * NH) stages(std::integral_constant<int, kLess < NH ? NP - kLess : 0>{});
+    else if (pn > wp + 16 * (NH - kLess)) stages(std::integral_constant<int, NH>{});
+    else if (kLess < NH && pn > wp) stages(std::integral_constant<int, kLess < NH ? NH - kLess : 0>{});
     else stages(std::integral_constant<int, 0>{});
   }
   if constexpr (GRAN != 0) {
