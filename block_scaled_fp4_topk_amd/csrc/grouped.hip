@@ -34,6 +34,15 @@ __device__ __forceinline__ void direct_load(const v4i& buffer, uint32_t off, uin
                : "memory");
 }
 
+// 2 (else 1) bytes per lane, to a word each.
+template <bool TWO>
+__device__ __forceinline__ void direct_load_small(const v4i& buffer, uint32_t off, uint32_t uniform_off, const uint8_t* lds) {
+  typedef const __attribute__((address_space(3))) uint8_t* lds1;
+  const uint32_t to = (uint32_t)(uintptr_t)(lds1)lds;
+  if (TWO) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, %3 offen lds" : : "s"(to), "v"(off), "s"(buffer), "s"(uniform_off) : "memory");
+  else asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds" : : "s"(to), "v"(off), "s"(buffer), "s"(uniform_off) : "memory");
+}
+
 // A buffer descriptor: `bytes` from p on.
 __device__ __forceinline__ v4i buffer_of(const uint8_t* p, uint32_t bytes) {
   const uint64_t at = reinterpret_cast<uintptr_t>(p);
@@ -229,8 +238,9 @@ __device__ __forceinline__ u32x4 dq8_scaled_bf16(uint32_t codes, float scale) {
 
 // FP4 weights as such an operand: a thread takes the 16 bytes of 32 codes of a
 // row through registers, and decodes them to where the direct loads would have
-// put them, a stage after they were asked for.
-template <bool TR, int SIZE, int NTH, int GRAN>
+// put them, a stage after they were asked for.  FAR: with their scales through a
+// place of its own in LDS, two stages after.
+template <bool TR, int SIZE, int NTH, int GRAN, bool FAR>
 struct Fp4Operand : Operand<TR, SIZE, NTH> {
   static_assert(SIZE * kS == 32 * NTH, "32 codes per thread and stage");
   static constexpr bool kClear = true;
@@ -242,49 +252,72 @@ struct Fp4Operand : Operand<TR, SIZE, NTH> {
   }
   static constexpr int kPer = TR ? SIZE / 32 : 2;  // pieces of a row
   const uint8_t *codes, *sf;  // uniform
-  int K;
+  int K, rows;  // (rows: of the tile, !TR)
   uint32_t row_c, row_s;  // the thread's row (TR: column), in bytes
+  // FAR: two stages' codes and scales (a word each), in the order of the threads
+  static constexpr int kRing = FAR ? 2 * NTH * 20 : 16;
+  static constexpr int kAhead = FAR ? 2 : 1;
+  uint8_t* ring;
   u32x4 c;
   uint32_t s;
 
   // w, w_sf: the tile's first row (TR: of the whole sum) and column; valid rows (TR: columns)
-  __device__ __forceinline__ void init(const uint8_t* w, const uint8_t* w_sf, int k, int valid) {
+  __device__ __forceinline__ void init(const uint8_t* w, const uint8_t* w_sf, int k, int valid, uint8_t* place) {
+    ring = place;
     codes = w;
     sf = w_sf;
     K = k;
+    rows = min(valid, SIZE);
     const uint32_t r = TR ? min(32 * ((int)threadIdx.x % kPer), valid - 32) : min((int)threadIdx.x / kPer, valid - 1);
     row_c = TR ? r / 2 : r * (K / 2);
     row_s = TR ? r / GRAN : r * (K / GRAN);
   }
 
+  __device__ __forceinline__ uint8_t* slot(int st) const { return ring + (st & 1) * (kRing / 2); }
+
+  // Stage st of a sum of n elements asked for (behind the last stage: the last one
+  // again).  FAR: by two direct loads.
   __device__ __forceinline__ void fetch(int st, int n) {
+    const int at = min(st, (n - 1) / kS) * kS;
     const uint8_t *pc = codes, *ps = sf;
-    uint32_t oc, os;
+    uint32_t oc = row_c, os = row_s;
+    int left = rows;
     if (TR) {
-      pc += (size_t)st * kS * (K / 2);
-      ps += (size_t)st * kS * (K / GRAN);
-      const uint32_t r = min((int)threadIdx.x / kPer, n - 1 - st * kS);
-      oc = row_c + r * (K / 2);
-      os = row_s + r * (K / GRAN);
+      pc += (size_t)at * (K / 2);
+      ps += (size_t)at * (K / GRAN);
+      left = min(n - at, kS);
+      const uint32_t r = min((int)threadIdx.x / kPer, left - 1);
+      oc += r * (K / 2);
+      os += r * (K / GRAN);
     } else {
-      const uint32_t at = min(st * kS + 32 * ((int)threadIdx.x % kPer), n - 32);
-      oc = row_c + at / 2;
-      os = row_s + at / GRAN;
+      const uint32_t k = min(at + 32 * ((int)threadIdx.x % kPer), n - 32);
+      oc += k / 2;
+      os += k / GRAN;
     }
-    c = *reinterpret_cast<const u32x4*>(pc + oc);
-    if (GRAN == 16) s = *reinterpret_cast<const uint16_t*>(ps + os);
-    else s = ps[os];
+    if constexpr (FAR) {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      direct_load(buffer_of(pc, left * (K / 2)), oc, 0, slot(st) + wave * 1024);
+      direct_load_small<GRAN == 16>(buffer_of(ps, left * (K / GRAN)), os, 0, slot(st) + NTH * 16 + wave * 256);
+    } else {
+      c = *reinterpret_cast<const u32x4*>(pc + oc);
+      if (GRAN == 16) s = *reinterpret_cast<const uint16_t*>(ps + os);
+      else s = ps[os];
+    }
   }
 
-  // What was fetched into stage buffer lds, eight codes at a time, and then the
-  // next stage asked for (behind the last one: the last one again).
+  // What was fetched into stage buffer lds, eight codes at a time, and then a later
+  // stage asked for.
   static constexpr int kPieces = 5;
   struct Stage { int st, n; };
   __device__ __forceinline__ Stage stage(int st, int n) const { return {st, n}; }
   __device__ __forceinline__ void piece(const Stage& of, int j, uint8_t* lds) {
     if (j == 4) {
-      fetch(min(of.st + 1, (of.n - 1) / kS), of.n);
+      fetch(of.st + kAhead, of.n);
       return;
+    }
+    if (FAR && j == 0) {
+      c = *reinterpret_cast<const u32x4*>(slot(of.st) + threadIdx.x * 16);
+      s = *reinterpret_cast<const uint32_t*>(slot(of.st) + NTH * 16 + threadIdx.x * 4);
     }
     const int row = threadIdx.x / kPer, piece = threadIdx.x % kPer;
     // (TR: pieces 256 bytes apart write the two halves of a chunk in turn, so that
@@ -304,10 +337,10 @@ struct Fp4Operand : Operand<TR, SIZE, NTH> {
   }
 };
 
-template <bool TR, int SIZE, int NTH, int GRAN>
-struct WeightOperand { typedef Fp4Operand<TR, SIZE, NTH, GRAN> type; };
-template <bool TR, int SIZE, int NTH>
-struct WeightOperand<TR, SIZE, NTH, 0> { typedef Operand<TR, SIZE, NTH> type; };
+template <bool TR, int SIZE, int NTH, int GRAN, bool FAR>
+struct WeightOperand { typedef Fp4Operand<TR, SIZE, NTH, GRAN, FAR> type; };
+template <bool TR, int SIZE, int NTH, bool FAR>
+struct WeightOperand<TR, SIZE, NTH, 0, FAR> { typedef Operand<TR, SIZE, NTH> type; };
 
 // A store, past the caches if asked for.  (The empty asm keeps the compiler from
 // making one ordinary store of the two.)
@@ -332,6 +365,14 @@ __device__ __forceinline__ void wait_all() {
   asm volatile("" ::: "memory");
 }
 
+// The wave's own loads but the LEFT newest.
+template <int LEFT>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
 // Every wave's loads but the `left` (0, 4, 8 or 16) newest accesses done, and a barrier.
 __device__ __forceinline__ void wait_loads(int left) {
   if (left == 0) wait_all<0>();
@@ -346,8 +387,8 @@ __device__ __forceinline__ void wait_loads(int left) {
 // P x Q outputs per workgroup: P along the rows (TN: along N), Q along the
 // output's contiguous side; WP x WQ waves.  blockIdx.y: the part of the sum (more
 // than one: to a.part as float32, which grouped_sum adds up).  GRAN: 0, or FP4 weights' group.  NB:
-// stages of the Q side in LDS (of the P side 2): where the weights come from HBM,
-// two stages of them in flight.  MANY: a workgroup takes a.many tiles next to each
+// 3 where the Q side is asked for two stages ahead (in LDS bfloat16 has three then, the
+// P side two), else 2.  MANY: a workgroup takes a.many tiles next to each
 // other along Q, the first loads of one on their way while the one before is
 // stored: for short sums, where finding the expert and waiting for a lone stage is
 // most of a tile's time.  (2: sums of one stage, whose room is that of one.)
@@ -356,9 +397,12 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   constexpr int NTH = WP * WQ * 64;
   constexpr int NP = P / WP / 16, NQ = Q / WQ / 16;  // a wave's 16-row tiles
   typedef Operand<FORM == TN, P, NTH> OpP;
-  typedef typename WeightOperand<FORM != NT, Q, NTH, GRAN>::type OpQ;
-  constexpr bool kFar = GRAN == 0 && NB == 3;  // the Q side's loads run two stages ahead, else one
-  __shared__ __attribute__((aligned(4096))) uint8_t s_p[(MANY == 2 ? 1 : 2) * OpP::kBytes], s_q[NB * OpQ::kBytes];
+  typedef typename WeightOperand<FORM != NT, Q, NTH, GRAN, NB == 3>::type OpQ;
+  constexpr bool kFar = GRAN == 0 && NB == 3, kFarCodes = GRAN != 0 && NB == 3;
+  constexpr int kQ = GRAN ? 2 : NB;  // stages of the Q side in LDS
+  constexpr int kLeft = kFarCodes ? 2 : kFar ? OpQ::kPieces : 0;  // a later stage's loads on their way at a handover
+  __shared__ __attribute__((aligned(4096))) uint8_t s_p[(MANY == 2 ? 1 : 2) * OpP::kBytes], s_q[kQ * OpQ::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_ring[kFarCodes ? 2 * NTH * 20 : 16];
   __shared__ __attribute__((aligned(16))) uint8_t s_turn[MANY ? WP * WQ * 4096 : 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -404,8 +448,11 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
       const size_t row = (size_t)r.e * a.N + (FORM == NT ? q0 : 0);
       const int col = FORM == NT ? 0 : q0;
       if constexpr (GRAN != 0) {
-        oq.init(a.w + row * (a.K / 2) + col / 2, a.w_sf + row * (a.K / GRAN) + col / GRAN, a.K, qn);
-        if (s1 > s0) oq.fetch(s0, sum);
+        oq.init(a.w + row * (a.K / 2) + col / 2, a.w_sf + row * (a.K / GRAN) + col / GRAN, a.K, qn, s_ring);
+        if (s1 > s0) {
+          oq.fetch(s0, sum);
+          if constexpr (kFarCodes) oq.fetch(s0 + 1, sum);
+        }
       } else {
         oq.init(a.q + row * a.K + col, 2 * a.K, qn);
       }
@@ -451,17 +498,17 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   auto handover = [&](bool last, uint32_t pb, uint32_t qb) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MANY) wait_loads(stores);
-    else wait_all<kFar ? OpQ::kPieces : 0>();  // (the stage after it is still on its way)
+    else wait_all<kLeft>();
     stores = 0;
     if ((OpQ::kClear || (OpP::kClear && !lone)) && tail && last) {
       if (OpP::kClear && !lone) OpP::clear(tail, s_p + pb);
       if constexpr (OpQ::kClear) OpQ::clear(tail, s_q + qb);
-      wait_all<MANY ? 63 : kFar ? OpQ::kPieces : 0>();
+      wait_all<MANY ? 63 : kLeft>();
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   uint32_t pb = 0, qb = 0;  // where the stage at hand lies
-  auto next_q = [](uint32_t b) __attribute__((always_inline)) { return b + OpQ::kBytes == NB * OpQ::kBytes ? 0 : b + OpQ::kBytes; };
+  auto next_q = [](uint32_t b) __attribute__((always_inline)) { return b + OpQ::kBytes == kQ * OpQ::kBytes ? 0 : b + OpQ::kBytes; };
   // TILES: of a wave's row tiles, those that exist (by halves; by quarters of 8).
   // Others are neither read nor multiplied, so that an expert's short last tile takes
   // as much less time (halves of 8 only, 16384 rows of 64 experts, N = 4096, K = 6144:
@@ -527,6 +574,7 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   auto start = [&](bool first) __attribute__((always_inline)) {
     if (s1 <= s0) return;
     if (!kFar && (first || s1 - s0 > 1)) op.load(s0, sum, s_p);
+    if constexpr (kFarCodes) wait_vm<OpP::kPieces + 2>();  // (the first stage's codes)
     oq.load(s0, sum, s_q);
     if constexpr (kFar) {
       op.load(s0, sum, s_p);
@@ -870,8 +918,11 @@ hipError_t launch_tile(const GroupedArgs& args, hipStream_t s) {
   // 926 us, 16 901, 4 898, 1 907 (64 experts of 8000 rows: 32 1082 us, 4 1063).  The
   // other forms: 32 the best or within 1% of it (8 experts of 16384 rows: 718 us, 4 748).
   const int most_group = FORM == TN ? 4 : 32;
-  a.group = (int)(tiles >= 8 * most_group ? most_group : (tiles + 7) / 8);
-  const long long round = 8 * a.group;  // (tile_of)
+  // (Where tiles are few, shared out evenly in two turns: as many as there will be if every expert
+  // has rows and half of its last tile is empty.)
+  const long long rows = args.M / P + (most + 1) / 2, likely = FORM == TN ? tiles : (rows > most ? rows : most) * nq;
+  a.group = (int)(likely >= 8 * most_group ? most_group : FORM == NT ? (likely + 15) / 16 : (likely + 7) / 8);
+  const long long round = 8 * (long long)a.group;  // (tile_of)
   const dim3 grid((unsigned)((tiles + round - 1) / round * round), a.parts);
   hipLaunchKernelGGL((grouped_tile_kernel<FORM, GRAN, P, Q, WP, WQ, NB, MANY>), grid, dim3(WP * WQ * 64), 0, s, a);
   const hipError_t err = hipGetLastError();
@@ -885,7 +936,9 @@ template <int FORM, int GRAN>
 hipError_t launch_form(const GroupedArgs& a, const GroupedPlan& plan, hipStream_t s) {
   if constexpr (FORM == NT) {
     if (plan.few == 1) return launch_few<GRAN, 2, 1, GRAN ? 1 : 3>(a, s);
-    if (plan.few == 2) return launch_few<GRAN, 2, 2, GRAN ? 1 : 3>(a, s);
+    if constexpr (GRAN == 0) {
+      if (plan.few == 2) return launch_few<GRAN, 2, 2, 3>(a, s);
+    }
   }
   if constexpr (GRAN == 0 && FORM != TN) {
     if (plan.many > 0 && (FORM == NT ? a.K : a.N) <= kS) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 1, 2>(a, s);
@@ -895,8 +948,13 @@ hipError_t launch_form(const GroupedArgs& a, const GroupedPlan& plan, hipStream_
   if constexpr (FORM == TN) {
     if (plan.tile == 64 && a.N > 64) return launch_tile<FORM, GRAN, 128, 64, 4, 1, 2>(a, s);
   }
-  if (plan.tile == 64) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
-  return launch_tile<FORM, GRAN, 128, 128, 2, 2, GRAN || FORM == TN ? 2 : 3>(a, s);
+  if (plan.tile == 64) {
+    if constexpr (GRAN != 0) {
+      if (FORM == NT || plan.far) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 3>(a, s);
+    }
+    if constexpr (GRAN == 0 || FORM != NT) return launch_tile<FORM, GRAN, 64, 128, 2, 2, 2>(a, s);
+  }
+  return launch_tile<FORM, GRAN, 128, 128, 2, 2, FORM == TN ? 2 : 3>(a, s);
 }
 
 }  // namespace
@@ -925,12 +983,12 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
     const long long n = (M + P / 2 * most) / P, rows = form == TN ? E * ((N + P - 1) / P) : n > most ? n : most;
     return rows * ((outs + Q - 1) / Q);
   };
-  GroupedPlan p{0, 128, 1, 0};
+  GroupedPlan p{0, 128, 1, 0, 0};
   if (form == TN) {
     if (N > 128 && K > 128 && tiles(256, 256) >= 256) p.tile = 256;
     else if (N <= 64 || K <= 64) p.tile = 64;  // (a low-rank factor's: 4000 rows, 64 experts, 32 x 6144 28 -> 21 us)
   } else {
-    if (form == NT && M <= (gran ? 16 : 6) * most) p.few = 1;
+    if (form == NT && M <= (gran ? 14 : 6) * most) p.few = 1;
     else if (form == NT && M <= 12 * most) p.few = 2;
     if (p.few) return p;
   }
@@ -947,13 +1005,14 @@ GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long l
   p.many = 0;
   if (form != TN) {
     if (tiles(256, 256) >= 256 && outs > 128 && (gran == 0 || M >= 192 * most)) p.tile = 256;
-    else if (tiles(128, 128) >= 256 && (gran == 0 || M >= 96 * most)) p.tile = 128;
+    else if (tiles(128, 128) >= 256 && (gran == 0 || M > (form == NT ? 28 : 64) * most)) p.tile = 128;
     else p.tile = 64;
   }
   const long long n = p.tile == 256 ? tiles(256, 256) : p.tile == 128 || form == TN ? tiles(128, 128) : tiles(64, 128);
   p.parts = (int)most_parts(form, M, E, N, K);  // (1 without rows)
   if (p.parts > 512 / n) p.parts = (int)(512 / n);
   if (n >= 256 || p.parts < 2 || stages * (p.parts - 1) < 18 * p.parts) p.parts = 1;
+  p.far = n * p.parts <= 512;
   return p;
 }
 

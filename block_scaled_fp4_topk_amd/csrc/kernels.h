@@ -224,7 +224,7 @@ struct GroupedArgs {
 // The form of a product: few 1, 2: the stream of the weights with 16 or 32 rows
 // per workgroup; else many > 0: so many tiles of 64 x 128 per workgroup, or tiles
 // of tile x tile outputs (64: 64 x 128), the sums in parts.
-struct GroupedPlan { int few, tile, parts, many; };
+struct GroupedPlan { int few, tile, parts, many, far; };
 GroupedPlan grouped_plan(int form, long long M, long long E, long long N, long long K, int gran);
 // The most floats that the parts of M or fewer rows take.
 long long grouped_part_floats(int form, long long M, long long E, long long N, long long K);
