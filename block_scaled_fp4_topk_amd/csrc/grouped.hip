@@ -5,6 +5,12 @@
 //   towards the weights: dW_e = sum_r dy[r] x[r]^T    (TN: both across it)
 // W_e [N, K] bfloat16, or E2M1 codes with group16 or group32 scales (decoded to
 // bfloat16, which holds a code times an E4M3 or UE8M0 scale exactly).
+//
+// All three run on the 16 x 16 x 32 bfloat16 matrix instructions with float32 sums;
+// an output is rounded once, to nearest.  Three things bound them: with few rows per
+// expert the weights' bytes from HBM, each read once (the stream of the weights below);
+// with many the matrix instructions, whose operands pass through LDS (the tiles); with
+// a short sum (a low-rank factor) the output's bytes and a tile's fixed time.
 #include "common.h"
 #include "kernels.h"
 
@@ -223,7 +229,8 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 }
 
 // Eight E2M1 codes times an E4M3 scale -> bfloat16, exact (6 significant bits):
-// multiplied as floats, whose upper halves are the result.
+// multiplied as floats, whose upper halves are the result.  (The conversion's own
+// scale is a power of two, and takes no E4M3 one.)
 __device__ __forceinline__ u32x4 dq8_scaled_bf16(uint32_t codes, float scale) {
   typedef float v2f __attribute__((ext_vector_type(2)));
   const v2f p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0),
@@ -239,7 +246,12 @@ __device__ __forceinline__ u32x4 dq8_scaled_bf16(uint32_t codes, float scale) {
 // FP4 weights as such an operand: a thread takes the 16 bytes of 32 codes of a
 // row through registers, and decodes them to where the direct loads would have
 // put them, a stage after they were asked for.  FAR: with their scales through a
-// place of its own in LDS, two stages after.
+// place of its own in LDS, two stages after: where few workgroups of small tiles wait
+// for HBM (32 group16 experts, N = 4096, K = 6144, tiles of 64 rows, 700 rows: 259 us
+// without, 190 with; of 128, 1000 rows: 229 and 221).  In tiles of 256 rows, whose
+// bound is LDS, its accesses cost more than it brings (8192 rows: 530 us without, 557
+// with), and so in the product towards the rows with tiles of 64 where there are many
+// (2000 rows: 256 and 276).
 template <bool TR, int SIZE, int NTH, int GRAN, bool FAR>
 struct Fp4Operand : Operand<TR, SIZE, NTH> {
   static_assert(SIZE * kS == 32 * NTH, "32 codes per thread and stage");
@@ -384,6 +396,18 @@ __device__ __forceinline__ void wait_loads(int left) {
 // ---------------------------------------------------------------------------
 // the tiled product
 
+// What bounds it.  One expert of 8192 x 8192 x 6144: 607 us, 1.36 PFLOP/s, where a
+// library's plain product of 8192^3 reaches 1.42 on the same card; the matrix
+// instructions are busy in two cycles of three at a clock that the card's power holds
+// at 1.85 GHz.  A wave takes 128 x 64 outputs (12 KB of LDS reads for 32
+// products; with 64 x 64, as in the tiles of 128, LDS becomes the bound: the sums of
+// dW of 65536 rows of 4 experts, N = 4096, K = 6144, 2692 us in tiles of 256, 3630 in
+// tiles of 128).  With ragged experts the weights' bytes and short last tiles come on
+// top: 16384 rows of 64 experts, N = 4096, K = 6144, 1031 us, of which the weights alone
+// would take 655 and the products alone 600.  dW: 620 us for 16384 more rows and 270
+// for writing 1.6 GB, which does not overlap with it: two tiles per CU (of 128 rows)
+// have the same 260 us.
+//
 // P x Q outputs per workgroup: P along the rows (TN: along N), Q along the
 // output's contiguous side; WP x WQ waves.  blockIdx.y: the part of the sum (more
 // than one: to a.part as float32, which grouped_sum adds up).  GRAN: 0, or FP4 weights' group.  NB:
@@ -751,7 +775,10 @@ __device__ __forceinline__ u32x4 few_scales(const uint8_t* base, uint32_t row, i
 
 // 16 NR weight rows x 16 NG rows of x per workgroup, the sum split over its 8
 // waves, chunk by chunk in turn; NC chunks of weights in flight per wave.  WHOLE:
-// the sum is whole chunks.
+// the sum is whole chunks.  Bound by HBM: the weights go through registers in whole
+// lines, past the caches, without a barrier; x comes from L2.  8 rows of 64 experts,
+// bfloat16, N = 4096, K = 6144: 62 us, 6.2 TB/s.  128 rows, group16: 168 to 197 us, 4 to
+// 4.7 TB/s; decoding the codes takes about as long as fetching them.
 template <int GRAN, bool WHOLE, int NR, int NG, int NC>
 __global__ __launch_bounds__(512, WHOLE && NG <= (GRAN ? 1 : 2) ? 4 : 2) void grouped_few_kernel(GroupedArgs a) {
   constexpr int CK = GRAN ? 256 : 64;  // elements per chunk
@@ -970,6 +997,22 @@ static long long most_parts(int form, long long M, long long E, long long N, lon
   return stages < 16 ? 1 : stages / 4 > 32 ? 32 : stages / 4;
 }
 
+// Which kernel and tile, by the rows per expert with rows (M / most) and by how many
+// tiles there are for the 256 CUs.  N = 4096, K = 6144 unless said:
+// - the stream of the weights.  bfloat16, 64 experts: up to 6 rows with 16 rows of x
+//   per workgroup (380 rows 465 us, with 32 463; 500 rows 496 and 485), up to 12 with 32
+//   (750 rows 520 us, tiles of 64 564; 1000 rows 574 and 565).  FP4, 32 group16 experts:
+//   up to 14 with 16 (400 rows 178 us, tiles of 64 185; 480 rows 208 and 190).
+// - tiles of 256 x 256 where there are 256 of them, bfloat16 from the first row on
+//   (64 experts, 4000 rows: 607 us, 128 x 128 674, 64 x 128 710; 1000 rows 579, 573,
+//   565), FP4 from 192 rows per expert on (32 experts, 3500 rows, group32: 394 us, 128 x
+//   128 321; 6000 rows 453 and 473).
+// - tiles of 128 x 128 where there are 256, FP4 from 28 (dx 64) rows per expert on
+//   (group16, 700 rows: 218 us, 64 x 128 190; 1000 rows 221 and 243; dx of 1500 rows 236
+//   and 225, group32 dx of 2500 rows 257 and 273).
+// - tiles of 64 x 128 else (dx of 600 rows of 8 experts, N = K = 4096: 70 us, 128 x 128
+//   73).  dW: 128 x 128, and 64 x 128 or 128 x 64 for a factor no larger than 64.
+//
 // With fewer than 256 tiles the sums are split so that there are up to 512, four
 // stages of 64 elements at least to a part (a stage of a lone workgroup takes 0.5
 // us, its loads' latency), where that saves more than the 6 us of adding the parts:

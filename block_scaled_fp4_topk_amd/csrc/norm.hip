@@ -3,7 +3,9 @@
 //   h' = h_scale h + scale act(gate) a
 //   n  = rms(h') * pre_w
 // and the gradient.  Memory bounds both: every tensor is read once and written
-// once, a row stays in registers between the two norms.
+// once, a row stays in registers between the two norms.  8192 x 6144, bfloat16: 84 us,
+// 4.8 TB/s, where a large copy reaches 4.9; the gradient with a float32 stream 206 us
+// and 5 us for the sums over rows, 4.4 TB/s.
 #include "common.h"
 #include "kernels.h"
 
@@ -230,7 +232,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_norm_kernel(NormArgs 
 //   d_pre_w = sum of dn hh, d_post_w = sum of da yy over the rows.
 // A workgroup takes every grid-th row and keeps its part of the sums over rows,
 // a thread its own columns', in LDS (MOST threads at most); norm_sum_kernel adds
-// the parts in order.
+// the parts in order.  Where registers allow it (kAhead) the next row is asked for
+// before this one's sums (on one card 8192 x 6144, float32: 245 us without, 235 with;
+// bfloat16 193 and 184; x 1024 84 and 41).
 template <bool WAVE, bool F32, int KIND, int MOST>
 __global__ __launch_bounds__(MOST) void block_norm_grad_kernel(NormArgs a) {
   __shared__ __attribute__((aligned(16))) float s_sum[2][kMostSums][kMostWaves];
