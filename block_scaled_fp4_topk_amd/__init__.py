@@ -293,7 +293,7 @@ def _grouped_need(direction, *problem):
 
 @functools.lru_cache(maxsize=1024)
 def _norm_grad_need(T, H):
-    return _need(lib().moe_fp4_block_norm_grad_workspace_bytes, ctypes.byref(Norm(T, H)))
+    return _need(lib().moe_fp4_block_norm_grad_workspace_bytes, ctypes.byref(Norm(T, H, eps=1.0)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -714,8 +714,8 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
     n = rms(h') pre_w; rms(v) = v / sqrt(mean(v^2) + eps).  h [T, H] bfloat16 or
     float32 (the residual stream), y [T, H] bfloat16 (the layer's output); gate [H]
     (per channel; also where T = H), [T] or [T, 1] (per token) or [T, H]; gate_act
-    None or "sigmoid"; weights and gate bfloat16 or float32.  h_out may be h (in
-    place).  Returns (h', n): h' of h's type, n [T, H] bfloat16.  Without y h' is h
+    None or "sigmoid"; weights and gate bfloat16 or float32; eps from 1e-20 to 1.
+    h_out may be h (in place).  Returns (h', n): h' of h's type, n [T, H] bfloat16.  Without y h' is h
     itself; without pre_w n is None."""
     import torch
     shape, _, problem, dev, at = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)

@@ -948,8 +948,9 @@ static moefp4_status norm_check(const moefp4_norm* p) {
   if (p->gate_kind < MOEFP4_GATE_NONE || p->gate_kind > MOEFP4_GATE_ELEMENT)
     return fail(MOEFP4_EINVAL, "unknown gate_kind %d", p->gate_kind);
   if (p->gate_sigmoid != 0 && p->gate_sigmoid != 1) return fail(MOEFP4_EINVAL, "gate_sigmoid must be 0 or 1, got %d", p->gate_sigmoid);
-  if (!isfinite(p->scale) || !isfinite(p->h_scale) || !isfinite(p->eps) || p->eps < 0)
-    return fail(MOEFP4_EINVAL, "scale, h_scale and eps must be finite, eps >= 0");
+  if (!isfinite(p->scale) || !isfinite(p->h_scale)) return fail(MOEFP4_EINVAL, "scale and h_scale must be finite");
+  // (squares below FP32's smallest number are nothing beside it, and it is nothing beside a mean beyond the largest one)
+  if (!(p->eps >= 1e-20f && p->eps <= 1.0f)) return fail(MOEFP4_EINVAL, "eps must be in [1e-20, 1], got %g", (double)p->eps);
   if (p->H > moefp4::kNormMostH || p->T > (1LL << 24) || p->T * p->H >= (1LL << 40))
     return fail(MOEFP4_EUNSUPPORTED, "H up to %d, T up to 2^24, T*H below 2^40", moefp4::kNormMostH);
   return MOEFP4_OK;

@@ -789,7 +789,7 @@ __global__ __launch_bounds__(512, WHOLE && NG <= (GRAN ? 1 : 2) ? 4 : 2) void gr
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4, K = a.K, N = a.N;
   const int nq = (N + ROWS - 1) / ROWS;
-  Rows r = rows_of(a.offsets, a.E, a.M, XR, nq, blockIdx.x);
+  Rows r = rows_of(a.offsets, a.E, a.M, XR, nq, blockIdx.y * gridDim.x + blockIdx.x);
   if (r.e < 0) return;
   const int e = __builtin_amdgcn_readfirstlane(r.e), i0 = __builtin_amdgcn_readfirstlane(r.i);
   const int m0 = i0 / nq * XR, n0 = i0 % nq * ROWS;
@@ -928,7 +928,9 @@ __global__ __launch_bounds__(512, WHOLE && NG <= (GRAN ? 1 : 2) ? 4 : 2) void gr
 template <int GRAN, int NR, int NG, int NC>
 hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   const long long nq = (a.N + 16 * NR - 1) / (16 * NR), most = a.E < a.M ? a.E : a.M;
-  const dim3 grid((unsigned)((a.M / (16 * NG) + most) * nq)), block(512);
+  // (a dimension of a grid has less than 2^32 threads)
+  const long long n = (a.M / (16 * NG) + most) * nq, x = n < (1 << 20) ? n : 1 << 20;
+  const dim3 grid((unsigned)x, (unsigned)((n + x - 1) / x)), block(512);
   if (a.K % (GRAN ? 256 : 64) == 0) hipLaunchKernelGGL((grouped_few_kernel<GRAN, true, NR, NG, NC>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((grouped_few_kernel<GRAN, false, NR, NG, NC>), grid, block, 0, s, a);
   return hipGetLastError();

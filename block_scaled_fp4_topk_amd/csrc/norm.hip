@@ -146,7 +146,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void block_norm_kernel(NormArgs 
   RowSum<WAVE> sum{s_sum};
   sum.init();
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x, tpr = WAVE ? 64 : blockDim.x, H = a.H;
-  const long long t = WAVE ? (long long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const long long b = (long long)blockIdx.y * gridDim.x + blockIdx.x, t = WAVE ? b * 4 + (threadIdx.x >> 6) : b;
   if (t >= a.T) return;  // (WAVE: whole waves, without barriers)
   const size_t row = (size_t)t * H;
   const float inv = 1.0f / (float)H;
@@ -595,6 +595,7 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int parts) {
 
 // Rows of up to 512 elements: a wave each.  Beyond, a workgroup of as many waves
 // as the row has pieces of 512 elements (1024 beyond 8192).
+constexpr long long kGridX = 1 << 20;  // (a dimension of a grid has less than 2^32 threads)
 int threads_of(int H, int C) { return (H + 512 * C - 1) / (512 * C) * 64; }
 
 template <bool WAVE, int C, bool F32, int KIND>
@@ -609,7 +610,8 @@ void launch_one(const NormArgs& a, int parts, hipStream_t s) {
     else if (block.x <= 768) hipLaunchKernelGGL((block_norm_grad_kernel<false, F32, KIND, 768>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((block_norm_grad_kernel<false, F32, KIND, 1024>), grid, block, 0, s, a);
   } else {
-    const dim3 grid((unsigned)(WAVE ? (a.T + 3) / 4 : a.T));
+    const long long n = WAVE ? (a.T + 3) / 4 : a.T, x = n < kGridX ? n : kGridX;
+    const dim3 grid((unsigned)x, (unsigned)((n + x - 1) / x));
     hipLaunchKernelGGL((block_norm_kernel<WAVE, C, F32, KIND>), grid, block, 0, s, a);
   }
 }

@@ -375,7 +375,7 @@ typedef struct moefp4_norm {
 } moefp4_norm;
 
 /* All device memory, 16-byte aligned (a gate per token 4-byte); H a positive
- * multiple of 8, eps >= 0, scale, h_scale and eps finite (EINVAL otherwise); H up
+ * multiple of 8, eps in [1e-20, 1], scale and h_scale finite (EINVAL otherwise); H up
  * to 16384, T up to 2^24, T*H below 2^40 (EUNSUPPORTED otherwise).  h_out may be
  * h itself (in place); no other output overlaps an input or the other one
  * (EINVAL).  No workspace.  Enqueued on `stream`. */

@@ -355,3 +355,41 @@ def test_streams_and_graphs():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, f()))
+
+
+def test_more_rows_than_a_grid_is_wide():
+    """T beyond 2^20 workgroups (or 2^22 waves)."""
+    require_gpu()
+    for T, H in (((1 << 20) + 5, 520), ((1 << 22) + 9, 8)):
+        c = Case(8, H, pre=True, y=False)
+        h = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+        h[:4], h[-4:] = c.h[:4], c.h[4:]
+        _, n = moe.block_norm(h, pre_w=c.pre)
+        want = moe.block_norm(c.h, pre_w=c.pre)[1]
+        assert torch.equal(n[:4], want[:4]) and torch.equal(n[-4:], want[4:]) and not bool(n[4:-4].any())
+
+
+def test_ends_of_eps():
+    """Rows so small that eps counts, down to the least one, and the largest one beside ordinary and large rows."""
+    require_gpu()
+    for H in (64, 1024, 8200):
+        for eps, sizes in ((1.1e-20, (1e-9, 1e-10, 1e-12)), (1.0, (1.0, 1e-3, 1e19))):
+            for size in sizes:
+                c = Case(4, H, gate="channel", stream=torch.float32, size=size, eps=eps)
+                c.dh.zero_()
+                c.check_forward()
+                c.check_backward()
+
+
+def test_operators_refuse_a_stream_of_another_device():
+    require_gpu()
+    from test_operator_streams import OnDevice
+    c = Case(4, 64, gate="channel")
+    w, off = torch.ones((1, 64, 64), device="cuda").bfloat16(), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    for call in (lambda s: moe.block_norm(c.h, c.y, **c.args(), stream=s), lambda s: moe.block_norm_grad(c.dh, c.dn, c.h, c.y, **c.args(), stream=s),
+                 lambda s: moe.grouped(c.y, w, off, stream=s), lambda s: moe.grouped_dx(c.y, w, off, stream=s),
+                 lambda s: moe.grouped_dw(c.y, c.y, off, stream=s)):
+        call(torch.cuda.Stream())
+        torch.cuda.synchronize()
+        with pytest.raises(ValueError, match="stream"):
+            call(OnDevice(1))

@@ -370,3 +370,35 @@ def test_offsets_past_32_bits(form):
     W = W.T if form == "grouped" else W
     ref, mag = a @ W, a.abs() @ W.abs()
     assert bool(((out[42:].double() - ref).abs() <= (max(N, K) + 18) * U32 * mag).all()) and bool((out[:2] == 0).all())
+
+
+def test_more_tiles_than_a_grid_is_wide():
+    """256 experts of a row each and N = 2^20: 2^23 workgroups of 512 threads and more."""
+    require_gpu()
+    E, N, K = 256, 1 << 20, 8
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
+    w[E - 1].copy_(torch.randn((N, K), device="cuda"))
+    x = torch.randn((E, K), device="cuda").bfloat16()
+    out = moe.grouped(x, w, offsets_of([1] * E))
+    ref, mag = w[E - 1].double() @ x[E - 1].double(), w[E - 1].double().abs() @ x[E - 1].double().abs()
+    b = (K + 18) * U32 * mag
+    assert bool(((out[E - 1].double() - ref).abs() <= b + UBF * (ref.abs() + b)).all()) and not bool(out[:E - 1].any())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with a workspace each, sums in parts among them, give what they give one by one."""
+    require_gpu()
+    cases = [Case([60], 2048, 64, seed=1), Case([700], 64, 2048, seed=2), Case([33, 20], 2048, 256, 16, seed=3)]
+    calls = [lambda c: moe.grouped_dx(c.dy, c.w, c.off, **c.kw()), lambda c: moe.grouped(c.x, c.w, c.off, **c.kw())]
+    want = [[f(c) for f in calls] for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append([[f(c) for f in calls] for c in cases])
+    torch.cuda.synchronize()
+    for g in got:
+        for r in g:
+            assert all(torch.equal(a, b) for x, y in zip(r, want) for a, b in zip(x, y))

@@ -154,6 +154,16 @@ def test_grouped_workspace_serves_smaller_batches(L):
                     assert call(odd(9, 64), need) == m.EINVAL and b"256" in L.moefp4_last_error()
                     assert call(far(9), need) == m.EINVAL and b"out overlaps" in L.moefp4_last_error()
     assert asked > 20
+    # FP4 weights choose other tiles, within the same workspace
+    for gran, E in ((16, 1), (16, 8), (32, 3), (32, 40)):
+        for N, K in ((4096, 4096), (64, 4096), (2048, 512), (8, 6144)):
+            for d in range(2):
+                for M in (1, 13, 15, 29, 40, 64, 65, 96, 200, 700, 2000, 5000):
+                    size = dict(M=M, N=N, K=K, E=E, gran_k=gran)
+                    n, p = grouped_ws(L, d, **size)[1], ctypes.byref(problem(**size))
+                    call = (L.moe_fp4_grouped, L.moe_fp4_grouped_dx)[d]
+                    assert call(p, far(0), far(1), far(2), Z, far(4), far(0), far(9), n, Z) == m.EINVAL
+                    assert b"out overlaps" in L.moefp4_last_error(), (d, size)
     # the workspace over an input or out
     p = ctypes.byref(problem(M=60, N=4096, K=4096, E=1))
     for k in (0, 1, 4, 5):
@@ -262,3 +272,8 @@ def test_python_refuses():
             call()
     with pytest.raises(ValueError, match="go with pre_w"):
         m.block_norm_grad(x, x, None, y=x)
+
+
+@pytest.mark.parametrize("eps,status", [(0.0, m.EINVAL), (9e-21, m.EINVAL), (1.01, m.EINVAL), (float("inf"), m.EINVAL), (1.01e-20, m.OK), (1.0, m.OK)])
+def test_norm_eps(L, eps, status):
+    assert norm_ws(L, norm(eps=eps))[0] == status
