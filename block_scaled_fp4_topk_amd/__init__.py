@@ -287,8 +287,14 @@ def _layer_need(device, top_k, shared, scoring, w_fmt, *problem):
 
 
 @functools.lru_cache(maxsize=1024)
+def _grouped_problem(direction, *problem):
+    """(the problem as the library takes it, the workspace it needs)"""
+    p = ctypes.byref(Grouped(*problem))
+    return p, _need(lib().moe_fp4_grouped_workspace_bytes, p, direction)
+
+
 def _grouped_need(direction, *problem):
-    return _need(lib().moe_fp4_grouped_workspace_bytes, ctypes.byref(Grouped(*problem)), direction)
+    return _grouped_problem(direction, *problem)[1]
 
 
 @functools.lru_cache(maxsize=1024)
@@ -588,43 +594,47 @@ def _out_dtype(out, out_dtype):
     return out_dtype, OUT_F32 if out_dtype is torch.float32 else OUT_BF16
 
 
-def _grouped_scratch(direction, problem, workspace, like, stream):
+def _grouped_scratch(need, workspace, like, stream):
     """(the workspace, held until the call is enqueued; its address; its size), None and 0 where none is needed."""
-    need = _grouped_need(direction, *problem)
     if need == 0 and workspace is None:
         return None, None, 0
     ws = _scratch(workspace, need, like, stream)
     return ws, ws.data_ptr(), ws.numel()
 
 
-def _grouped_product(fn, direction, name, x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream, out_dtype):
+def _grouped_product(entry, direction, name, x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream, out_dtype):
     import torch
-    along_k = direction == 0
     u8, bf = (torch.uint8,), (torch.bfloat16,)
     M, cols = _dims(x, name, bf, 2)
     dev = _current(x, stream)
-    if gran_k not in (None, 0, 16, 32):
-        raise ValueError(f"gran_k must be None (bfloat16 weights), 16 or 32, got {gran_k}")
-    E, N, K = _dims(w, "w", u8 if gran_k else bf, 3)
+    sf = gs = None
     if gran_k:
+        if gran_k not in (16, 32):
+            raise ValueError(f"gran_k must be None (bfloat16 weights), 16 or 32, got {gran_k}")
+        E, N, K = _dims(w, "w", u8, 3)
         K *= 2
         if w_sf is None:
             raise ValueError("FP4 weights need w_sf")
-    elif w_sf is not None or w_gs is not None:
-        raise ValueError("w_sf and w_gs go with FP4 weights (gran_k)")
-    _arg(w, "w", u8 if gran_k else bf, (E, N, K // 2 if gran_k else K), dev)
-    _arg(x, name, bf, (M, K if along_k else N), dev)
-    outs = N if along_k else K
+        sf = _arg(w_sf, "w_sf", u8, (E, N, K // gran_k), dev)
+        gs = _arg(w_gs, "w_gs", (torch.float32,), (E,), dev)
+    else:
+        E, N, K = _dims(w, "w", bf, 3)
+        if w_sf is not None or w_gs is not None:
+            raise ValueError("w_sf and w_gs go with FP4 weights (gran_k)")
+    ins, outs = (K, N) if direction == 0 else (N, K)
+    if cols != ins or w.device != dev:  # (what else _arg looks at is known)
+        _arg(x, name, bf, (M, ins), dev)
+        _arg(w, "w", (w.dtype,), w.shape, dev)
     out_dtype, fmt = _out_dtype(out, out_dtype)
-    sf = _arg(w_sf, "w_sf", u8, (E, N, K // gran_k), dev) if gran_k else None
-    gs = _arg(w_gs, "w_gs", (torch.float32,), (E,), dev)
     off = _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    problem, need = _grouped_problem(direction, M, N, K, E, gran_k or 0, fmt)
     if out is None:
         out = _empty(x, (M, outs), out_dtype, stream)
-    problem = (M, N, K, E, gran_k or 0, fmt)
-    ws, *room = _grouped_scratch(direction, problem, workspace, x, stream)
-    _check(fn(ctypes.byref(Grouped(*problem)), x.data_ptr(), w.data_ptr(), sf, gs, off,
-              _arg(out, "out", (out_dtype,), (M, outs), dev), *room, _raw_stream(stream, dev)))
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, "out", (out_dtype,), (M, outs), dev)
+    ws, *room = _grouped_scratch(need, workspace, x, stream)
+    _check(getattr(_lib, entry)(problem, x.data_ptr(), w.data_ptr(), sf, gs, off, out_at, *room, _raw_stream(stream, dev)))
     return out
 
 
@@ -635,7 +645,7 @@ def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, workspac
     FP4 codes with w_sf [E, N, K/gran_k] uint8 (and w_gs [E] float32) and gran_k 16
     or 32.  Returns out [M, N] bfloat16 (default) or float32; rows outside
     [offsets[0], offsets[E]) are left as they are."""
-    return _grouped_product(lib().moe_fp4_grouped, 0, "x", x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
+    return _grouped_product("moe_fp4_grouped", 0, "x", x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)
 
 
@@ -644,7 +654,7 @@ def grouped_dx(dy, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, work
     """The gradient of grouped() towards its rows: out[r] = W_e^T dy[r], dy [M, N]
     bfloat16, the weights and offsets as grouped() takes them.  Returns out
     [M, K]."""
-    return _grouped_product(lib().moe_fp4_grouped_dx, 1, "dy", dy, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
+    return _grouped_product("moe_fp4_grouped_dx", 1, "dy", dy, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)
 
 
@@ -662,12 +672,14 @@ def grouped_dw(dy, x, offsets, out=None, accumulate=False, workspace=None, strea
         raise ValueError("accumulate needs out")
     out_dtype, fmt = _out_dtype(out, out_dtype)
     at = dy.data_ptr(), _arg(x, "x", bf, (M, K), dev), _arg(offsets, "offsets", (torch.int32,), (E + 1,), dev)
+    problem, need = _grouped_problem(2, M, N, K, E, 0, fmt)
     if out is None:
-        out = _empty(dy, (max(E, 0), N, K), out_dtype, stream)
-    problem = (M, N, K, E, 0, fmt)
-    ws, *room = _grouped_scratch(2, problem, workspace, dy, stream)
-    _check(_lib.moe_fp4_grouped_dw(ctypes.byref(Grouped(*problem)), *at, _arg(out, "out", (out_dtype,), (E, N, K), dev),
-                                   1 if accumulate else 0, *room, _raw_stream(stream, dev)))
+        out = _empty(dy, (E, N, K), out_dtype, stream)
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, "out", (out_dtype,), (E, N, K), dev)
+    ws, *room = _grouped_scratch(need, workspace, dy, stream)
+    _check(_lib.moe_fp4_grouped_dw(problem, *at, out_at, 1 if accumulate else 0, *room, _raw_stream(stream, dev)))
     return out
 
 
@@ -723,12 +735,14 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
         raise ValueError("h_out goes with y")
     if pre_w is None and n is not None:
         raise ValueError("n goes with pre_w")
+    h_at, n_at = _arg(h_out, "h_out", (h.dtype,), shape, dev), _arg(n, "n", (torch.bfloat16,), shape, dev)
     if y is not None and h_out is None:
         h_out = _empty(h, shape, h.dtype, stream)
+        h_at = h_out.data_ptr()
     if pre_w is not None and n is None:
         n = _empty(h, shape, torch.bfloat16, stream)
-    _check(lib().moe_fp4_block_norm(problem, h.data_ptr(), *at, _arg(h_out, "h_out", (h.dtype,), shape, dev),
-                                    _arg(n, "n", (torch.bfloat16,), shape, dev), _raw_stream(stream, dev)))
+        n_at = n.data_ptr()
+    _check((_lib or lib()).moe_fp4_block_norm(problem, h.data_ptr(), *at, h_at, n_at, _raw_stream(stream, dev)))
     return (h if y is None else h_out), n
 
 
@@ -741,7 +755,6 @@ def block_norm_grad(dh, dn, h, y=None, post_w=None, gate=None, gate_act=None, sc
     d_h of h's type, d_y bfloat16, the weights' and the gate's float32 (a gate [T, H]:
     of its type)."""
     import torch
-    f32 = (torch.float32,)
     if (pre_w is None) != (dn is None) or (pre_w is None) != (h is None):
         raise ValueError("dn and h go with pre_w")
     first, name = (h, "h") if h is not None else (dh, "dh")
@@ -749,19 +762,31 @@ def block_norm_grad(dh, dn, h, y=None, post_w=None, gate=None, gate_act=None, sc
     T, H = shape
     need = _norm_grad_need(T, H)
     own = (first.dtype,)
-    dh_at, dn_at, h_at = _arg(dh, "dh", own, shape, dev), _arg(dn, "dn", (torch.bfloat16,), shape, dev), None
+    bf16, f32 = torch.bfloat16, torch.float32
+    dh_at, dn_at, h_at = _arg(dh, "dh", own, shape, dev), _arg(dn, "dn", (bf16,), shape, dev), None
     if h is not None:
-        h_at = _arg(h, "h", own, shape, dev)
+        h_at = h.data_ptr()
     if d_h is None:
         d_h = _empty(first, shape, first.dtype, stream)
-    new = lambda like, size, dtype: None if like is None else _empty(first, size, dtype, stream)
-    d_y, d_post, d_pre = new(y, shape, torch.bfloat16), new(post_w, (H,), torch.float32), new(pre_w, (H,), torch.float32)
-    d_gate = None if gate is None else new(gate, tuple(gate.shape), gate.dtype if kind == 3 else torch.float32)
+        d_h_at = d_h.data_ptr()
+    else:
+        d_h_at = _arg(d_h, "d_h", own, shape, dev)
+    d_y = d_post = d_gate = d_pre = d_y_at = d_post_at = d_gate_at = d_pre_at = None
+    if y is not None:
+        d_y = _empty(first, shape, bf16, stream)
+        d_y_at = d_y.data_ptr()
+    if post_w is not None:
+        d_post = _empty(first, (H,), f32, stream)
+        d_post_at = d_post.data_ptr()
+    if gate is not None:
+        d_gate = _empty(first, gate.shape, gate.dtype if kind == 3 else f32, stream)
+        d_gate_at = d_gate.data_ptr()
+    if pre_w is not None:
+        d_pre = _empty(first, (H,), f32, stream)
+        d_pre_at = d_pre.data_ptr()
     ws = _scratch(workspace, need, first, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib().moe_fp4_block_norm_grad(problem, dh_at, dn_at, h_at, *at, _arg(d_h, "d_h", own, shape, dev),
-                                         ptr(d_y), ptr(d_post), ptr(d_gate), ptr(d_pre), ws.data_ptr(), ws.numel(),
-                                         _raw_stream(stream, dev)))
+    _check(_lib.moe_fp4_block_norm_grad(problem, dh_at, dn_at, h_at, *at, d_h_at, d_y_at, d_post_at, d_gate_at, d_pre_at,
+                                        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)))
     return d_h, d_y, d_post, d_gate, d_pre
 
 
