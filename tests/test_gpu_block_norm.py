@@ -393,3 +393,12 @@ def test_operators_refuse_a_stream_of_another_device():
         torch.cuda.synchronize()
         with pytest.raises(ValueError, match="stream"):
             call(OnDevice(1))
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("H", [8, 1032, 3080, 5000, 7000, 8192, 8200])
+def test_the_norm_before_the_first_layer(H, stream):
+    require_gpu()
+    c = Case(5, H, y=False, stream=stream)
+    c.check_forward()
+    c.check_backward()

@@ -402,3 +402,20 @@ def test_two_calls_at_once():
     for g in got:
         for r in g:
             assert all(torch.equal(a, b) for x, y in zip(r, want) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("gran", [0, 16, 32])
+@pytest.mark.parametrize("rows", [(300, 420, 17), (100, 90, 65), (257, 256, 31)], ids=str)
+def test_dx_of_wide_experts(rows, gran):
+    """The larger tiles towards the rows, a sum that is no whole stages, tiles that end with an expert's rows."""
+    require_gpu()
+    for N in (200, 392):
+        Case(rows, N, 32768, gran, seed=N).dx()
+
+
+@pytest.mark.parametrize("K", [64, 128, 1088])
+def test_rows_for_the_wider_stream(K):
+    """6 to 12 rows per expert of bfloat16 weights, sums of whole lines."""
+    require_gpu()
+    Case([10, 8, 12, 7], 72, K).product()
+    Case([0, 33, 1, 12, 2], 40, K).product()
