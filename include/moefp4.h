@@ -343,7 +343,8 @@ moefp4_status moe_fp4_grouped_workspace_bytes(const moefp4_grouped* p, int32_t d
  * device memory; N and K multiples of 8, K of 32 with FP4 weights (EINVAL
  * otherwise); E up to 512, M up to 2^24, N and K up to 2^20, M*N, M*K and E*N*K
  * below 2^40 (EUNSUPPORTED otherwise).  out overlaps no input and not the
- * workspace (EINVAL).  Enqueued on `stream`. */
+ * workspace (EINVAL).  Calls that run at once (streams, replayed graphs) need a
+ * workspace each.  Enqueued on `stream`. */
 moefp4_status moe_fp4_grouped(const moefp4_grouped* p, const void* x, const void* w, const uint8_t* w_sf,
                               const float* w_gs, const int32_t* offsets, void* out, void* workspace, size_t ws_bytes,
                               hipStream_t stream);
@@ -389,7 +390,7 @@ moefp4_status moe_fp4_block_norm(const moefp4_norm* p, const void* h, const void
  * call before did not have is NULL here too: without y also d_y, without pre_w
  * also h, dn and d_pre_w (then dh is needed).  Sums over rows are formed in a
  * fixed order.  d_h may be dh itself; no other output overlaps anything
- * (EINVAL). */
+ * (EINVAL).  Calls that run at once need a workspace each. */
 moefp4_status moe_fp4_block_norm_grad_workspace_bytes(const moefp4_norm* p, size_t* bytes);
 moefp4_status moe_fp4_block_norm_grad(const moefp4_norm* p, const void* dh, const void* dn, const void* h, const void* y,
                                       const void* post_w, const void* gate, const void* pre_w, void* d_h, void* d_y,
