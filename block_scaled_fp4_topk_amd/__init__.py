@@ -32,6 +32,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 __all__ = ["Problem", "MoeFp4Error", "lib", "workspace_bytes", "workspace_offsets", "gate", "route", "forward",
            "forward_problem", "forward_static", "layer", "project", "grouped", "grouped_dx", "grouped_dw",
@@ -683,9 +684,13 @@ def grouped_dw(dy, x, offsets, out=None, accumulate=False, workspace=None, strea
     return out
 
 
+_numbers = struct.Struct("3d")
+
+
 @functools.lru_cache(maxsize=1024)
 def _norm_problem(*fields):
-    return ctypes.byref(Norm(*fields))
+    """The problem of a block norm as the library takes it; last of the fields: scale, h_scale and eps as _numbers."""
+    return ctypes.byref(Norm(*fields[:-1], *_numbers.unpack(fields[-1])))
 
 
 def _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream):
@@ -712,10 +717,14 @@ def _norm_args(first, name, y, post_w, gate, gate_act, pre_w, scale, h_scale, ep
         gate_at, gate_fmt = _arg(gate, "gate", some, gate.shape, dev), OUT_F32 if gate.dtype is f32 else OUT_BF16
     at = (_arg(y, "y", bf, shape, dev), _arg(post_w, "post_w", some, (H,), dev), gate_at,
           _arg(pre_w, "pre_w", some, (H,), dev))
+    # (what a problem is remembered by are its numbers' bits, as they are at this call: a tensor's value can change, and
+    # -0.0 == 0.0)
+    if not (type(scale) is type(h_scale) is type(eps) is float):
+        scale, h_scale, eps = (ctypes.c_double(v).value for v in (scale, h_scale, eps))
     problem = _norm_problem(T, H, OUT_F32 if first.dtype is f32 else OUT_BF16,
                             OUT_F32 if post_w is not None and post_w.dtype is f32 else OUT_BF16,
                             OUT_F32 if pre_w is not None and pre_w.dtype is f32 else OUT_BF16, gate_fmt, kind,
-                            0 if gate_act is None else 1, scale, h_scale, eps)
+                            0 if gate_act is None else 1, _numbers.pack(scale, h_scale, eps))
     return shape, kind, problem, dev, at
 
 
@@ -727,8 +736,10 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
     float32 (the residual stream), y [T, H] bfloat16 (the layer's output); gate [H]
     (per channel; also where T = H), [T] or [T, 1] (per token) or [T, H]; gate_act
     None or "sigmoid"; weights and gate bfloat16 or float32; eps from 1e-20 to 1.
-    h_out may be h (in place).  Returns (h', n): h' of h's type, n [T, H] bfloat16.  Without y h' is h
-    itself; without pre_w n is None."""
+    scale, h_scale and eps are numbers; of a tensor with one element the value at the
+    call is taken, on the host (one on the device is waited for, and cannot be taken
+    while a graph is captured).  h_out may be h (in place).  Returns (h', n): h' of h's
+    type, n [T, H] bfloat16.  Without y h' is h itself; without pre_w n is None."""
     import torch
     shape, _, problem, dev, at = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
     if y is None and h_out is not None:
