@@ -612,6 +612,7 @@ def _grouped_product(entry, direction, name, x, w, offsets, w_sf, w_gs, gran_k, 
     if gran_k:
         if gran_k not in (16, 32):
             raise ValueError(f"gran_k must be None (bfloat16 weights), 16 or 32, got {gran_k}")
+        gran_k = int(gran_k)  # (what the problem is remembered by: a tensor's value can change)
         E, N, K = _dims(w, "w", u8, 3)
         K *= 2
         if w_sf is None:
