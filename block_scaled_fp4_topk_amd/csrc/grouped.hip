@@ -447,6 +447,10 @@ __global__ __launch_bounds__(WP * WQ * 64, P * Q / (WP * WQ) > 8192 ? 1 : 2) voi
   if constexpr (FORM == TN) {
     r.r0 = __builtin_amdgcn_readfirstlane(r.r0);
     r.n = __builtin_amdgcn_readfirstlane(r.n);
+    // (an expert without rows is left as it is: a sum of nothing would make 0.0 of its -0.0, and
+    // takes reading and writing it: 2048 rows of 8 of 64 experts, N = 4096, K = 6144, float32:
+    // 3060 us so, 496 us without)
+    if (a.accumulate && r.n == 0) return;
   }
   int tp, tq;
   tile_at(r.i, r.np, nq, &tp, &tq);
@@ -720,7 +724,7 @@ __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupedArgs a, int out
   }
   if (TN_ && a.accumulate) {
     const int e = (int)(i / outs / a.N);
-    if (a.offsets[e + 1] <= a.offsets[e]) return;  // (nothing to add)
+    if (min(max(a.offsets[e + 1], 0), a.M) <= min(max(a.offsets[e], 0), a.M)) return;  // (nothing to add, no parts)
   }
   v4f v = {0.f, 0.f, 0.f, 0.f}, w = v;
 #pragma unroll 4
