@@ -394,7 +394,7 @@ __global__ __launch_bounds__(MOST) void block_norm_grad_kernel(NormArgs a) {
       if (at >= H) continue;
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = ry * (D[c][j] - y[c][j] * ry * mv);
+      for (int j = 0; j < 8; ++j) o[j] = a.post_w ? ry * (D[c][j] - y[c][j] * ry * mv) : D[c][j];  // (y may be an infinity)
       store8(a.d_y, false, row + at, o);
     }
   }
@@ -561,7 +561,7 @@ __global__ __launch_bounds__(1024) void block_norm_grad_wide_kernel(NormArgs a) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         d[j] *= hs;
-        v[j] = ry * (v[j] - yy[j] * mv);
+        if (a.post_w) v[j] = ry * (v[j] - yy[j] * mv);  // (else v: y may be an infinity)
       }
       store8(a.d_h, F32, row + at, d);
       store8(a.d_y, false, row + at, v);
