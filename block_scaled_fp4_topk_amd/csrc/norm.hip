@@ -46,14 +46,16 @@ __device__ __forceinline__ float load1(const void* p, bool f32, size_t i) {
 }
 
 // 1 / (1 + e^-g) to a few ulp: 2^t with the rounding of t = -g log2(e) put back,
-// and the hardware's reciprocal.  (Beyond +-87, where one side is 1 and the other
-// at the end of FP32's normal range, as there; NaN stays.)
+// and the hardware's reciprocal.  Beyond +-87, where one side is 1 and the other
+// leaves FP32's normal range, 1 and 0: a gate that is closed by -infinity or by its
+// type's lowest value lets nothing through.  (NaN stays.)
 __device__ __forceinline__ float sigmoid(float g) {
   const float x = g > 87.0f ? -87.0f : g < -87.0f ? 87.0f : -g;
   const float t = x * 0x1.715476p+0f;
   const float lo = __builtin_fmaf(x, 0x1.715476p+0f, -t) + x * 0x1.4AE0C0p-26f;  // log2(e) = the two parts' sum
   const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, lo * 0x1.62E430p-1f, e));
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, lo * 0x1.62E430p-1f, e));
+  return g < -87.0f ? 0.0f : s;
 }
 
 // Eight values as they lie in memory.

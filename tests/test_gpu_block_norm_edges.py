@@ -30,3 +30,17 @@ def test_a_branch_without_a_norm_has_its_gradient_whatever_it_holds(H, gate):
             torch.cuda.synchronize()
             assert bool(torch.isfinite(want[1]).all())
             assert torch.equal(got[0], want[0]) and torch.equal(got[1].view(torch.int16), want[1].view(torch.int16)), (stream, act)
+
+
+def test_a_closed_gate():
+    """sigmoid of the types' lowest values and of -infinity is 0: nothing of y enters h', and no gradient y."""
+    require_gpu()
+    for H in (64, 1024, 8200):
+        h, y = torch.zeros((4, H), device="cuda"), torch.full((4, H), 3e30, device="cuda").bfloat16()
+        w = torch.ones(H, device="cuda")
+        for dtype in (torch.bfloat16, torch.float32):
+            g = torch.tensor([-float("inf"), torch.finfo(dtype).min, -200.0, -105.0], device="cuda").to(dtype)
+            for gate in (g, g[:, None].expand(4, H).contiguous()):
+                out, n = moe.block_norm(h, y, gate=gate, gate_act="sigmoid", pre_w=w)
+                _, dy, _, dg, _ = moe.block_norm_grad(torch.ones_like(h), None, None, y, gate=gate, gate_act="sigmoid")
+                assert not bool(out.any()) and not bool(n.any()) and not bool(dy.any()) and not bool(dg.any())
