@@ -48,13 +48,16 @@ __device__ __forceinline__ float load1(const void* p, bool f32, size_t i) {
 // 1 / (1 + e^-g) to a few ulp: 2^t with the rounding of t = -g log2(e) put back,
 // and the hardware's reciprocal.  Beyond +-87, where one side is 1 and the other
 // leaves FP32's normal range, 1 and 0: a gate that is closed by -infinity or by its
-// type's lowest value lets nothing through.  (NaN stays.)
-__device__ __forceinline__ float sigmoid(float g) {
+// type's lowest value lets nothing through.  (NaN stays.)  Its slope is e / (1 + e)^2,
+// e = e^-g, and 0 beyond +-87: of a large gate s (1 - s) would leave the rounding of s
+// (0 from 17 on).
+__device__ __forceinline__ float sigmoid(float g, float* slope = nullptr) {
   const float x = g > 87.0f ? -87.0f : g < -87.0f ? 87.0f : -g;
   const float t = x * 0x1.715476p+0f;
   const float lo = __builtin_fmaf(x, 0x1.715476p+0f, -t) + x * 0x1.4AE0C0p-26f;  // log2(e) = the two parts' sum
-  const float e = __builtin_amdgcn_exp2f(t);
-  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, lo * 0x1.62E430p-1f, e));
+  const float e0 = __builtin_amdgcn_exp2f(t), e = __builtin_fmaf(e0, lo * 0x1.62E430p-1f, e0);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  if (slope) *slope = fabsf(g) > 87.0f ? 0.0f : e * s * s;
   return g < -87.0f ? 0.0f : s;
 }
 
@@ -354,10 +357,7 @@ __global__ __launch_bounds__(MOST) void block_norm_grad_kernel(NormArgs a) {
     float act_t = 1.0f, slope_t = 1.0f;
     if (KIND == 2) {
       act_t = load1(a.gate, a.gate_f32, t);
-      if (a.gate_act) {
-        act_t = sigmoid(act_t);
-        slope_t = act_t * (1.0f - act_t);
-      }
+      if (a.gate_act) act_t = sigmoid(act_t, &slope_t);
     }
     float vs[2] = {0.0f, 0.0f};  // sums of v yy and of D a
 #pragma unroll
@@ -373,8 +373,8 @@ __global__ __launch_bounds__(MOST) void block_norm_grad_kernel(NormArgs a) {
         const float sd = a.scale * D[c][j], Da = sd * (yy * wj);
         float act = act_t, slope = slope_t;
         if (KIND == 1 || KIND == 3) {
-          act = a.gate_act ? sigmoid(g[j]) : g[j];
-          slope = a.gate_act ? act * (1.0f - act) : 1.0f;
+          slope = 1.0f;
+          act = a.gate_act ? sigmoid(g[j], &slope) : g[j];
         }
         o[j] = Da * slope;
         const float da = sd * act;
@@ -482,10 +482,7 @@ __global__ __launch_bounds__(1024) void block_norm_grad_wide_kernel(NormArgs a) 
     float act_t = 1.0f, slope_t = 1.0f;
     if (KIND == 2) {
       act_t = load1(a.gate, a.gate_f32, t);
-      if (a.gate_act) {
-        act_t = sigmoid(act_t);
-        slope_t = act_t * (1.0f - act_t);
-      }
+      if (a.gate_act) act_t = sigmoid(act_t, &slope_t);
     }
     // d = D of the eight at `at`
     auto total = [&](int at, bool first, float (&d)[8]) __attribute__((always_inline)) {
@@ -522,8 +519,8 @@ __global__ __launch_bounds__(1024) void block_norm_grad_wide_kernel(NormArgs a) 
         const float wj = a.post_w ? w[j] : 1.0f, sd = a.scale * d[j], Da = sd * (yy[j] * wj);
         float act = act_t, slope = slope_t;
         if (KIND == 1 || KIND == 3) {
-          act = a.gate_act ? sigmoid(g[j]) : g[j];
-          slope = a.gate_act ? act * (1.0f - act) : 1.0f;
+          slope = 1.0f;
+          act = a.gate_act ? sigmoid(g[j], &slope) : g[j];
         }
         o[j] = Da * slope;
         p[j] = sd * act * yy[j];
