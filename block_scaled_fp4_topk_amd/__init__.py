@@ -645,7 +645,8 @@ def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, workspac
     [offsets[e], offsets[e + 1]).  x [M, K] bfloat16; offsets [E + 1] int32,
     ascending (as route() gives them); w [E, N, K] bfloat16, or [E, N, K/2] uint8
     FP4 codes with w_sf [E, N, K/gran_k] uint8 (and w_gs [E] float32) and gran_k 16
-    or 32.  Returns out [M, N] bfloat16 (default) or float32; rows outside
+    or 32 (a code times its scale is taken as a bfloat16: exact below 2^128, an
+    infinity from there on).  Returns out [M, N] bfloat16 (default) or float32; rows outside
     [offsets[0], offsets[E]) are left as they are."""
     return _grouped_product("moe_fp4_grouped", 0, "x", x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)

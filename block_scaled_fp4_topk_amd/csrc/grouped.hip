@@ -3,8 +3,10 @@
 //   product:            y[r]  = W_e x[r]              (NT: both operands along the sum)
 //   towards the rows:   dx[r] = W_e^T dy[r]           (NN: the weights across it)
 //   towards the weights: dW_e = sum_r dy[r] x[r]^T    (TN: both across it)
-// W_e [N, K] bfloat16, or E2M1 codes with group16 or group32 scales (decoded to
-// bfloat16, which holds a code times an E4M3 or UE8M0 scale exactly).
+// W_e [N, K] bfloat16, or E2M1 codes with group16 or group32 scales, decoded to
+// bfloat16.  That holds a code times its scale exactly, at the lower end as a
+// subnormal, which the matrix instructions take, wherever it is below 2^128: with every
+// E4M3 scale and with UE8M0 bytes up to 252 (beyond, 4 times 2^126 is an infinity).
 //
 // All three run on the 16 x 16 x 32 bfloat16 matrix instructions with float32 sums;
 // an output is rounded once, to nearest.  Three things bound them: with few rows per

@@ -325,7 +325,9 @@ moefp4_status moe_fp4_project(const moefp4_linear* p, const void* x, const uint8
  *   moe_fp4_grouped_dw  dW_e  = sum over e's rows of dy[r] x[r]^T   [E, N, K]
  * W_e [N, K]: bfloat16 (gran_k 0; w [E, N, K], w_sf and w_gs NULL), or FP4 in
  * the RAW layout above with group16 or group32 scales (and w_gs [E] or NULL):
- * the gradient through frozen experts.  x and dy bfloat16, FP32 accumulation,
+ * the gradient through frozen experts (a code times its scale is taken as a
+ * bfloat16: exact below 2^128, as all are with UE8M0 bytes up to 252, and an
+ * infinity from there on).  x and dy bfloat16, FP32 accumulation,
  * outputs bfloat16 or float32 (out_fmt, moefp4_out_fmt).  dw is written whole,
  * zeros for an expert without rows; with accumulate != 0 the sums are added to
  * what it holds (an expert without rows is left as it is). */
