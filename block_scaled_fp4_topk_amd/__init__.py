@@ -25,6 +25,10 @@ Functions mirror the C entry points:
   prepare_gemm_weights_g16(src, src_sf, src_gs, ...) -> moe_fp4_prepare_gemm_weights_g16
   quantize_act(x, ...)                -> moe_fp4_quantize_act
   quantize_act_fp4(x, ...)            -> moe_fp4_quantize_act_fp4
+
+None of them records a graph for autograd: results need no gradient, whatever
+the arguments do; gradients are calls of their own (grouped_dx, grouped_dw,
+block_norm_grad).
 """
 
 from __future__ import annotations
@@ -647,7 +651,12 @@ def grouped(x, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, workspac
     FP4 codes with w_sf [E, N, K/gran_k] uint8 (and w_gs [E] float32) and gran_k 16
     or 32 (a code times its scale is taken as a bfloat16: exact below 2^128, an
     infinity from there on).  Returns out [M, N] bfloat16 (default) or float32; rows outside
-    [offsets[0], offsets[E]) are left as they are."""
+    [offsets[0], offsets[E]) are left as they are (not set, in an out that the call
+    allocates).
+
+    No call of this module records a graph for autograd: its results need no gradient,
+    whatever its arguments do.  The gradients are calls of their own (grouped_dx,
+    grouped_dw, block_norm_grad), for a torch.autograd.Function's backward."""
     return _grouped_product("moe_fp4_grouped", 0, "x", x, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)
 
@@ -656,7 +665,7 @@ def grouped_dx(dy, w, offsets, w_sf=None, w_gs=None, gran_k=None, out=None, work
                out_dtype=None):
     """The gradient of grouped() towards its rows: out[r] = W_e^T dy[r], dy [M, N]
     bfloat16, the weights and offsets as grouped() takes them.  Returns out
-    [M, K]."""
+    [M, K]; rows outside [offsets[0], offsets[E]) as there."""
     return _grouped_product("moe_fp4_grouped_dx", 1, "dy", dy, w, offsets, w_sf, w_gs, gran_k, out, workspace, stream,
                             out_dtype)
 
@@ -741,7 +750,8 @@ def block_norm(h, y=None, post_w=None, gate=None, gate_act=None, scale=1.0, h_sc
     scale, h_scale and eps are numbers; of a tensor with one element the value at the
     call is taken, on the host (one on the device is waited for, and cannot be taken
     while a graph is captured).  h_out may be h (in place).  Returns (h', n): h' of h's
-    type, n [T, H] bfloat16.  Without y h' is h itself; without pre_w n is None."""
+    type, n [T, H] bfloat16.  Without y h' is h itself; without pre_w n is None.  Nothing is
+    recorded for autograd: the gradient is block_norm_grad()."""
     import torch
     shape, _, problem, dev, at = _norm_args(h, "h", y, post_w, gate, gate_act, pre_w, scale, h_scale, eps, stream)
     if y is None and h_out is not None:
