@@ -1006,7 +1006,14 @@ static long long most_parts(int form, long long M, long long E, long long N, lon
 }
 
 // Which kernel and tile, by the rows per expert with rows (M / most) and by how many
-// tiles there are for the 256 CUs.  N = 4096, K = 6144 unless said:
+// tiles there are for the 256 CUs.  N = 4096, K = 6144 unless said; with smaller weights
+// the borders move (1111 rows of 40 experts, 1000 x 696: 19.8 us in tiles of 128, as
+// chosen, 17.3 of 64).  The host does not know the offsets: rows are taken to be spread
+// over the experts within a factor of a few.  The stream of the weights reads an
+// expert's matrix once per 16 or 32 of its rows, and is the slower the more of all rows
+// one expert has (384 rows of 64 experts: 587 us spread evenly, 712 with three quarters
+// in one; with all in one 217 us, where a call with that expert alone takes 41; 3000 rows
+// of 512 experts, 2048 x 2048: 1065, 1168; 601 and 36).
 // - the stream of the weights.  bfloat16, 64 experts: up to 6 rows with 16 rows of x
 //   per workgroup (380 rows 465 us, with 32 463; 500 rows 496 and 485), up to 12 with 32
 //   (750 rows 520 us, tiles of 64 564; 1000 rows 574 and 565).  FP4, 32 group16 experts:
